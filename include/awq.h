@@ -18,7 +18,9 @@
  * codes (awq_lowbit_*), the mixed-precision ablation that motivates the
  * method (awq_salient_keep_loss), GPTQ error feedback after the scaling
  * (awq_gptq_*) and SmoothQuant W8A8 (awq_smooth_scales,
- * awq_quantize_rows_int8, awq_w8a8_loss).
+ * awq_quantize_rows_int8, awq_w8a8_loss), and what stands between the low-bit
+ * projections of an attention layer: rotary positions (awq_rope*) and a paged
+ * key/value cache in 8 bits with the attention over it (awq_kv_*).
  *
  * Sources (web pages on the method):
  *   [P1] "Как работает quantization-aware scaling в AWQ для защиты важных
@@ -29,8 +31,8 @@
  *   [P4] "GPTQ与AWQ" (study notes), sections "AWQ实现要点" and GPTQ
  *
  * Conventions shared by every entry point
- *   - Every tensor is a dense row-major buffer in device memory, allocated and
- *     owned by the caller; the library allocates no device memory.  Host
+ *   - Every tensor is a dense row-major buffer in device memory (but for the
+ *     strided ones of awq_rope and awq_kv_*), allocated and owned by the caller; the library allocates no device memory.  Host
  *     buffers are named as such below.
  *   - Work is enqueued asynchronously on `stream` (NULL = the null stream);
  *     outputs are valid once the stream has been synchronised.  Calls that
@@ -46,7 +48,7 @@
  *   - W and X share one dtype.  fp16/bf16 layers use the MFMA path (fp32
  *     accumulation); fp32 layers use an fp32 vector-ALU path.
  *   - Sizes: every operand buffer must be below 4 GiB (byte offsets are
- *     32-bit inside the kernels); bits in [2, 8]; group a power of two in
+ *     32-bit inside the kernels; not so in awq_rope and awq_kv_*); bits in [2, 8]; group a power of two in
  *     [32, 512] dividing K.
  */
 #ifndef AWQ_MI355X_AWQ_H
@@ -445,6 +447,139 @@ awq_status_t awq_w8a8_loss(const void* W, const void* X, awq_dtype_t dtype, int6
                            void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Between the low-bit projections: rotary positions, and attention over a
+ * paged key/value cache held in 8 bits.
+ *
+ * The tensors of this section take strides (in elements) where they say so;
+ * a head's D columns are always contiguous.
+ *
+ * awq_rope_table: table [n_pos][rot/2][2] fp32 = (cos, sin) of p f_i times
+ *   magnitude, formed in fp64, for positions p < n_pos and pairs i < rot/2:
+ *     f_i = base^(-2i/rot), slowed for longer contexts as scaling says (NULL:
+ *     as AWQ_ROPE_SCALING_NONE, magnitude 1).
+ *   LINEAR: f_i / factor.  TURNS, LOG_TURNS: by the turns n_i = original f_i /
+ *   (2 pi) that a pair makes over `original` positions, w = clamp((n_i - low) /
+ *   (high - low), 0, 1), or the same on log n_i; w f_i + (1 - w) f_i / factor.
+ *   rot even, >= 2; base, factor > 0; 0 < low < high and original > 0 for the
+ *   last two.
+ *
+ * awq_rope: out = x with the first rot columns of every head turned by the
+ *   position of its row: pair i is columns (i, i + rot/2), or (2i, 2i + 1) with
+ *   AWQ_ROPE_INTERLEAVED; c, s = table[position][i];
+ *     y1 = x1 c - x2 s,  y2 = x2 c + x1 s   (fp32, every product and sum rounded)
+ *   and AWQ_ROPE_TRANSPOSE takes -s for s: the gradient with respect to x.
+ *   Columns from rot on are copied.  x [B, S, H, D] of x_dtype with strides
+ *   x_strides[3] over B, S and H, out likewise of out_dtype; out may be x (with
+ *   the same dtype and strides), otherwise they must not overlap.  positions
+ *   int32, row (b, s) at b * position_stride + s (stride 0: shared), or NULL: s.
+ *   A position outside [0, n_pos) turns its row to NaN.  rot <= D <= 65536.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  AWQ_ROPE_SCALING_NONE = 0,
+  AWQ_ROPE_SCALING_LINEAR = 1,
+  AWQ_ROPE_SCALING_TURNS = 2,
+  AWQ_ROPE_SCALING_LOG_TURNS = 3,
+  AWQ_ROPE_SCALING_MAX_ENUM = 0x7fffffff
+} awq_rope_scaling_kind_t;
+typedef struct {
+  awq_rope_scaling_kind_t kind;
+  double factor;               /* how many times slower the slow pairs turn */
+  double original, low, high;  /* TURNS and LOG_TURNS */
+  double magnitude;            /* multiplies cos and sin */
+} awq_rope_scaling_t;
+#define AWQ_ROPE_INTERLEAVED 1u
+#define AWQ_ROPE_TRANSPOSE 2u
+awq_status_t awq_rope_table(int64_t n_pos, int rot, double base, const awq_rope_scaling_t* scaling,
+                            float* table, hipStream_t stream);
+awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, int64_t H,
+                      int64_t D, const int64_t* x_strides, const int32_t* positions,
+                      int64_t position_stride, const float* table, int64_t n_pos, int rot,
+                      uint32_t flags, void* out, awq_dtype_t out_dtype,
+                      const int64_t* out_strides, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * The cache.  A page holds `page` consecutive tokens of one sequence, all
+ * kv_heads heads: k_codes [n_pages][kv_heads][page][head_dim] and v_codes
+ * [n_pages][kv_heads][head_dim][page] uint8 (a value's tokens lie next to each
+ * other), each code u = c + 128 with c in [-127, 127]; k_steps and v_steps
+ * [n_pages][kv_heads] fp32, a block's value being c * step.  head_dim a
+ * multiple of 8 in [8, 256]; page 16, 32, 64, 128 or 256; codes 16-byte aligned.
+ * The arrays may pass 4 GiB.  The struct is read by the call only; it and the
+ * strides are host memory.
+ *
+ * pages [B][max_pages] int32 (device): the page of tokens [p page, (p + 1)
+ * page) of sequence b.  An entry outside [0, n_pages) is a page that is not
+ * there (one that a window has left behind, say): its tokens are not kept, not
+ * seen, and read as zero.  Two sequences may share pages that are only read.
+ * starts [B + 1] int32 (device): sequence b has rows [starts[b], starts[b + 1])
+ * of a call's T rows; NULL: row b is sequence b's, one each (decoding).
+ * lens [B] int32 (device): tokens of a sequence, a call's new ones among them,
+ * so row r of sequence b is its token lens[b] - (starts[b + 1] - r).
+ * max_new, max_len (host): at least the largest number of rows and length of a
+ * sequence; grids are sized by them.  Rows beyond max_new are not processed,
+ * tokens beyond max_len not attended to.
+ *
+ * awq_kv_append: puts rows k and v [T, kv_heads, D] of dtype (strides over
+ *   rows and heads: kv_strides[0..1] of k, [2..3] of v) into the cache.  With a
+ *   table (else NULL, rot 0) k is first turned as awq_rope does (flags:
+ *   AWQ_ROPE_INTERLEAVED), at positions[r] (int32) or, NULL, at its token's
+ *   number.  For each block that gets tokens, in fp32 and in this order:
+ *     step' = max(step, max |new| / 127), step = 0 if the page held no tokens
+ *     older c' = clamp(rint(c * (step / step')), -127, 127) if step' != step
+ *     new c = clamp(rint(x / step'), -127, 127), 0 where x / step' is NaN
+ *   (rint: ties to even).  A NaN or an infinity makes the step that, and what
+ *   the block holds reads as NaN: nothing plausible comes of it.  Tokens
+ *   with a negative number are dropped.  Pages that get tokens must differ
+ *   between sequences.  q (may be NULL, then Hq 0) [T, Hq, D] of dtype, Hq a
+ *   multiple of kv_heads, strides q_strides[2]: turned alike into q_out [T, Hq,
+ *   D] dense of q_out_dtype, by the same launch.
+ * awq_kv_read: tokens first[b] (device int32) and on, one for each row of the
+ *   sequence, back as values: k_out and v_out [T, kv_heads, D] dense of out_dtype =
+ *   fp32(c * step) rounded once.
+ * awq_kv_attention: for row r = token i of sequence b and query head h, over
+ *   the tokens j < lens[b] with j <= i (unless AWQ_ATT_FULL) and, window > 0, j >
+ *   i - window, whose page is there, of kv head h / (Hq / kv_heads):
+ *     out[r, h] = sum_j p_j v_j,  p = softmax(scale q[r, h] . k_j)
+ *     lse[r, h] = log sum_j exp(scale q[r, h] . k_j)   (fp32; lse may be NULL)
+ *   q [T, Hq, D] of dtype (AWQ_F16 or AWQ_BF16; strides q_strides[2]), out [T,
+ *   Hq, D] dense of dtype.  A row that sees no token gives 0 and -inf.  Scores,
+ *   sums and outputs are held in fp32; probabilities are rounded to fp16
+ *   before they weigh the values.  scale finite and >= 0.  Results are
+ *   reproducible.  workspace: awq_kv_attention_workspace_size(T, B, Hq,
+ *   kv_heads, D, max_new, max_len) bytes, 256-byte aligned, may be NULL when that is 0.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_steps;
+  float* v_steps;
+  int64_t n_pages;
+  int32_t kv_heads, head_dim, page;
+} awq_kv_cache_t;
+#define AWQ_ATT_FULL 1u
+awq_status_t awq_kv_append(const awq_kv_cache_t* cache, const void* k, const void* v,
+                           awq_dtype_t dtype, int64_t T, const int64_t* kv_strides,
+                           const int32_t* starts, const int32_t* lens, int64_t B,
+                           const int32_t* pages, int64_t max_pages, int64_t max_new,
+                           const float* table, int64_t n_pos, int rot, uint32_t flags,
+                           const int32_t* positions, const void* q, int64_t Hq,
+                           const int64_t* q_strides, void* q_out, awq_dtype_t q_out_dtype,
+                           hipStream_t stream);
+awq_status_t awq_kv_read(const awq_kv_cache_t* cache, int64_t T, const int32_t* starts,
+                         const int32_t* first, int64_t B, const int32_t* pages, int64_t max_pages,
+                         int64_t max_new, void* k_out, void* v_out, awq_dtype_t out_dtype,
+                         hipStream_t stream);
+size_t awq_kv_attention_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t kv_heads,
+                                       int64_t D, int64_t max_new, int64_t max_len);
+awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dtype_t dtype,
+                              int64_t T, int64_t Hq, const int64_t* q_strides,
+                              const int32_t* starts, const int32_t* lens, int64_t B,
+                              const int32_t* pages, int64_t max_pages, int64_t max_new,
+                              int64_t max_len, double scale, int64_t window, uint32_t flags,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Kernel timing.  While enabled, every kernel the library launches (or, after
  * awq_profile_select(prefix), every kernel whose name starts with prefix) is
  * bracketed by a pair of HIP events on its stream; each event pair adds a few
@@ -458,7 +593,8 @@ awq_status_t awq_w8a8_loss(const void* W, const void* X, awq_dtype_t dtype, int6
  * launches of each: awq_gptq_hessian, awq_gptq_prep, awq_gptq_cholesky,
  * awq_gptq_inverse, awq_gptq_columns, awq_gptq_pack.  SmoothQuant: awq_smooth_scales,
  * awq_quant_rows_int8, awq_gemm_w8a8_sse (the INT8 GEMM with the squared-error
- * epilogue), awq_gemm_w8a8_store (the INT8 GEMM writing y).
+ * epilogue), awq_gemm_w8a8_store (the INT8 GEMM writing y).  awq_rope_table, awq_rope,
+ * awq_kv_append, awq_kv_read, awq_kv_attention, awq_kv_attention_join.
  * awq_profile_reset() drops the records.  Thread-safe.
  * ------------------------------------------------------------------------ */
 awq_status_t awq_profile_enable(int enable);

@@ -28,6 +28,9 @@ __all__ = [
     "awq_gptq_workspace_size",
     "awq_gptq_factor_ld", "awq_gptq_quantize", "awq_smooth_scales", "awq_quantize_rows_int8",
     "awq_w8a8_workspace_size", "awq_w8a8_loss",
+    "AWQ_ROPE_INTERLEAVED", "AWQ_ROPE_TRANSPOSE", "AWQ_ATT_FULL", "KvCache",
+    "awq_rope_table", "awq_rope", "awq_kv_append", "awq_kv_read",
+    "awq_kv_attention_workspace_size", "awq_kv_attention",
     "awq_profile_enable", "awq_profile_select", "awq_profile_read", "awq_profile_reset",
     "packed_words_per_row",
 ]
@@ -38,6 +41,11 @@ AWQ_SEARCH_REFERENCE_OUTPUT = 1
 AWQ_FQ_WEIGHT_HAT = 0
 AWQ_FQ_WEIGHT_DELTA = 1
 AWQ_LOWBIT_STATIC_SCRATCH_BYTES = 32 << 20
+
+AWQ_ROPE_INTERLEAVED = 1
+AWQ_ROPE_TRANSPOSE = 2
+AWQ_ATT_FULL = 1
+_ROPE_SCALING = {"none": 0, "linear": 1, "turns": 2, "log_turns": 3}
 
 _DTYPES = {torch.float32: AWQ_F32, torch.float16: AWQ_F16, torch.bfloat16: AWQ_BF16}
 _STATUS = {0: "AWQ_OK", -1: "AWQ_ERR_INVALID_ARG", -2: "AWQ_ERR_UNSUPPORTED",
@@ -67,6 +75,30 @@ class SearchLayout(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int),
+        ("factor", ctypes.c_double),
+        ("original", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("magnitude", ctypes.c_double),
+    ]
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("k_steps", ctypes.c_void_p),
+        ("v_steps", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+    ]
 
 
 def library_path() -> Path:
@@ -106,6 +138,15 @@ _SIGS = {
     "awq_quantize_rows_int8": ([_P, _I32, _I64, _I64, _P, _I32, _P, _P, _P], _I32),
     "awq_w8a8_workspace_size": ([_I64, _I64, _I64], _SZ),
     "awq_w8a8_loss": ([_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P], _I32),
+    "awq_rope_table": ([_I64, _I32, _D, ctypes.POINTER(RopeScaling), _P, _P], _I32),
+    "awq_rope": ([_P, _I32, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _I32, _U32, _P, _I32,
+                  _P, _P], _I32),
+    "awq_kv_append": ([_P, _P, _P, _I32, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _P, _I64, _I32,
+                       _U32, _P, _P, _I64, _P, _P, _I32, _P], _I32),
+    "awq_kv_read": ([_P, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
+    "awq_kv_attention_workspace_size": ([_I64] * 7, _SZ),
+    "awq_kv_attention": ([_P, _P, _I32, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _D,
+                          _I64, _U32, _P, _P, _P, _SZ, _P], _I32),
     "awq_profile_enable": ([_I32], _I32),
     "awq_profile_select": ([ctypes.c_char_p], _I32),
     "awq_profile_read": ([ctypes.c_char_p, ctypes.POINTER(_I64), ctypes.POINTER(_D)], _I32),
@@ -466,6 +507,245 @@ def awq_lowbit_gemm(Xs: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tenso
                                      meta_t.data_ptr(), N, bits, group, out.data_ptr(),
                                      _stream(Xs.device)))
     return out
+
+
+def _heads(t: torch.Tensor, name: str, dims: int = 3) -> torch.Tensor:
+    """A GPU tensor [rows, heads, D] (or [B, S, H, D]) whose heads' columns lie together."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t
+
+
+def _ints(t: torch.Tensor, name: str, *shape: int) -> int:
+    _dev(t, name)
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _same_device(like, /, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def awq_rope_table(n_pos: int, rot: int, base: float = 10000.0, scaling: str = "none",
+                   factor: float = 1.0, original: float = 0.0, low: float = 1.0,
+                   high: float = 4.0, magnitude: float = 1.0, device="cuda") -> torch.Tensor:
+    """cos and sin of positions 0 .. n_pos - 1, fp32 [n_pos, rot/2, 2] (formed in fp64).
+    scaling: "none", "linear", "turns" or "log_turns" (see the header)."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
+    sc = RopeScaling(_ROPE_SCALING[scaling], factor, original, low, high, magnitude)
+    table = torch.empty((max(n_pos, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device=device)
+    _dev(table, "table")
+    with torch.cuda.device(table.device):
+        _check(library().awq_rope_table(n_pos, rot, base, ctypes.byref(sc), table.data_ptr(),
+                                        _stream(table.device)))
+    return table
+
+
+def _table(table: torch.Tensor):
+    _dev(table, "table")
+    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32:
+        raise ValueError("table must be fp32 [positions, rot/2, 2] (awq_rope_table)")
+    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+
+
+def awq_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor | None = None,
+             interleaved: bool = False, transpose: bool = False, out: torch.Tensor | None = None,
+             out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """x [T, H, D] or [B, S, H, D] (any strides, the last dimension contiguous) with each
+    head's first 2 * table.shape[1] columns turned by the row's position; transpose=True gives the
+    gradient with respect to x.  positions int32 [T], [S] or [B, S]; None: the row's index.
+    out may be x."""
+    x4 = _heads(x, "x", x.dim() if isinstance(x, torch.Tensor) and x.dim() == 4 else 3)
+    x4 = x4 if x4.dim() == 4 else x4.unsqueeze(0)
+    tp, n_pos, rot = _table(table)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must have x's shape and out_dtype")
+    o4 = _heads(out, "out", x.dim())
+    o4 = o4 if o4.dim() == 4 else o4.unsqueeze(0)
+    B, S, H, D = x4.shape
+    pp, ps = None, 0
+    if positions is not None:
+        shape = (B, S) if positions.dim() == 2 else (S,)
+        pp, ps = _ints(positions, "positions", *shape), S if positions.dim() == 2 else 0
+    _same_device(x, table=table, positions=positions, out=out)
+    xs, os_ = (_I64 * 3)(*x4.stride()[:3]), (_I64 * 3)(*o4.stride()[:3])
+    with torch.cuda.device(x.device):
+        _check(library().awq_rope(x.data_ptr(), _dtype(x), B, S, H, D, xs, pp, ps, tp, n_pos, rot,
+                                  (AWQ_ROPE_INTERLEAVED if interleaved else 0)
+                                  | (AWQ_ROPE_TRANSPOSE if transpose else 0), out.data_ptr(),
+                                  _dtype(out), os_, _stream(x.device)))
+    return out
+
+
+class KvCache:
+    """A paged key/value cache in 8 bits: k_codes uint8 [n_pages, kv_heads, page, D],
+    v_codes uint8 [n_pages, kv_heads, D, page], k_steps and v_steps fp32 [n_pages, kv_heads].
+    Holds the tensors; which page is whose is the caller's (page tables)."""
+
+    def __init__(self, k_codes, v_codes, k_steps, v_steps):
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes"), (k_steps, "k_steps"),
+                        (v_steps, "v_steps")):
+            _dev(t, name)
+            _same_device(k_codes, **{name: t})
+        if k_codes.dim() != 4 or k_codes.dtype != torch.uint8:
+            raise ValueError("k_codes must be uint8 [n_pages, kv_heads, page, D]")
+        n, h, p, d = k_codes.shape
+        if tuple(v_codes.shape) != (n, h, d, p) or v_codes.dtype != torch.uint8:
+            raise ValueError(f"v_codes must be uint8 {[n, h, d, p]}")
+        for t, name in ((k_steps, "k_steps"), (v_steps, "v_steps")):
+            if tuple(t.shape) != (n, h) or t.dtype != torch.float32:
+                raise ValueError(f"{name} must be fp32 {[n, h]}")
+        self.k_codes, self.v_codes, self.k_steps, self.v_steps = k_codes, v_codes, k_steps, v_steps
+        self.n_pages, self.kv_heads, self.page, self.head_dim = n, h, p, d
+        self.device = k_codes.device
+        self._struct = KvCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_steps.data_ptr(),
+                                     v_steps.data_ptr(), n, h, d, p)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, page: int, head_dim: int, device="cuda"):
+        return cls(torch.empty((n_pages, kv_heads, page, head_dim), dtype=torch.uint8, device=device),
+                   torch.empty((n_pages, kv_heads, head_dim, page), dtype=torch.uint8, device=device),
+                   torch.empty((n_pages, kv_heads), dtype=torch.float32, device=device),
+                   torch.empty((n_pages, kv_heads), dtype=torch.float32, device=device))
+
+
+def _paged(cache: KvCache, pages, starts, **per_sequence):
+    """(B, pointers of pages and starts and of each int32 [B] tensor, pages of a sequence)."""
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache")
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
+        raise ValueError("pages must be an int32 tensor [sequences, pages]")
+    B = pages.shape[0]
+    ptrs = [_ints(pages, "pages", B, pages.shape[1]),
+            None if starts is None else _ints(starts, "starts", B + 1)]
+    ptrs += [_ints(t, name, B) for name, t in per_sequence.items()]
+    _same_device(cache, pages=pages, starts=starts, **per_sequence)
+    return B, ptrs
+
+
+def awq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,
+                  pages: torch.Tensor, starts: torch.Tensor | None = None,
+                  max_new: int | None = None, table: torch.Tensor | None = None,
+                  interleaved: bool = False, positions: torch.Tensor | None = None,
+                  q: torch.Tensor | None = None, q_dtype: torch.dtype | None = None,
+                  q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Rows k and v [T, kv_heads, D] into the cache, k turned by the table on the way; q
+    [T, Hq, D], if given, is turned alike and returned (dense, of q_dtype).  lens int32 [B] counts
+    the new rows too; starts None: one row for each sequence; max_new: the most rows of a
+    sequence (None: 1 without starts, T with)."""
+    B, (pp, sp, lp) = _paged(cache, pages, starts, lens=lens)
+    _heads(k, "k")
+    _heads(v, "v")
+    T = k.shape[0]
+    if tuple(k.shape) != (T, cache.kv_heads, cache.head_dim) or v.shape != k.shape \
+            or v.dtype != k.dtype:
+        raise ValueError(f"k and v must be [T, {cache.kv_heads}, {cache.head_dim}] of one dtype")
+    tp, n_pos, rot = (None, 0, 0) if table is None else _table(table)
+    qp, op, Hq, qs, odt = None, None, 0, None, AWQ_F32
+    if q is not None:
+        _heads(q, "q")
+        Hq = q.shape[1]
+        if tuple(q.shape) != (T, Hq, cache.head_dim) or q.dtype != k.dtype:
+            raise ValueError(f"q must be [T, Hq, {cache.head_dim}] of k's dtype")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
+        elif q_out.shape != q.shape or (q_dtype is not None and q_out.dtype != q_dtype):
+            raise ValueError("q_out must have q's shape and q_dtype")
+        qp, op, odt = q.data_ptr(), _dev(q_out, "q_out").data_ptr(), _dtype(q_out)
+        qs = (_I64 * 2)(q.stride(0), q.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(cache, k=k, v=v, table=table, positions=positions, q=q, q_out=q_out)
+    strides = (_I64 * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    if max_new is None:
+        max_new = 1 if starts is None else T
+    with torch.cuda.device(cache.device):
+        _check(library().awq_kv_append(
+            cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k), T, strides, sp, lp, B, pp,
+            pages.shape[1], max_new, tp, n_pos, rot, AWQ_ROPE_INTERLEAVED if interleaved else 0,
+            None if positions is None else _ints(positions, "positions", T), qp, Hq, qs, op, odt,
+            _stream(cache.device)))
+    return q_out
+
+
+def awq_kv_read(cache: KvCache, first: torch.Tensor, pages: torch.Tensor,
+                starts: torch.Tensor | None = None, total: int | None = None,
+                max_count: int | None = None, dtype: torch.dtype = torch.float32):
+    """Tokens first[b] and on of every sequence as values -> (k, v) [total, kv_heads, D];
+    starts int32 [B + 1] places each sequence's rows (None: one token each), total =
+    starts[B] on the host, max_count the most tokens of a sequence (None: total)."""
+    B, (pp, sp, fp) = _paged(cache, pages, starts, first=first)
+    if total is None:
+        if starts is not None:
+            raise ValueError("total (starts[B], on the host) is needed with starts")
+        total = B
+    if max_count is None:
+        max_count = 1 if starts is None else total
+    k = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
+    with torch.cuda.device(cache.device):
+        _check(library().awq_kv_read(cache._ref, total, sp, fp, B, pp, pages.shape[1], max_count,
+                                     k.data_ptr(), v.data_ptr(), _dtype(k),
+                                     _stream(cache.device)))
+    return k, v
+
+
+def awq_kv_attention_workspace_size(T: int, B: int, Hq: int, kv_heads: int, D: int, max_new: int,
+                                    max_len: int) -> int:
+    return int(library().awq_kv_attention_workspace_size(T, B, Hq, kv_heads, D, max_new, max_len))
+
+
+def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor,
+                     starts: torch.Tensor | None = None, max_new: int | None = None,
+                     max_len: int | None = None, scale: float | None = None, window: int = 0,
+                     causal: bool = True, out: torch.Tensor | None = None,
+                     return_lse: bool = False, workspace: torch.Tensor | None = None):
+    """Attention of q [T, Hq, D] (fp16 or bf16) over the cache -> out [T, Hq, D] and, on
+    request, the logarithm of each row's sum, fp32 [T, Hq].  lens int32 [B]: tokens of each
+    sequence, the queries' own among them; max_new as in awq_kv_append; max_len: at least the
+    longest length (None: what the page table can hold); scale None: D ** -0.5."""
+    B, (pp, sp, lp) = _paged(cache, pages, starts, lens=lens)
+    _heads(q, "q")
+    T, Hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q must be [T, Hq, {cache.head_dim}]")
+    most = pages.shape[1] * cache.page
+    max_len = most if max_len is None else min(max_len, most)
+    if max_new is None:
+        max_new = 1 if starts is None else T
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        need = awq_kv_attention_workspace_size(T, B, Hq, cache.kv_heads, D, max_new, max_len)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _same_device(cache, q=q, out=out, workspace=workspace)
+    qs = (_I64 * 2)(q.stride(0), q.stride(1))
+    with torch.cuda.device(cache.device):
+        _check(library().awq_kv_attention(
+            cache._ref, q.data_ptr(), _dtype(q), T, Hq, qs, sp, lp, B, pp, pages.shape[1], max_new,
+            max_len, scale, window, 0 if causal else AWQ_ATT_FULL, _dev(out, "out").data_ptr(),
+            None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _stream(cache.device)))
+    return (out, lse) if return_lse else out
 
 
 def awq_profile_enable(enable: bool = True) -> None:

@@ -32,11 +32,15 @@ PER_FILE = {
     # Same quantiser rules; the fp64 updates ask for their FMAs explicitly.
     "gptq.hip": ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
                  "-fno-gpu-flush-denormals-to-zero"],
+    # Codes of rotated keys agree bit for bit with any IEEE evaluation; NaNs are kept.
+    "rope.hip": ["-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero"],
+    "kvcache.hip": ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
+                    "-fno-gpu-flush-denormals-to-zero"],
     "w8a8.hip": ["-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
                  "-fno-gpu-flush-denormals-to-zero"],
 }
 SOURCES = ["act_stats.hip", "quant.hip", "gemm_sse.hip", "lowbit.hip", "gptq.hip", "w8a8.hip",
-           "awq_api.cpp"]
+           "rope.hip", "kvcache.hip", "attention.hip", "awq_api.cpp"]
 
 
 def hipcc() -> str:

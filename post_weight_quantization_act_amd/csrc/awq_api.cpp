@@ -1,7 +1,7 @@
 // C ABI of the AWQ scale-search library: argument validation, workspace
 // layout, the order of launches on the caller's stream, error reporting and
 // optional per-launch timing.  All arithmetic runs in the HIP kernels of
-// act_stats.hip, quant.hip and gemm_sse.hip.
+// the .hip files.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -14,7 +14,7 @@
 #include <string>
 #include <vector>
 
-#include "common.h"
+#include "kv.h"
 
 namespace {
 
@@ -40,6 +40,8 @@ constexpr int kLaunchRounds = 4;      // candidate-GEMM rounds of the persistent
 constexpr int64_t kGptqMaxK = 32768;   // the fp64 factor matrix is K^2 * 8 bytes
 constexpr int64_t kLowbitGemmMaxM = 65535ll * 128;  // activation-row tiles on grid y
 constexpr int64_t kLowbitGemmMaxK = 1ll << 22;       // a 256-row activation tile in 32-bit offsets
+constexpr int64_t kMaxGrid = INT32_MAX;               // workgroups of a launch
+constexpr int kMaxHeads = 16384;
 
 int esize(awq_dtype_t dt) { return dt == AWQ_F32 ? 4 : 2; }
 
@@ -158,6 +160,61 @@ awq_status_t keep_layout(awq_dtype_t dt, int64_t N, int64_t K, int64_t T, KeepLa
   L->s_copy_offset = off;
   off = align_up(off + (size_t)K * 4);
   L->total_bytes = off;
+  return AWQ_OK;
+}
+
+// Checks shared by the cache's entry points, and their kernels' common arguments.
+awq_status_t kv_args(const awq_kv_cache_t* cache, int64_t T, const int32_t* starts, int64_t B,
+                     const int32_t* pages, int64_t max_pages, int64_t max_new, awq::KvArgs* a) {
+  if (!cache) return fail(AWQ_ERR_INVALID_ARG, "null cache");
+  if (cache->kv_heads < 1 || cache->n_pages < 1)
+    return fail(AWQ_ERR_INVALID_ARG, "kv_heads=%d and n_pages=%lld must be >= 1", cache->kv_heads,
+                (long long)cache->n_pages);
+  if (cache->head_dim < 8 || cache->head_dim > 256 || cache->head_dim % 8 != 0)
+    return fail(AWQ_ERR_UNSUPPORTED, "head_dim=%d must be a multiple of 8 in [8, 256]",
+                cache->head_dim);
+  if (cache->page < 16 || cache->page > 256 || (cache->page & (cache->page - 1)) != 0)
+    return fail(AWQ_ERR_UNSUPPORTED, "page=%d must be 16, 32, 64, 128 or 256", cache->page);
+  if (cache->kv_heads > kMaxHeads || cache->n_pages > INT32_MAX)
+    return fail(AWQ_ERR_UNSUPPORTED, "kv_heads=%d or n_pages=%lld too large", cache->kv_heads,
+                (long long)cache->n_pages);
+  if (!cache->k_codes || !cache->v_codes || !cache->k_steps || !cache->v_steps)
+    return fail(AWQ_ERR_INVALID_ARG, "null pointer in the cache");
+  if (!aligned(cache->k_codes, 16) || !aligned(cache->v_codes, 16) ||
+      !aligned(cache->k_steps, 4) || !aligned(cache->v_steps, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "the cache's codes must be 16-byte aligned");
+  if (T < 0 || B < 0 || max_pages < 0 || max_new < 0)
+    return fail(AWQ_ERR_INVALID_ARG, "negative size");
+  if (T > INT32_MAX || max_pages > INT32_MAX || max_new > INT32_MAX / 2)
+    return fail(AWQ_ERR_UNSUPPORTED, "T, max_pages and max_new must fit 31 bits");
+  if (!starts && B != T)
+    return fail(AWQ_ERR_INVALID_ARG, "without starts every sequence has one row: T=%lld, B=%lld",
+                (long long)T, (long long)B);
+  if (T > 0 && B > 0) {
+    if (max_new < 1 || max_pages < 1)
+      return fail(AWQ_ERR_INVALID_ARG, "max_new and max_pages must be >= 1");
+    if (!pages) return fail(AWQ_ERR_INVALID_ARG, "null pages");
+    if (!aligned(pages, 4) || !aligned(starts, 4))
+      return fail(AWQ_ERR_UNSUPPORTED, "pages and starts must be 4-byte aligned");
+    const int64_t pps = (max_new + cache->page - 2) / cache->page + 1;
+    if (B > kMaxGrid / (pps * cache->kv_heads))
+      return fail(AWQ_ERR_UNSUPPORTED, "too many sequences, heads and pages for one launch");
+  }
+  a->k_codes = cache->k_codes;
+  a->v_codes = cache->v_codes;
+  a->k_steps = cache->k_steps;
+  a->v_steps = cache->v_steps;
+  a->pages = pages;
+  a->starts = starts;
+  a->n_pages = cache->n_pages;
+  a->T = T;
+  a->B = (int)B;
+  a->max_pages = (int)max_pages;
+  a->Hkv = cache->kv_heads;
+  a->D = cache->head_dim;
+  a->P = cache->page;
+  a->p_shift = 0;
+  while ((1 << a->p_shift) < a->P) ++a->p_shift;
   return AWQ_OK;
 }
 
@@ -752,6 +809,240 @@ awq_status_t awq_quantize_pack(const void* W, awq_dtype_t w_dtype, int64_t N, in
   hipError_t e = awq::launch_quantize_pack(W, w_dtype, N, K, s, bits, group, codes_out, scales_out,
                                            zeros_out, stream);
   if (e != hipSuccess) return hip_fail(e, "quantize_pack launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions and the 8-bit cache.
+// ---------------------------------------------------------------------------
+awq_status_t awq_rope_table(int64_t n_pos, int rot, double base, const awq_rope_scaling_t* scaling,
+                            float* table, hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  if (n_pos < 1 || rot < 2 || rot % 2 != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "n_pos=%lld must be >= 1, rot=%d even and >= 2",
+                (long long)n_pos, rot);
+  if (!table) return fail(AWQ_ERR_INVALID_ARG, "null table");
+  if (!aligned(table, 8)) return fail(AWQ_ERR_UNSUPPORTED, "table must be 8-byte aligned");
+  if (!std::isfinite(base) || base <= 0) return fail(AWQ_ERR_INVALID_ARG, "base must be > 0");
+  if (n_pos > kMaxGrid * 128 / rot)
+    return fail(AWQ_ERR_UNSUPPORTED, "a table of %lld positions is too long", (long long)n_pos);
+  awq::RopeFreqs fr = {};
+  fr.base = base;
+  fr.factor = fr.magnitude = 1.0;
+  fr.kind = AWQ_ROPE_SCALING_NONE;
+  if (scaling) {
+    const int kind = (int)scaling->kind;
+    if (kind < AWQ_ROPE_SCALING_NONE || kind > AWQ_ROPE_SCALING_LOG_TURNS)
+      return fail(AWQ_ERR_INVALID_ARG, "unknown scaling kind %d", kind);
+    if (!std::isfinite(scaling->magnitude))
+      return fail(AWQ_ERR_INVALID_ARG, "magnitude must be finite");
+    if (kind != AWQ_ROPE_SCALING_NONE && !(std::isfinite(scaling->factor) && scaling->factor > 0))
+      return fail(AWQ_ERR_INVALID_ARG, "factor must be > 0");
+    if (kind >= AWQ_ROPE_SCALING_TURNS &&
+        !(std::isfinite(scaling->original) && scaling->original > 0 && scaling->low > 0 &&
+          std::isfinite(scaling->high) && scaling->high > scaling->low))
+      return fail(AWQ_ERR_INVALID_ARG, "original must be > 0 and 0 < low < high");
+    fr.kind = kind;
+    fr.factor = scaling->factor;
+    fr.magnitude = scaling->magnitude;
+    fr.original = scaling->original;
+    fr.low = scaling->low;
+    fr.high = scaling->high;
+  }
+  hipError_t e = awq::launch_rope_table(n_pos, rot, fr, table, stream);
+  if (e != hipSuccess) return hip_fail(e, "rope_table launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, int64_t H,
+                      int64_t D, const int64_t* x_strides, const int32_t* positions,
+                      int64_t position_stride, const float* table, int64_t n_pos, int rot,
+                      uint32_t flags, void* out, awq_dtype_t out_dtype,
+                      const int64_t* out_strides, hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  if (!valid_dtype(x_dtype) || !valid_dtype(out_dtype))
+    return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d or %d", (int)x_dtype, (int)out_dtype);
+  if (B < 0 || S < 0 || H < 0 || D < 1)
+    return fail(AWQ_ERR_INVALID_ARG, "sizes must not be negative, D >= 1");
+  if (flags & ~(AWQ_ROPE_INTERLEAVED | AWQ_ROPE_TRANSPOSE))
+    return fail(AWQ_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (rot < 2 || rot % 2 != 0 || rot > D)
+    return fail(AWQ_ERR_INVALID_ARG, "rot=%d must be even, in [2, D=%lld]", rot, (long long)D);
+  if (n_pos < 1) return fail(AWQ_ERR_INVALID_ARG, "n_pos must be >= 1");
+  if (D > 65536) return fail(AWQ_ERR_UNSUPPORTED, "D=%lld above 65536", (long long)D);
+  if (B > INT32_MAX || S > INT32_MAX || H > INT32_MAX)
+    return fail(AWQ_ERR_UNSUPPORTED, "B, S and H must fit 31 bits");
+  if (B == 0 || S == 0 || H == 0) return AWQ_OK;
+  if (!x || !table || !out || !x_strides || !out_strides)
+    return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, esize(x_dtype)) || !aligned(out, esize(out_dtype)) || !aligned(table, 8) ||
+      !aligned(positions, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned to its elements");
+  if (B * S > kMaxGrid * 256 / (H * D))
+    return fail(AWQ_ERR_UNSUPPORTED, "more than %lld elements", (long long)(kMaxGrid * 256));
+  awq::RopeArgs a = {};
+  a.x = x;
+  a.out = out;
+  a.positions = positions;
+  a.table = table;
+  a.B = B;
+  a.S = S;
+  a.H = H;
+  for (int i = 0; i < 3; ++i) {
+    a.xs[i] = x_strides[i];
+    a.os[i] = out_strides[i];
+  }
+  a.pos_stride = position_stride;
+  a.n_pos = n_pos;
+  a.D = (int)D;
+  a.rot = rot;
+  a.interleaved = (flags & AWQ_ROPE_INTERLEAVED) != 0;
+  a.transpose = (flags & AWQ_ROPE_TRANSPOSE) != 0;
+  hipError_t e = awq::launch_rope(a, x_dtype, out_dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "rope launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_kv_append(const awq_kv_cache_t* cache, const void* k, const void* v,
+                           awq_dtype_t dtype, int64_t T, const int64_t* kv_strides,
+                           const int32_t* starts, const int32_t* lens, int64_t B,
+                           const int32_t* pages, int64_t max_pages, int64_t max_new,
+                           const float* table, int64_t n_pos, int rot, uint32_t flags,
+                           const int32_t* positions, const void* q, int64_t Hq,
+                           const int64_t* q_strides, void* q_out, awq_dtype_t q_out_dtype,
+                           hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq::AppendArgs a = {};
+  awq_status_t st = kv_args(cache, T, starts, B, pages, max_pages, max_new, &a.c);
+  if (st != AWQ_OK) return st;
+  if (!valid_dtype(dtype) || (q && !valid_dtype(q_out_dtype)))
+    return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d or %d", (int)dtype, (int)q_out_dtype);
+  if (flags & ~AWQ_ROPE_INTERLEAVED)
+    return fail(AWQ_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (table && (rot < 2 || rot % 2 != 0 || rot > a.c.D || n_pos < 1))
+    return fail(AWQ_ERR_INVALID_ARG, "rot=%d must be even, in [2, head_dim=%d], n_pos >= 1", rot,
+                a.c.D);
+  if (!table && rot != 0) return fail(AWQ_ERR_INVALID_ARG, "rot=%d without a table", rot);
+  if (q ? (Hq < 1 || Hq % a.c.Hkv != 0 || Hq > kMaxHeads) : Hq != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "Hq=%lld must be a multiple of kv_heads=%d (0 without q)",
+                (long long)Hq, a.c.Hkv);
+  if (T == 0 || B == 0) return AWQ_OK;
+  if (!k || !v || !kv_strides || !lens || (q && (!q_out || !q_strides)))
+    return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(k, esize(dtype)) || !aligned(v, esize(dtype)) || !aligned(q, esize(dtype)) ||
+      !aligned(q_out, 16) || !aligned(table, 8) || !aligned(lens, 4) || !aligned(positions, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned (q_out: to 16 bytes)");
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.q_out = q_out;
+  a.lens = lens;
+  a.positions = positions;
+  a.table = table;
+  for (int i = 0; i < 2; ++i) {
+    a.ks[i] = kv_strides[i];
+    a.vs[i] = kv_strides[2 + i];
+    a.qs[i] = q ? q_strides[i] : 0;
+  }
+  a.n_pos = n_pos;
+  a.rot = rot;
+  a.interleaved = (flags & AWQ_ROPE_INTERLEAVED) != 0;
+  a.Hq = (int)Hq;
+  a.pages_per_seq = (int)((max_new + a.c.P - 2) / a.c.P + 1);
+  hipError_t e = awq::launch_kv_append(a, dtype, q ? q_out_dtype : AWQ_F32, stream);
+  if (e != hipSuccess) return hip_fail(e, "kv_append launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_kv_read(const awq_kv_cache_t* cache, int64_t T, const int32_t* starts,
+                         const int32_t* first, int64_t B, const int32_t* pages, int64_t max_pages,
+                         int64_t max_new, void* k_out, void* v_out, awq_dtype_t out_dtype,
+                         hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq::ReadArgs a = {};
+  awq_status_t st = kv_args(cache, T, starts, B, pages, max_pages, max_new, &a.c);
+  if (st != AWQ_OK) return st;
+  if (!valid_dtype(out_dtype)) return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d", (int)out_dtype);
+  if (T == 0 || B == 0) return AWQ_OK;
+  if (!first || !k_out || !v_out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(first, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(AWQ_ERR_UNSUPPORTED, "k_out and v_out must be 16-byte aligned");
+  a.first = first;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.pages_per_seq = (int)((max_new + a.c.P - 2) / a.c.P + 1);
+  hipError_t e = awq::launch_kv_read(a, out_dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "kv_read launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+size_t awq_kv_attention_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t kv_heads,
+                                       int64_t D, int64_t max_new, int64_t max_len) {
+  if (T < 1 || B < 1 || kv_heads < 1 || Hq < 1 || Hq % kv_heads != 0 || D < 1 || max_new < 1 ||
+      max_len < 1 || T > INT32_MAX || B > INT32_MAX || Hq > kMaxHeads || D > 256 ||
+      max_new > INT32_MAX || max_len > INT32_MAX)
+    return 0;
+  return align_up(awq::kv_attention_ws_bytes(T, B, (int)Hq, (int)kv_heads, (int)D, (int)max_new,
+                                             (int)max_len));
+}
+
+awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dtype_t dtype,
+                              int64_t T, int64_t Hq, const int64_t* q_strides,
+                              const int32_t* starts, const int32_t* lens, int64_t B,
+                              const int32_t* pages, int64_t max_pages, int64_t max_new,
+                              int64_t max_len, double scale, int64_t window, uint32_t flags,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq::AttArgs a = {};
+  awq_status_t st = kv_args(cache, T, starts, B, pages, max_pages, max_new, &a.c);
+  if (st != AWQ_OK) return st;
+  if (!valid_dtype(dtype)) return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if (dtype == AWQ_F32)
+    return fail(AWQ_ERR_UNSUPPORTED, "queries are fp16 or bf16 (awq_kv_append rounds them)");
+  if (Hq < 1 || Hq % a.c.Hkv != 0 || Hq > kMaxHeads)
+    return fail(AWQ_ERR_INVALID_ARG, "Hq=%lld must be a multiple of kv_heads=%d", (long long)Hq,
+                a.c.Hkv);
+  if (!std::isfinite(scale) || !std::isfinite((float)scale) || scale < 0)
+    return fail(AWQ_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (window < 0 || max_len < 0 || max_len > INT32_MAX)
+    return fail(AWQ_ERR_INVALID_ARG, "window=%lld or max_len=%lld", (long long)window,
+                (long long)max_len);
+  if (flags & ~AWQ_ATT_FULL) return fail(AWQ_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (T == 0 || B == 0) return AWQ_OK;
+  if (!q || !q_strides || !lens || !out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q, 2) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned (out: to 16 bytes)");
+  const int64_t reach = std::max<int64_t>(1, std::min<int64_t>(max_len, max_pages * a.c.P));
+  if (awq::kv_attention_blocks(T, B, (int)Hq, a.c.Hkv, a.c.D, (int)max_new, (int)reach) > kMaxGrid)
+    return fail(AWQ_ERR_UNSUPPORTED, "too many rows for one launch");
+  const size_t need = awq_kv_attention_workspace_size(T, B, Hq, a.c.Hkv, a.c.D, max_new, reach);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(AWQ_ERR_WORKSPACE, "kv_attention needs %zu workspace bytes, got %zu", need,
+                  workspace ? workspace_bytes : (size_t)0);
+    if (!aligned(workspace, 256))
+      return fail(AWQ_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  }
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.lens = lens;
+  a.qs[0] = q_strides[0];
+  a.qs[1] = q_strides[1];
+  a.scale = (float)scale;
+  a.Hq = (int)Hq;
+  a.causal = (flags & AWQ_ATT_FULL) == 0;
+  a.window = (int)std::min<int64_t>(window, INT32_MAX);
+  a.max_new = (int)max_new;
+  a.max_len = (int)reach;
+  hipError_t e = awq::launch_kv_attention(a, dtype, workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "kv_attention launch");
   return AWQ_OK;
   AWQ_GUARD_END
 }
