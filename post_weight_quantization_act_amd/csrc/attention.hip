@@ -3,100 +3,511 @@
 //   o = sum_j p_j v_j,  p = softmax_j(scale q . k_j)  over the tokens j that the row sees,
 //   k_j = (u - 128) step of its page and head, v_j likewise.
 // A row that sees nothing gives 0, and -inf for the logarithm of its sum.
+//
+// One pass over the cache.  A wave takes tiles of 64 tokens and tiles of 16 rows
+// (rows: the query heads that share a kv head, token after token) and stays in
+// registers: S^T = K Q^T leaves each lane 16 scores of one row, in the order in
+// which O^T += V^T P^T wants its probabilities, because the rows of the K tiles
+// are taken in the order token(i, m) = 16 (m / 4) + 4 i + m % 4 (tile i of 4, row m
+// of 16): lane 16 g + q then holds tokens 16 g .. 16 g + 15 of row q.  A page holds a
+// multiple of 16 tokens, so those sixteen share one page, one key step and one
+// value step.
+//
+// Codes become fp16 exactly: the byte u under 0x64 reads 1024 + u.  For the
+// scores the surplus, 1152 sum_d q_d, is the accumulators' first value; for the
+// values 1152 is subtracted (a packed fp16 operation, exact).  Queries are scaled
+// by a power of two of their row to |q| < 2 and are exact in fp16 but for bf16
+// elements more than 2^-14 below their row's largest, which keep 24 bits below 1.
+//
+// With t = log2 of (weight times value step), one reference R for each row serves
+// sums and values: p = exp2(t - R) weighs the codes, and the row's sum adds
+// p / step once for sixteen tokens, in fp32.  p is rounded to fp16 for the matrix
+// cores; R follows the largest t so that p stays below 2^15 and above 2^-14 with
+// full precision for everything within 2^-22 of the row's largest contribution.
 #include "kv.h"
 
 namespace awq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr int kTile = 64;                 // tokens of a wave's tile
+constexpr float kTop = 15.0f, kRest = 8.0f;   // R follows when t - R passes kTop, to t - kRest
+constexpr float kLeastFactor = 1e-30f;
+constexpr float kLeastStep = 7.888609052210118e-31f;   // 2^-100: a value step below counts as 0
 
-__device__ __forceinline__ float block_reduce(float v, bool sum, float* red) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const float o = __shfl_xor(v, m);
-    v = sum ? v + o : fmaxf(v, o);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
-  for (int w = 1; w < kThreads / 64; ++w) v = sum ? v + red[w] : fmaxf(v, red[w]);
-  return v;
+struct Split {
+  int splits;        // workgroups along the tokens of one row tile
+  int tiles;         // 64-token tiles of each
+  int row_tiles;     // row tiles of a sequence and kv head
+  float* o;          // [splits][T * Hq][D], null when splits == 1
+  float2* rl;        // [splits][T * Hq]: reference and sum
+};
+
+__device__ __forceinline__ float xor_max(float x) {   // over the four lane groups
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
-// One workgroup for each row and query head, one token a lane.
-template <class T>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttArgs a) {
+__device__ __forceinline__ float xor_sum(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// Eight codes as fp16 values 1024 + u.
+__device__ __forceinline__ half8 surplus(uint32_t lo, uint32_t hi) {
+  struct { uint32_t v[4]; } r;
+  r.v[0] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u);
+  r.v[1] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u);
+  r.v[2] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u);
+  r.v[3] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u);
+  return __builtin_bit_cast(half8, r);
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_loose __attribute__((aligned(2)));   // any element's address: the caller's strides
+
+// One row tile's queries, bounds and running state.
+template <int DB>
+struct Rows {
+  half8 q[DB];       // 8 columns of each 32-block
+  float bias;        // -1152 sum q
+  float f;           // scale log2(e) 2^e of the row
+  int lo, hi;        // tokens that the row sees
+  float r, l;        // reference, this lane's share of the sum
+  f32x4 o[2 * DB];   // O^T: columns 16 dt + 4 g + i
+};
+
+// Rows of a tile: the column that MFMA step ks of lane group g starts at.
+template <bool W16>
+__device__ __forceinline__ int column(int ks, int g) {
+  return W16 ? 64 * (ks >> 1) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
+}
+
+template <class T, int DB, bool W16>
+__device__ __forceinline__ void load_rows(const AttArgs& a, Rows<DB>& w, int64_t row0, int n, int len,
+                                          int h, int rr, int g) {
   typedef typename T::storage S;
-  __shared__ float qs[256], ps[kThreads], red[kThreads / 64];
+  const int G = a.Hq / a.c.Hkv, i = rr / G;
+  w.r = -INFINITY;
+  w.l = 0.0f;
+  w.lo = 0;
+  w.hi = INT32_MAX;   // a row that is not there sees everything: it masks no tile
+#pragma unroll
+  for (int dt = 0; dt < 2 * DB; ++dt) w.o[dt] = f32x4{0, 0, 0, 0};
+  float x[DB][8];
+  const bool valid = i < n;
+  if (valid) seen_by(a, len, n, i, w.lo, w.hi);
+  const S* q = (const S*)a.q + (row0 + (valid ? i : 0)) * a.qs[0] + (h * G + (valid ? rr % G : 0)) * a.qs[1];
+  uint32_t top = 0;
+#pragma unroll
+  for (int ks = 0; ks < DB; ++ks) {
+    const int d = column<W16>(ks, g);
+    struct V { S v[8]; } v;
+    const bool in = valid && d < a.c.D;
+    v = in ? __builtin_bit_cast(V, *(const u32x4_loose*)(q + d)) : V{};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[ks][j] = to_f32(v.v[j]);
+      const uint32_t m = abs_bits(x[ks][j]);
+      top = top > m ? top : m;
+    }
+  }
+  // the row's largest exponent, from all four groups (orders like the values for these bits)
+  float m = xor_max(__uint_as_float(top > 0x7f7fffffu ? 0x3f800000u : top));
+  int e = (int)(__float_as_uint(m) >> 23) - 127;
+  e = m == 0.0f ? 0 : e;
+  float sum = 0.0f;
+#pragma unroll
+  for (int ks = 0; ks < DB; ++ks)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const _Float16 v = (_Float16)ldexpf(x[ks][j], -e);
+      w.q[ks][j] = v;
+      sum += (float)v;
+    }
+  w.bias = -1152.0f * xor_sum(sum);
+  w.f = ldexpf(a.scale * kLog2e, e);
+}
+
+// The codes and steps of one 64-token tile on their way in.
+template <int DB>
+struct Keys {
+  u32x4 k[4][(DB + 1) / 2];
+  float ks, sv;
+  int there;         // the lane's sixteen tokens have a page
+};
+
+struct Ids {
+  int k, v;          // pages of the lane's key rows and of its sixteen tokens
+};
+
+__device__ __forceinline__ Ids tile_ids(const AttArgs& a, int b, int tile, int lane) {
+  const int64_t t = (int64_t)tile * kTile;
+  Ids id;
+  id.k = page_id(a.c, b, (t + 16 * ((lane & 15) >> 2)) >> a.c.p_shift);
+  id.v = page_id(a.c, b, (t + 16 * (lane >> 4)) >> a.c.p_shift);
+  return id;
+}
+
+template <int DB, bool W16>
+__device__ __forceinline__ void load_keys(const AttArgs& a, Keys<DB>& k, Ids id, int h, int tile,
+                                          int lane) {
+  const int c = lane & 15, g = lane >> 4, D = a.c.D;
+  const int slot = (tile * kTile + 16 * (c >> 2) + (c & 3)) & (a.c.P - 1);
+  const uint8_t* p = a.c.k_codes + (((int64_t)(id.k < 0 ? 0 : id.k) * a.c.Hkv + h) * a.c.P + slot) * D;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t* r = p + 4 * i * D;
+    if (W16) {
+#pragma unroll
+      for (int s = 0; s < DB / 2; ++s) k.k[i][s] = *(const u32x4*)(r + 64 * s + 16 * g);
+    } else {
+#pragma unroll
+      for (int s = 0; s < DB; ++s) {
+        const int d = column<false>(s, g);
+        const u32x2 v = *(const u32x2*)(r + (d < D ? d : 0));   // past the head: times a query of 0
+        k.k[i][s >> 1][2 * (s & 1)] = v[0];
+        k.k[i][s >> 1][2 * (s & 1) + 1] = v[1];
+      }
+    }
+  }
+  const int64_t blk = (int64_t)(id.v < 0 ? 0 : id.v) * a.c.Hkv + h;
+  k.there = id.v >= 0;
+  k.ks = a.c.k_steps[blk];
+  k.sv = a.c.v_steps[blk];
+}
+
+// NW waves share the tokens of one row tile (QT x 16 rows) and split; their
+// results meet in LDS.
+template <class T, int DB, int QT, int NW, bool W16>
+__global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp) {
+  typedef typename T::storage S;
+  constexpr int DT = 2 * DB;
+  constexpr int kPitch = 32 * DB + 4;
+  __shared__ __attribute__((aligned(16))) float so[NW][QT * 16][kPitch];
+  __shared__ float2 srl[NW][QT * 16];
   const KvArgs& c = a.c;
-  int64_t g = blockIdx.x;
-  const int hq = (int)(g % a.Hq);
-  g /= a.Hq;
-  const int i = (int)(g % a.max_new), b = (int)(g / a.max_new);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, g = lane >> 4;
+
+  int bid = blockIdx.x;
+  const int split = bid % sp.splits;
+  bid /= sp.splits;
+  const int rt = bid % sp.row_tiles;
+  bid /= sp.row_tiles;
+  const int h = bid % c.Hkv, b = bid / c.Hkv;
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
-  if (i >= n) return;
-  const int tid = threadIdx.x, h = hq / (a.Hq / c.Hkv), len = a.lens[b];
-  int lo, hi;
-  seen_by(a, len, n, i, lo, hi);
-  const S* q = (const S*)a.q + (row0 + i) * a.qs[0] + hq * a.qs[1];
-  if (tid < c.D) qs[tid] = to_f32(q[tid]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int t0 = lo; t0 < hi; t0 += kThreads) {
-    const int t = t0 + tid;
-    const int id = t < hi ? page_id(c, b, t >> c.p_shift) : -1;
-    float s = -INFINITY;
-    float vstep = 0.0f;
-    if (id >= 0) {
-      const int64_t blk = (int64_t)id * c.Hkv + h;
-      const uint8_t* k = c.k_codes + (blk * c.P + (t & (c.P - 1))) * c.D;
-      float dot = 0.0f;
-      for (int d = 0; d < c.D; ++d) dot += qs[d] * (float)((int)k[d] - 128);
-      s = dot * c.k_steps[blk] * a.scale;
-      vstep = c.v_steps[blk];
-    }
-    const float top = fmaxf(m, block_reduce(s, false, red));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    const float p = id >= 0 ? __expf(s - ref) : 0.0f;
-    const float keep = __expf(m - ref);
-    l = l * keep + block_reduce(p, true, red);
-    o *= keep;
-    m = top;
-    ps[tid] = id >= 0 ? p * vstep : 0.0f;
-    __syncthreads();
-    if (tid < c.D) {
-      const int count = hi - t0 < kThreads ? hi - t0 : kThreads;
-      for (int j = 0; j < count; ++j) {
-        const int id2 = page_id(c, b, (t0 + j) >> c.p_shift);
-        if (id2 < 0) continue;
-        const uint8_t* v = c.v_codes + (((int64_t)id2 * c.Hkv + h) * c.D + tid) * c.P;
-        o += ps[j] * (float)((int)v[(t0 + j) & (c.P - 1)] - 128);
+  n = n < a.max_new ? n : a.max_new;
+  const int G = a.Hq / c.Hkv, base = rt * 16 * QT, rows = n * G;
+  if (base >= rows) return;
+  const int len = a.lens[b];
+  int lo, hi, unused;
+  seen_by(a, len, n, base / G, lo, unused);
+  seen_by(a, len, n, (base + 16 * QT < rows ? base + 16 * QT - 1 : rows - 1) / G, unused, hi);
+  const int t0 = lo / kTile, nt = hi > lo ? (hi + kTile - 1) / kTile - t0 : 0;
+  const int s0 = t0 + split * sp.tiles;
+  const int s1 = s0 + sp.tiles < t0 + nt ? s0 + sp.tiles : t0 + nt;
+  if (split > 0 && s0 >= s1) return;
+  const bool alone = nt <= sp.tiles;    // no other split has tokens of these rows
+
+  Rows<DB> w[QT];
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt)
+    load_rows<T, DB, W16>(a, w[qt], row0, n, len, h, base + 16 * qt + col, g);
+
+  Keys<DB> kt;
+  Ids id = {-1, -1}, next = {-1, -1};
+  int tile = s0 + wave;
+  if (tile < s1) {
+    id = tile_ids(a, b, tile, lane);
+    load_keys<DB, W16>(a, kt, id, h, tile, lane);
+    next = tile_ids(a, b, tile + NW, lane);
+  }
+  for (; tile < s1; tile += NW) {
+    // values of this tile: sixteen tokens of column 16 dt + col
+    u32x4 v[DT];
+    {
+      const int slot = (tile * kTile + 16 * g) & (c.P - 1);
+      const uint8_t* p = c.v_codes + ((int64_t)(id.v < 0 ? 0 : id.v) * c.Hkv + h) * c.D * c.P + slot;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        const int d = 16 * dt + col;
+        v[dt] = *(const u32x4*)(p + (d < c.D ? d : 0) * c.P);
       }
     }
-    __syncthreads();
+    f32x4 s[QT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) s[qt][i] = f32x4{w[qt].bias, w[qt].bias, w[qt].bias, w[qt].bias};
+#pragma unroll
+      for (int ks = 0; ks < DB; ++ks) {
+        const u32x4 raw = kt.k[i][ks >> 1];
+        const half8 k8 = surplus(raw[2 * (ks & 1)], raw[2 * (ks & 1) + 1]);
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt)
+          s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w[qt].q[ks], s[qt][i], 0, 0, 0);
+      }
+    }
+    // a step that is not finite is NaN for everything that its block touches
+    const float ks = kt.ks + (kt.ks - kt.ks);
+    float sv = kt.sv + (kt.sv - kt.sv);
+    const bool zero = sv < kLeastStep;   // weighs in the sum, adds nothing
+    sv = zero ? kLeastStep : sv;
+    const int there = kt.there;
+    const int tok = tile * kTile + 16 * g;
+    if (tile + NW < s1) {
+      id = next;
+      load_keys<DB, W16>(a, kt, id, h, tile + NW, lane);
+      next = tile_ids(a, b, tile + 2 * NW, lane);
+    }
+    const float lsv = __builtin_amdgcn_logf(sv), rsv = __builtin_amdgcn_rcpf(sv);
+    half8 p[QT][2];
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      Rows<DB>& r = w[qt];
+      // a row that sees none of the lane's tokens takes nothing from their block, NaN or not
+      const bool some = there && r.lo < tok + 16 && tok < r.hi;
+      const bool whole = there && r.lo <= tok && tok + 16 <= r.hi;
+      const float f = some ? r.f * ks : 1.0f, lg = some ? lsv : 0.0f;
+      if (__any(!whole)) {
+        const uint32_t from = (uint32_t)(tok - r.lo), span = some ? (uint32_t)(r.hi - r.lo) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[qt][i][j] = from + (uint32_t)(4 * i + j) < span ? s[qt][i][j] : -INFINITY;
+      }
+      float top = s[qt][0][0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, s[qt][i][j]);
+      // a factor of 0 would make NaN of the -inf of tokens that are not seen
+      const float fp = f < kLeastFactor ? kLeastFactor : f;
+      top = xor_max(top * fp + lg);
+      if (__any(top > r.r + kTop)) {
+        const float to = top > r.r + kTop ? top - kRest : r.r;
+        const float by = to == r.r ? 1.0f : __builtin_amdgcn_exp2f(r.r - to);
+        r.r = to;
+        r.l *= by;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) r.o[dt] *= by;
+      }
+      const float off = lg - (r.r == -INFINITY ? 0.0f : r.r);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[qt][i][j], fp, off));
+          sum += e;
+          p[qt][i >> 1][4 * (i & 1) + j] = (_Float16)e;
+        }
+      if (__any(zero)) {
+        p[qt][0] = zero ? half8{} : p[qt][0];
+        p[qt][1] = zero ? half8{} : p[qt][1];
+      }
+      r.l += some ? sum * rsv : 0.0f;
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      const half8 less = {1152, 1152, 1152, 1152, 1152, 1152, 1152, 1152};
+      const half8 v0 = surplus(v[dt][0], v[dt][1]) - less, v1 = surplus(v[dt][2], v[dt][3]) - less;
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) {
+        w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[qt][0], w[qt].o[dt], 0, 0, 0);
+        w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[qt][1], w[qt].o[dt], 0, 0, 0);
+      }
+    }
   }
-  const int64_t r = (row0 + i) * a.Hq + hq;
-  if (tid < c.D) ((S*)a.out)[r * c.D + tid] = from_f32<S>(l == 0.0f ? 0.0f : o / l);
-  if (tid == 0 && a.lse) a.lse[r] = l == 0.0f ? -INFINITY : m + __logf(l);
+
+  // the waves' results meet
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) {
+    const float l = xor_sum(w[qt].l);
+    if (g == 0) srl[wave][16 * qt + col] = make_float2(w[qt].r, l);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) *(f32x4*)&so[wave][16 * qt + col][16 * dt + 4 * g] = w[qt].o[dt];
+  }
+  __syncthreads();
+  const int quads = c.D / 4;
+  for (int e = tid; e < 16 * QT * quads; e += NW * 64) {
+    const int r = e / quads, d = 4 * (e % quads), rr = base + r;
+    if (rr >= rows) break;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) top = fmaxf(top, srl[k][r].x);
+    f32x4 o = {0, 0, 0, 0};
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float2 x = srl[k][r];
+      const float by = x.x == top ? 1.0f : __builtin_amdgcn_exp2f(x.x - top);
+      o += *(const f32x4*)&so[k][r][d] * by;
+      l += x.y * by;
+    }
+    const int64_t out = (row0 + rr / G) * a.Hq + h * G + rr % G;
+    if (alone) {
+      const float by = l == 0.0f ? 0.0f : 1.0f / l;
+      struct { S v[4]; } y;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y.v[j] = from_f32<S>(o[j] * by);
+      *(u32x2*)((S*)a.out + out * c.D + d) = __builtin_bit_cast(u32x2, y);
+      if (d == 0 && a.lse) a.lse[out] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+    } else {
+      const int64_t part = split * c.T * a.Hq + out;
+      *(f32x4*)(sp.o + part * c.D + d) = o;
+      if (d == 0) sp.rl[part] = make_float2(top, l);
+    }
+  }
+}
+
+// Joins the splits of the rows that had more than one: a wave for each row and head.
+template <class T>
+__global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows_per_tile) {
+  typedef typename T::storage S;
+  const KvArgs& c = a.c;
+  const int lane = threadIdx.x & 63;
+  int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // (b, i, hq)
+  const int hq = (int)(e % a.Hq);
+  e /= a.Hq;
+  const int i = (int)(e % a.max_new);
+  const int64_t b = e / a.max_new;
+  if (b >= c.B) return;
+  int64_t row0;
+  int n;
+  rows_of(c, (int)b, row0, n);
+  n = n < a.max_new ? n : a.max_new;
+  if (i >= n) return;
+  const int G = a.Hq / c.Hkv, len = a.lens[b], rows = n * G;
+  const int base = (i * G + hq % G) / rows_per_tile * rows_per_tile;
+  int lo, hi, unused;
+  seen_by(a, len, n, base / G, lo, unused);
+  seen_by(a, len, n, (base + rows_per_tile < rows ? base + rows_per_tile - 1 : rows - 1) / G, unused, hi);
+  const int t0 = lo / kTile, nt = hi > lo ? (hi + kTile - 1) / kTile - t0 : 0;
+  if (nt <= sp.tiles) return;
+  const int active = (nt + sp.tiles - 1) / sp.tiles;
+  const int64_t out = (row0 + i) * a.Hq + hq, step = c.T * a.Hq;
+  float top = -INFINITY;
+  for (int s = lane; s < active; s += 64) top = fmaxf(top, sp.rl[s * step + out].x);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+  float l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  const int d = 4 * lane;
+  for (int s = 0; s < active; ++s) {
+    const float2 x = sp.rl[s * step + out];
+    const float by = x.x == top ? 1.0f : __builtin_amdgcn_exp2f(x.x - top);
+    l += x.y * by;
+    if (d < c.D) o += *(const f32x4*)(sp.o + (s * step + out) * c.D + d) * by;
+  }
+  const float by = l == 0.0f ? 0.0f : 1.0f / l;
+  if (d < c.D) {
+    struct { S v[4]; } y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y.v[j] = from_f32<S>(o[j] * by);
+    *(u32x2*)((S*)a.out + out * c.D + d) = __builtin_bit_cast(u32x2, y);
+  }
+  if (lane == 0 && a.lse) a.lse[out] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// How a call is split, from its sizes alone.
+struct Plan {
+  int QT, NW, splits, tiles, row_tiles;
+};
+
+Plan plan(int64_t B, int Hq, int Hkv, int max_new, int max_len) {
+  Plan p;
+  const int64_t rows = (int64_t)max_new * (Hq / Hkv);
+  p.QT = rows > 16 ? 2 : 1;
+  p.NW = 4;
+  p.row_tiles = (int)((rows + 16 * p.QT - 1) / (16 * p.QT));
+  const int tiles = (max_len + kTile - 1) / kTile + 1;   // a window may begin inside a tile
+  const int64_t groups = B * Hkv * (int64_t)p.row_tiles;
+  int64_t want = groups >= 1024 ? 1 : 1024 / groups;
+  const int64_t most = (tiles + p.NW - 1) / p.NW;
+  want = want < most ? want : most;
+  p.tiles = (int)((tiles + want - 1) / want);
+  p.tiles = (p.tiles + p.NW - 1) / p.NW * p.NW;
+  p.splits = (tiles + p.tiles - 1) / p.tiles;
+  return p;
+}
+
+template <class T, int DB, int QT, int NW>
+void go_w(const AttArgs& a, const Split& sp, unsigned grid, hipStream_t st) {
+  if constexpr (DB % 2 == 0) {
+    if (a.c.D % 64 == 0) {
+      attention_kernel<T, DB, QT, NW, true><<<grid, NW * 64, 0, st>>>(a, sp);
+      return;
+    }
+  }
+  attention_kernel<T, DB, QT, NW, false><<<grid, NW * 64, 0, st>>>(a, sp);
+}
+
+template <class T, int DB>
+void go_q(const AttArgs& a, const Plan& p, const Split& sp, unsigned grid, hipStream_t st) {
+  if (p.QT == 1) go_w<T, DB, 1, 4>(a, sp, grid, st);
+  else go_w<T, DB, 2, 4>(a, sp, grid, st);
+}
+
+template <class T>
+hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)a.c.B * a.c.Hkv * p.row_tiles * p.splits);
+  {
+    ProfScope prof("awq_kv_attention", st);
+    switch ((a.c.D + 31) / 32) {
+      case 1: go_q<T, 1>(a, p, sp, grid, st); break;
+      case 2: go_q<T, 2>(a, p, sp, grid, st); break;
+      case 3: go_q<T, 3>(a, p, sp, grid, st); break;
+      case 4: go_q<T, 4>(a, p, sp, grid, st); break;
+      case 5: go_q<T, 5>(a, p, sp, grid, st); break;
+      case 6: go_q<T, 6>(a, p, sp, grid, st); break;
+      case 7: go_q<T, 7>(a, p, sp, grid, st); break;
+      default: go_q<T, 8>(a, p, sp, grid, st); break;
+    }
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  ProfScope prof("awq_kv_attention_join", st);
+  const int64_t rows = (int64_t)a.c.B * a.max_new * a.Hq;
+  join_kernel<T><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a, sp, 16 * p.QT);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t kv_attention_ws_bytes(int64_t, int64_t, int, int, int, int, int) { return 0; }
-
-int64_t kv_attention_blocks(int64_t, int64_t B, int Hq, int, int, int max_new, int) {
-  return max_new > INT64_MAX / Hq / B ? INT64_MAX : B * max_new * Hq;
+size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
+                             int max_len) {
+  const Plan p = plan(B, Hq, Hkv, max_new, max_len);
+  return p.splits == 1 ? 0 : (size_t)p.splits * T * Hq * (D + 2) * 4;
 }
 
-hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void*, hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.c.B * a.max_new * a.Hq);
-  ProfScope prof("awq_kv_attention", st);
-  if (dt == AWQ_F16) attention_kernel<F16T><<<grid, kThreads, 0, st>>>(a);
-  else attention_kernel<BF16T><<<grid, kThreads, 0, st>>>(a);
-  return hipGetLastError();
+int64_t kv_attention_blocks(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
+                            int max_len) {
+  if (max_new > (int64_t)INT32_MAX / Hq) return INT64_MAX;
+  const Plan p = plan(B, Hq, Hkv, max_new, max_len);
+  const int64_t a = p.row_tiles * (int64_t)p.splits, rows = (int64_t)max_new * Hq;
+  if (B * Hkv > INT32_MAX || B * Hkv > INT32_MAX / a || B > INT32_MAX / rows * 4) return INT64_MAX;
+  return B * Hkv * a;
+}
+
+hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipStream_t st) {
+  const Plan p = plan(a.c.B, a.Hq, a.c.Hkv, a.max_new, a.max_len);
+  Split sp = {p.splits, p.tiles, p.row_tiles, nullptr, nullptr};
+  if (p.splits > 1) {
+    sp.o = (float*)ws;
+    sp.rl = (float2*)(sp.o + (size_t)p.splits * a.c.T * a.Hq * a.c.D);
+  }
+  return dt == AWQ_F16 ? go<F16T>(a, p, sp, st) : go<BF16T>(a, p, sp, st);
 }
 
 }  // namespace awq

@@ -985,7 +985,7 @@ size_t awq_kv_attention_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t
                                        int64_t D, int64_t max_new, int64_t max_len) {
   if (T < 1 || B < 1 || kv_heads < 1 || Hq < 1 || Hq % kv_heads != 0 || D < 1 || max_new < 1 ||
       max_len < 1 || T > INT32_MAX || B > INT32_MAX || Hq > kMaxHeads || D > 256 ||
-      max_new > INT32_MAX || max_len > INT32_MAX)
+      max_new > INT32_MAX / 2 || max_len > (1 << 30))
     return 0;
   return align_up(awq::kv_attention_ws_bytes(T, B, (int)Hq, (int)kv_heads, (int)D, (int)max_new,
                                              (int)max_len));
@@ -1019,6 +1019,8 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
   if (!aligned(q, 2) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4))
     return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned (out: to 16 bytes)");
   const int64_t reach = std::max<int64_t>(1, std::min<int64_t>(max_len, max_pages * a.c.P));
+  if (reach > (1 << 30))
+    return fail(AWQ_ERR_UNSUPPORTED, "%lld tokens of a sequence exceed 2^30", (long long)reach);
   if (awq::kv_attention_blocks(T, B, (int)Hq, a.c.Hkv, a.c.D, (int)max_new, (int)reach) > kMaxGrid)
     return fail(AWQ_ERR_UNSUPPORTED, "too many rows for one launch");
   const size_t need = awq_kv_attention_workspace_size(T, B, Hq, a.c.Hkv, a.c.D, max_new, reach);

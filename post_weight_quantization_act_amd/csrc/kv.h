@@ -135,6 +135,7 @@ __device__ __forceinline__ void seen_by(const AttArgs& a, int len, int n, int i,
   const int64_t table = (int64_t)a.c.max_pages << a.c.p_shift;   // past it there are no pages
   hi = hi > len ? len : hi;
   hi = hi > table ? (int)table : hi;
+  hi = hi > a.max_len ? a.max_len : hi;
   lo = lo < 0 ? 0 : lo;
 }
 
