@@ -109,6 +109,7 @@ _LIB = None
 
 _P, _I64, _I32, _U32, _SZ, _D = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint32,
                                  ctypes.c_size_t, ctypes.c_double)
+_I64x4 = _I64 * 4
 _SIGS = {
     "awq_version": ([], ctypes.c_char_p),
     "awq_last_error": ([], ctypes.c_char_p),
@@ -509,30 +510,62 @@ def awq_lowbit_gemm(Xs: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tenso
     return out
 
 
-def _heads(t: torch.Tensor, name: str, dims: int = 3) -> torch.Tensor:
-    """A GPU tensor [rows, heads, D] (or [B, S, H, D]) whose heads' columns lie together."""
+def _on_gpu(t: torch.Tensor, name: str) -> int:
+    """The GPU that t is on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
+    return t.get_device()
+
+
+def _beside(t: torch.Tensor, name: str, gpu: int) -> torch.Tensor:
+    if _on_gpu(t, name) != gpu:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{gpu}")
+    return t
+
+
+def _heads(t: torch.Tensor, name: str, gpu: int, dims: int = 3) -> torch.Tensor:
+    """A GPU tensor [rows, heads, D] (or [B, S, H, D]) whose heads' columns lie together."""
+    _beside(t, name, gpu)
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return t
 
 
-def _ints(t: torch.Tensor, name: str, *shape: int) -> int:
-    _dev(t, name)
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+def _ints(t: torch.Tensor, name: str, gpu: int, shape: tuple) -> int:
+    _beside(t, name, gpu)
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)}, got {t.dtype} "
+                         f"{list(t.shape)}")
     return t.data_ptr()
 
 
-def _same_device(like, /, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+def _dense(t: torch.Tensor, name: str, gpu: int, like: torch.Tensor, dtype: torch.dtype) -> int:
+    _beside(t, name, gpu)
+    if t.shape != like.shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(like.shape)}, got {t.dtype} "
+                         f"{list(t.shape)}")
+    return t.data_ptr()
+
+
+def _run(fn: str, gpu: int, *args) -> None:
+    """Calls fn on the tensors' GPU and its current stream."""
+    f = getattr(library(), fn)
+    if torch.cuda.current_device() == gpu:
+        status = f(*args, _raw_stream(gpu))
+    else:
+        with torch.cuda.device(gpu):
+            status = f(*args, _raw_stream(gpu))
+    if status != 0:
+        _check(status)
+
+
+# the current stream's handle without a Stream object around it (a few calls in a
+# decode step's few microseconds each)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
 
 
 def awq_rope_table(n_pos: int, rot: int, base: float = 10000.0, scaling: str = "none",
@@ -544,18 +577,18 @@ def awq_rope_table(n_pos: int, rot: int, base: float = 10000.0, scaling: str = "
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
     sc = RopeScaling(_ROPE_SCALING[scaling], factor, original, low, high, magnitude)
     table = torch.empty((max(n_pos, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device=device)
-    _dev(table, "table")
-    with torch.cuda.device(table.device):
-        _check(library().awq_rope_table(n_pos, rot, base, ctypes.byref(sc), table.data_ptr(),
-                                        _stream(table.device)))
+    _run("awq_rope_table", _on_gpu(table, "table"), n_pos, rot, base, ctypes.byref(sc),
+         table.data_ptr())
     return table
 
 
-def _table(table: torch.Tensor):
-    _dev(table, "table")
-    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32:
-        raise ValueError("table must be fp32 [positions, rot/2, 2] (awq_rope_table)")
-    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+def _table(table: torch.Tensor, gpu: int):
+    _beside(table, "table", gpu)
+    if table.dim() != 3 or table.shape[2] != 2 or table.dtype is not torch.float32 \
+            or not table.is_contiguous():
+        raise ValueError("table must be contiguous fp32 [positions, rot/2, 2] (awq_rope_table)")
+    n_pos, half, _ = table.shape
+    return table.data_ptr(), n_pos, 2 * half
 
 
 def awq_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor | None = None,
@@ -565,27 +598,29 @@ def awq_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor | Non
     head's first 2 * table.shape[1] columns turned by the row's position; transpose=True gives the
     gradient with respect to x.  positions int32 [T], [S] or [B, S]; None: the row's index.
     out may be x."""
-    x4 = _heads(x, "x", x.dim() if isinstance(x, torch.Tensor) and x.dim() == 4 else 3)
-    x4 = x4 if x4.dim() == 4 else x4.unsqueeze(0)
-    tp, n_pos, rot = _table(table)
+    gpu = _on_gpu(x, "x")
+    dims = 4 if x.dim() == 4 else 3
+    _heads(x, "x", gpu, dims)
+    tp, n_pos, rot = _table(table, gpu)
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError("out must have x's shape and out_dtype")
-    o4 = _heads(out, "out", x.dim())
-    o4 = o4 if o4.dim() == 4 else o4.unsqueeze(0)
-    B, S, H, D = x4.shape
+    else:
+        _heads(out, "out", gpu, dims)
+        if out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must have x's shape and out_dtype")
+    xs, os_ = x.stride(), out.stride()
+    if dims == 4:
+        B, S, H, D = x.shape
+    else:
+        (S, H, D), B = x.shape, 1
+        xs, os_ = (0, *xs), (0, *os_)
     pp, ps = None, 0
     if positions is not None:
-        shape = (B, S) if positions.dim() == 2 else (S,)
-        pp, ps = _ints(positions, "positions", *shape), S if positions.dim() == 2 else 0
-    _same_device(x, table=table, positions=positions, out=out)
-    xs, os_ = (_I64 * 3)(*x4.stride()[:3]), (_I64 * 3)(*o4.stride()[:3])
-    with torch.cuda.device(x.device):
-        _check(library().awq_rope(x.data_ptr(), _dtype(x), B, S, H, D, xs, pp, ps, tp, n_pos, rot,
-                                  (AWQ_ROPE_INTERLEAVED if interleaved else 0)
-                                  | (AWQ_ROPE_TRANSPOSE if transpose else 0), out.data_ptr(),
-                                  _dtype(out), os_, _stream(x.device)))
+        ps = S if positions.dim() == 2 else 0
+        pp = _ints(positions, "positions", gpu, (B, S) if ps else (S,))
+    _run("awq_rope", gpu, x.data_ptr(), _dtype(x), B, S, H, D, _I64x4(*xs), pp, ps, tp, n_pos, rot,
+         (AWQ_ROPE_INTERLEAVED if interleaved else 0) | (AWQ_ROPE_TRANSPOSE if transpose else 0),
+         out.data_ptr(), _dtype(out), _I64x4(*os_))
     return out
 
 
@@ -595,18 +630,16 @@ class KvCache:
     Holds the tensors; which page is whose is the caller's (page tables)."""
 
     def __init__(self, k_codes, v_codes, k_steps, v_steps):
-        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes"), (k_steps, "k_steps"),
-                        (v_steps, "v_steps")):
-            _dev(t, name)
-            _same_device(k_codes, **{name: t})
-        if k_codes.dim() != 4 or k_codes.dtype != torch.uint8:
-            raise ValueError("k_codes must be uint8 [n_pages, kv_heads, page, D]")
+        self.gpu = _on_gpu(k_codes, "k_codes")
+        if k_codes.dim() != 4 or k_codes.dtype is not torch.uint8 or not k_codes.is_contiguous():
+            raise ValueError("k_codes must be contiguous uint8 [n_pages, kv_heads, page, D]")
         n, h, p, d = k_codes.shape
-        if tuple(v_codes.shape) != (n, h, d, p) or v_codes.dtype != torch.uint8:
-            raise ValueError(f"v_codes must be uint8 {[n, h, d, p]}")
-        for t, name in ((k_steps, "k_steps"), (v_steps, "v_steps")):
-            if tuple(t.shape) != (n, h) or t.dtype != torch.float32:
-                raise ValueError(f"{name} must be fp32 {[n, h]}")
+        for t, name, dtype, shape in ((v_codes, "v_codes", torch.uint8, (n, h, d, p)),
+                                      (k_steps, "k_steps", torch.float32, (n, h)),
+                                      (v_steps, "v_steps", torch.float32, (n, h))):
+            _beside(t, name, self.gpu)
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
         self.k_codes, self.v_codes, self.k_steps, self.v_steps = k_codes, v_codes, k_steps, v_steps
         self.n_pages, self.kv_heads, self.page, self.head_dim = n, h, p, d
         self.device = k_codes.device
@@ -622,18 +655,17 @@ class KvCache:
                    torch.empty((n_pages, kv_heads), dtype=torch.float32, device=device))
 
 
-def _paged(cache: KvCache, pages, starts, **per_sequence):
-    """(B, pointers of pages and starts and of each int32 [B] tensor, pages of a sequence)."""
+def _paged(cache: KvCache, pages, starts, per_sequence, name):
+    """(GPU, sequences, pages of a sequence, pointers of pages, starts and the int32 [B] tensor)."""
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache")
+    gpu = cache.gpu
     if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
         raise ValueError("pages must be an int32 tensor [sequences, pages]")
-    B = pages.shape[0]
-    ptrs = [_ints(pages, "pages", B, pages.shape[1]),
-            None if starts is None else _ints(starts, "starts", B + 1)]
-    ptrs += [_ints(t, name, B) for name, t in per_sequence.items()]
-    _same_device(cache, pages=pages, starts=starts, **per_sequence)
-    return B, ptrs
+    B, most = pages.shape
+    return (gpu, B, most, _ints(pages, "pages", gpu, (B, most)),
+            None if starts is None else _ints(starts, "starts", gpu, (B + 1,)),
+            _ints(per_sequence, name, gpu, (B,)))
 
 
 def awq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,
@@ -646,38 +678,36 @@ def awq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.
     [T, Hq, D], if given, is turned alike and returned (dense, of q_dtype).  lens int32 [B] counts
     the new rows too; starts None: one row for each sequence; max_new: the most rows of a
     sequence (None: 1 without starts, T with)."""
-    B, (pp, sp, lp) = _paged(cache, pages, starts, lens=lens)
-    _heads(k, "k")
-    _heads(v, "v")
-    T = k.shape[0]
-    if tuple(k.shape) != (T, cache.kv_heads, cache.head_dim) or v.shape != k.shape \
-            or v.dtype != k.dtype:
+    gpu, B, most, pp, sp, lp = _paged(cache, pages, starts, lens, "lens")
+    _heads(k, "k", gpu)
+    _heads(v, "v", gpu)
+    shape, dtype = k.shape, k.dtype
+    T = shape[0]
+    if shape != (T, cache.kv_heads, cache.head_dim) or v.shape != shape or v.dtype is not dtype:
         raise ValueError(f"k and v must be [T, {cache.kv_heads}, {cache.head_dim}] of one dtype")
-    tp, n_pos, rot = (None, 0, 0) if table is None else _table(table)
+    tp, n_pos, rot = (None, 0, 0) if table is None else _table(table, gpu)
     qp, op, Hq, qs, odt = None, None, 0, None, AWQ_F32
     if q is not None:
-        _heads(q, "q")
+        _heads(q, "q", gpu)
         Hq = q.shape[1]
-        if tuple(q.shape) != (T, Hq, cache.head_dim) or q.dtype != k.dtype:
+        if q.shape != (T, Hq, cache.head_dim) or q.dtype is not dtype:
             raise ValueError(f"q must be [T, Hq, {cache.head_dim}] of k's dtype")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
-        elif q_out.shape != q.shape or (q_dtype is not None and q_out.dtype != q_dtype):
-            raise ValueError("q_out must have q's shape and q_dtype")
-        qp, op, odt = q.data_ptr(), _dev(q_out, "q_out").data_ptr(), _dtype(q_out)
-        qs = (_I64 * 2)(q.stride(0), q.stride(1))
+            q_out = torch.empty(q.shape, dtype=q_dtype or dtype, device=cache.device)
+            op = q_out.data_ptr()
+        else:
+            op = _dense(q_out, "q_out", gpu, q, q_dtype or q_out.dtype)
+        qp, odt = q.data_ptr(), _dtype(q_out)
+        qs = _I64x4(*q.stride()[:2])
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _same_device(cache, k=k, v=v, table=table, positions=positions, q=q, q_out=q_out)
-    strides = (_I64 * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
     if max_new is None:
         max_new = 1 if starts is None else T
-    with torch.cuda.device(cache.device):
-        _check(library().awq_kv_append(
-            cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k), T, strides, sp, lp, B, pp,
-            pages.shape[1], max_new, tp, n_pos, rot, AWQ_ROPE_INTERLEAVED if interleaved else 0,
-            None if positions is None else _ints(positions, "positions", T), qp, Hq, qs, op, odt,
-            _stream(cache.device)))
+    _run("awq_kv_append", gpu, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k), T,
+         _I64x4(*k.stride()[:2], *v.stride()[:2]), sp, lp, B, pp, most, max_new, tp, n_pos, rot,
+         AWQ_ROPE_INTERLEAVED if interleaved else 0,
+         None if positions is None else _ints(positions, "positions", gpu, (T,)), qp, Hq, qs, op,
+         odt)
     return q_out
 
 
@@ -687,7 +717,7 @@ def awq_kv_read(cache: KvCache, first: torch.Tensor, pages: torch.Tensor,
     """Tokens first[b] and on of every sequence as values -> (k, v) [total, kv_heads, D];
     starts int32 [B + 1] places each sequence's rows (None: one token each), total =
     starts[B] on the host, max_count the most tokens of a sequence (None: total)."""
-    B, (pp, sp, fp) = _paged(cache, pages, starts, first=first)
+    gpu, B, most, pp, sp, fp = _paged(cache, pages, starts, first, "first")
     if total is None:
         if starts is not None:
             raise ValueError("total (starts[B], on the host) is needed with starts")
@@ -696,10 +726,8 @@ def awq_kv_read(cache: KvCache, first: torch.Tensor, pages: torch.Tensor,
         max_count = 1 if starts is None else total
     k = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
     v = torch.empty_like(k)
-    with torch.cuda.device(cache.device):
-        _check(library().awq_kv_read(cache._ref, total, sp, fp, B, pp, pages.shape[1], max_count,
-                                     k.data_ptr(), v.data_ptr(), _dtype(k),
-                                     _stream(cache.device)))
+    _run("awq_kv_read", gpu, cache._ref, total, sp, fp, B, pp, most, max_count, k.data_ptr(),
+         v.data_ptr(), _dtype(k))
     return k, v
 
 
@@ -717,34 +745,35 @@ def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages:
     request, the logarithm of each row's sum, fp32 [T, Hq].  lens int32 [B]: tokens of each
     sequence, the queries' own among them; max_new as in awq_kv_append; max_len: at least the
     longest length (None: what the page table can hold); scale None: D ** -0.5."""
-    B, (pp, sp, lp) = _paged(cache, pages, starts, lens=lens)
-    _heads(q, "q")
+    gpu, B, most, pp, sp, lp = _paged(cache, pages, starts, lens, "lens")
+    _heads(q, "q", gpu)
     T, Hq, D = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q must be [T, Hq, {cache.head_dim}]")
-    most = pages.shape[1] * cache.page
-    max_len = most if max_len is None else min(max_len, most)
+    if max_len is None or max_len > most * cache.page:
+        max_len = most * cache.page
     if max_new is None:
         max_new = 1 if starts is None else T
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and dtype")
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    if workspace is None:
-        need = awq_kv_attention_workspace_size(T, B, Hq, cache.kv_heads, D, max_new, max_len)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _same_device(cache, q=q, out=out, workspace=workspace)
-    qs = (_I64 * 2)(q.stride(0), q.stride(1))
-    with torch.cuda.device(cache.device):
-        _check(library().awq_kv_attention(
-            cache._ref, q.data_ptr(), _dtype(q), T, Hq, qs, sp, lp, B, pp, pages.shape[1], max_new,
-            max_len, scale, window, 0 if causal else AWQ_ATT_FULL, _dev(out, "out").data_ptr(),
-            None if lse is None else lse.data_ptr(),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), _stream(cache.device)))
+        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", gpu, q, q.dtype)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=cache.device) if return_lse else None
+    ws, size = None, 0
+    if workspace is not None:
+        ws, size = _dev(_beside(workspace, "workspace", gpu), "workspace").data_ptr(), workspace.nbytes
+    else:
+        size = library().awq_kv_attention_workspace_size(T, B, Hq, cache.kv_heads, D, max_new,
+                                                         max_len)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
+            ws = workspace.data_ptr()
+    _run("awq_kv_attention", gpu, cache._ref, q.data_ptr(), _dtype(q), T, Hq,
+         _I64x4(*q.stride()[:2]), sp, lp, B, pp, most, max_new, max_len, scale, window,
+         0 if causal else AWQ_ATT_FULL, op, None if lse is None else lse.data_ptr(), ws, size)
     return (out, lse) if return_lse else out
 
 

@@ -196,12 +196,15 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
 
+  // heads first, splits last: workgroups are dealt to the eight XCDs in turn, so a
+  // sequence's splits, of which only the first few may hold tokens, never fall on one
+  // XCD, and with 8 heads the row tiles of a head read its keys through one L2
   int bid = blockIdx.x;
-  const int split = bid % sp.splits;
-  bid /= sp.splits;
-  const int rt = bid % sp.row_tiles;
-  bid /= sp.row_tiles;
-  const int h = bid % c.Hkv, b = bid / c.Hkv;
+  const int h = bid % c.Hkv;
+  bid /= c.Hkv;
+  const int b = bid % c.B;
+  bid /= c.B;
+  const int rt = bid % sp.row_tiles, split = bid / sp.row_tiles;
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
@@ -371,21 +374,24 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
   }
 }
 
-// Joins the splits of the rows that had more than one: a wave for each row and head.
+// Joins the splits of a row and head that had more than one: a workgroup each, its
+// threads in groups of D / 4 that share the splits, so that the loads of many
+// splits are in flight at once.
 template <class T>
 __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows_per_tile) {
   typedef typename T::storage S;
+  __shared__ __attribute__((aligned(16))) float so[256 * 4];
+  __shared__ float sl[128], stop[4];
   const KvArgs& c = a.c;
-  const int lane = threadIdx.x & 63;
-  int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // (b, i, hq)
+  const int tid = threadIdx.x;
+  int64_t e = blockIdx.x;   // (b, i, hq)
   const int hq = (int)(e % a.Hq);
   e /= a.Hq;
   const int i = (int)(e % a.max_new);
-  const int64_t b = e / a.max_new;
-  if (b >= c.B) return;
+  const int b = (int)(e / a.max_new);
   int64_t row0;
   int n;
-  rows_of(c, (int)b, row0, n);
+  rows_of(c, b, row0, n);
   n = n < a.max_new ? n : a.max_new;
   if (i >= n) return;
   const int G = a.Hq / c.Hkv, len = a.lens[b], rows = n * G;
@@ -398,26 +404,40 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows
   const int active = (nt + sp.tiles - 1) / sp.tiles;
   const int64_t out = (row0 + i) * a.Hq + hq, step = c.T * a.Hq;
   float top = -INFINITY;
-  for (int s = lane; s < active; s += 64) top = fmaxf(top, sp.rl[s * step + out].x);
+  for (int s = tid; s < active; s += 256) top = fmaxf(top, sp.rl[s * step + out].x);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+  if ((tid & 63) == 0) stop[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(stop[0], stop[1]), fmaxf(stop[2], stop[3]));
+  const int quads = c.D / 4, groups = 256 / quads, group = tid / quads, d = 4 * (tid % quads);
   float l = 0.0f;
   f32x4 o = {0, 0, 0, 0};
-  const int d = 4 * lane;
-  for (int s = 0; s < active; ++s) {
-    const float2 x = sp.rl[s * step + out];
-    const float by = x.x == top ? 1.0f : __builtin_amdgcn_exp2f(x.x - top);
-    l += x.y * by;
-    if (d < c.D) o += *(const f32x4*)(sp.o + (s * step + out) * c.D + d) * by;
+  if (group < groups) {
+#pragma unroll 4
+    for (int s = group; s < active; s += groups) {
+      const float2 x = sp.rl[s * step + out];
+      const float by = x.x == top ? 1.0f : __builtin_amdgcn_exp2f(x.x - top);
+      l += x.y * by;
+      o += *(const f32x4*)(sp.o + (s * step + out) * c.D + d) * by;
+    }
+    *(f32x4*)&so[group * c.D + d] = o;
+    if (d == 0) sl[group] = l;
+  }
+  __syncthreads();
+  if (group != 0) return;
+  o = f32x4{0, 0, 0, 0};
+  l = 0.0f;
+  for (int g = 0; g < groups; ++g) {
+    o += *(const f32x4*)&so[g * c.D + d];
+    l += sl[g];
   }
   const float by = l == 0.0f ? 0.0f : 1.0f / l;
-  if (d < c.D) {
-    struct { S v[4]; } y;
+  struct { S v[4]; } y;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y.v[j] = from_f32<S>(o[j] * by);
-    *(u32x2*)((S*)a.out + out * c.D + d) = __builtin_bit_cast(u32x2, y);
-  }
-  if (lane == 0 && a.lse) a.lse[out] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+  for (int j = 0; j < 4; ++j) y.v[j] = from_f32<S>(o[j] * by);
+  *(u32x2*)((S*)a.out + out * c.D + d) = __builtin_bit_cast(u32x2, y);
+  if (d == 0 && a.lse) a.lse[out] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // How a call is split, from its sizes alone.
@@ -429,12 +449,16 @@ Plan plan(int64_t B, int Hq, int Hkv, int max_new, int max_len) {
   Plan p;
   const int64_t rows = (int64_t)max_new * (Hq / Hkv);
   p.QT = rows > 16 ? 2 : 1;
-  p.NW = 4;
   p.row_tiles = (int)((rows + 16 * p.QT - 1) / (16 * p.QT));
-  const int tiles = (max_len + kTile - 1) / kTile + 1;   // a window may begin inside a tile
+  const int tiles = (max_len + kTile - 1) / kTile;
   const int64_t groups = B * Hkv * (int64_t)p.row_tiles;
-  int64_t want = groups >= 1024 ? 1 : 1024 / groups;
-  const int64_t most = (tiles + p.NW - 1) / p.NW;
+  // Few short sequences: eight waves a workgroup and no second launch.
+  p.NW = p.QT == 1 && groups <= 256 && tiles <= 16 ? 8 : 4;
+  // One sequence: all workgroups alike, so as many as run at once (two on a compute
+  // unit).  Several: lengths differ, and finer splits even them out.
+  const int64_t target = B == 1 ? 512 : 4096;
+  int64_t want = groups >= target ? 1 : target / groups;
+  const int64_t most = (tiles + 2 * p.NW - 1) / (2 * p.NW);
   want = want < most ? want : most;
   p.tiles = (int)((tiles + want - 1) / want);
   p.tiles = (p.tiles + p.NW - 1) / p.NW * p.NW;
@@ -455,7 +479,8 @@ void go_w(const AttArgs& a, const Split& sp, unsigned grid, hipStream_t st) {
 
 template <class T, int DB>
 void go_q(const AttArgs& a, const Plan& p, const Split& sp, unsigned grid, hipStream_t st) {
-  if (p.QT == 1) go_w<T, DB, 1, 4>(a, sp, grid, st);
+  if (p.QT == 1 && p.NW == 8) go_w<T, DB, 1, 8>(a, sp, grid, st);
+  else if (p.QT == 1) go_w<T, DB, 1, 4>(a, sp, grid, st);
   else go_w<T, DB, 2, 4>(a, sp, grid, st);
 }
 
@@ -479,7 +504,7 @@ hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) 
   if (e != hipSuccess || p.splits == 1) return e;
   ProfScope prof("awq_kv_attention_join", st);
   const int64_t rows = (int64_t)a.c.B * a.max_new * a.Hq;
-  join_kernel<T><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a, sp, 16 * p.QT);
+  join_kernel<T><<<(unsigned)rows, 256, 0, st>>>(a, sp, 16 * p.QT);
   return hipGetLastError();
 }
 
@@ -496,7 +521,7 @@ int64_t kv_attention_blocks(int64_t T, int64_t B, int Hq, int Hkv, int D, int ma
   if (max_new > (int64_t)INT32_MAX / Hq) return INT64_MAX;
   const Plan p = plan(B, Hq, Hkv, max_new, max_len);
   const int64_t a = p.row_tiles * (int64_t)p.splits, rows = (int64_t)max_new * Hq;
-  if (B * Hkv > INT32_MAX || B * Hkv > INT32_MAX / a || B > INT32_MAX / rows * 4) return INT64_MAX;
+  if (B * Hkv > INT32_MAX || B * Hkv > INT32_MAX / a || B > INT32_MAX / rows) return INT64_MAX;
   return B * Hkv * a;
 }
 
