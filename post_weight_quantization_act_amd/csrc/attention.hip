@@ -68,10 +68,6 @@ __device__ __forceinline__ half8 surplus(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(half8, r);
 }
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_loose __attribute__((aligned(2)));   // any element's address: the caller's strides
-
 // One row tile's queries, bounds and running state.
 template <int DB>
 struct Rows {

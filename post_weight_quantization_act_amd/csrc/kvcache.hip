@@ -14,19 +14,240 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Largest of two values over the workgroup (red: one pair for each wave).
+__device__ __forceinline__ void block_max(uint32_t& k, uint32_t& v, uint2* red) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) {
-    const uint32_t o = __shfl_xor(v, m);
-    v = v > o ? v : o;
+    k = umax(k, (uint32_t)__shfl_xor((int)k, m));
+    v = umax(v, (uint32_t)__shfl_xor((int)v, m));
   }
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = make_uint2(k, v);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
+  for (int w = 0; w < waves; ++w) {
+    k = umax(k, red[w].x);
+    v = umax(v, red[w].y);
+  }
+}
+
+// The step after the new tokens' largest value came in (bits of |x|: a NaN's are above
+// every number's, so a NaN among the values gives a NaN step).
+__device__ __forceinline__ float next_step(uint32_t top, float was) {
+  const float step = __uint_as_float(top) / 127.0f;
+  return __float_as_uint(step) > __float_as_uint(was) ? step : was;
+}
+
+__device__ __forceinline__ uint32_t coded(float x, float step) {
+  return (uint32_t)((step > 0.0f ? code_of(x / step) : 0) + 128);
+}
+
+// Codes of one dword to a step `by` times as coarse.
+__device__ __forceinline__ uint32_t moved(uint32_t w, float by) {
+  uint32_t r = 0;
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) v = v > red[w] ? v : red[w];
-  return v;
+  for (int i = 0; i < 4; ++i)
+    r |= (uint32_t)(code_of((float)((int)((w >> (8 * i)) & 255) - 128) * by) + 128) << (8 * i);
+  return r;
+}
+
+// Where a workgroup of an append works: the new tokens [lo, hi) of a page of a sequence.
+struct Place {
+  int64_t row_lo, row0, first;   // rows of token lo and of the sequence; number of its first new token
+  int64_t page;                  // the sequence's page
+  int lo, hi;
+};
+
+__device__ __forceinline__ bool find_place(const AppendArgs& a, int b, int j, Place& p) {
+  const KvArgs& c = a.c;
+  int n;
+  rows_of(c, b, p.row0, n);
+  const int64_t len = a.lens[b];
+  p.first = len - n;
+  p.page = ((p.first < 0 ? 0 : p.first) >> c.p_shift) + j;
+  const int64_t base = p.page << c.p_shift;
+  if (n == 0 || base >= len) return false;
+  p.lo = (int)((p.first > base ? p.first : base) - base);
+  p.hi = (int)((len < base + c.P ? len : base + c.P) - base);
+  p.row_lo = p.row0 + (base + p.lo - p.first);
+  return true;
+}
+
+__device__ __forceinline__ int64_t position_of(const AppendArgs& a, const Place& p, int64_t row) {
+  return a.positions ? (int64_t)a.positions[row] : row - p.row0 + p.first;
+}
+
+// Steps of a block before and after, and the factor for its older codes.
+struct Steps {
+  float k, v, k_by, v_by;
+  bool k_grew, v_grew;
+};
+
+__device__ __forceinline__ Steps steps_after(const Place& p, float k_was, float v_was, uint32_t km,
+                                             uint32_t vm) {
+  Steps s;
+  s.k = next_step(km, k_was);
+  s.v = next_step(vm, v_was);
+  s.k_grew = p.lo > 0 && s.k != k_was;
+  s.v_grew = p.lo > 0 && s.v != v_was;
+  s.k_by = k_was / s.k;
+  s.v_by = v_was / s.v;
+  return s;
+}
+
+// rot % 16 == 0 (or no table).  A workgroup takes a page and head's keys and values, or
+// the queries that share the head.  The turned keys and the values stay in
+// registers between the search for the largest and the rounding: HOLD units of
+// sixteen keys, or patches of four tokens by four columns of values, a thread.
+template <class TI, class TQ, int HOLD>
+__global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
+  typedef typename TI::storage SI;
+  typedef typename TQ::storage SQ;
+  __shared__ uint2 red[16];
+  const KvArgs& c = a.c;
+  int g = blockIdx.x;
+  const int h = g % c.Hkv;
+  g /= c.Hkv;
+  const int j = g % a.pages_per_seq;
+  g /= a.pages_per_seq;
+  const int b = g % c.B;
+  const bool queries = g >= c.B;
+  Place p;
+  if (!find_place(a, b, j, p)) return;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int units = units_of(c.D, a.rot), tokens = p.hi - p.lo, half = a.rot >> 1;
+
+  if (queries) {
+    const int G = a.Hq / c.Hkv;
+    for (int e = tid; e < tokens * G * units; e += threads) {
+      const int u = e % units, r = e / units, hq = h * G + r % G;
+      const int64_t row = p.row_lo + r / G;
+      const Unit w = unit_of(c.D, a.rot, a.interleaved, u);
+      const SI* x = (const SI*)a.q + row * a.qs[0] + hq * a.qs[1];
+      float x0[8], x1[8];
+      widen(load8(x + w.d0), x0);
+      widen(load8(x + (w.two ? w.d1 : w.d0)), x1);
+      if (w.turn)
+        turn_unit(x0, x1, turns_at(a.table, a.n_pos, half, position_of(a, p, row), u),
+                  a.interleaved, false);
+      SQ* y = (SQ*)a.q_out + (row * a.Hq + hq) * c.D;
+      store8(y + w.d0, x0);
+      if (w.two) store8(y + w.d1, x1);
+    }
+    return;
+  }
+
+  const int id = page_id(c, b, p.page);
+  if (id < 0) return;   // no such page: its tokens are not kept
+  const int64_t blk = (int64_t)id * c.Hkv + h;
+  const float k_was = p.lo > 0 ? c.k_steps[blk] : 0.0f, v_was = p.lo > 0 ? c.v_steps[blk] : 0.0f;
+
+  // patches of values: tokens 4 t .. 4 t + 3 of the page, columns 4 d .. 4 d + 3
+  const int t_lo = p.lo >> 2, t_n = ((p.hi + 3) >> 2) - t_lo, dq = c.D >> 2;
+  const SI* v_rows = (const SI*)a.v + h * a.vs[1];
+  SI v[HOLD][4][4];
+  uint32_t vm = 0;
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int e = tid + k * threads;
+    if (e < t_n * dq) {
+      const int d = e % dq, t = 4 * (t_lo + e / dq);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = t + i >= p.lo && t + i < p.hi;
+        const SI* x = v_rows + (p.row_lo + (in ? t + i - p.lo : 0)) * a.vs[0] + 4 * d;
+        const Four<SI> r = load4(x);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) v[k][i][m] = in ? r.v[m] : (SI)0.0f;
+      }
+    }
+  }
+  float x0[HOLD][8], x1[HOLD][8];
+  uint32_t km = 0;
+  const SI* k_rows = (const SI*)a.k + h * a.ks[1];
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int e = tid + k * threads;
+    if (e < tokens * units) {
+      const int u = e % units;
+      const int64_t row = p.row_lo + e / units;
+      const Unit w = unit_of(c.D, a.rot, a.interleaved, u);
+      const SI* x = k_rows + row * a.ks[0];
+      widen(load8(x + w.d0), x0[k]);
+      widen(load8(x + (w.two ? w.d1 : w.d0)), x1[k]);
+      if (w.turn)
+        turn_unit(x0[k], x1[k], turns_at(a.table, a.n_pos, half, position_of(a, p, row), u),
+                  a.interleaved, false);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) km = umax(km, umax(abs_bits(x0[k][i]), abs_bits(x1[k][i])));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (tid + k * threads < t_n * dq)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) vm = umax(vm, abs_bits(to_f32(v[k][i >> 2][i & 3])));
+  block_max(km, vm, red);
+  const Steps s = steps_after(p, k_was, v_was, km, vm);
+
+  uint8_t* kc = c.k_codes + blk * c.P * c.D;
+  uint8_t* vc = c.v_codes + blk * c.P * c.D;
+  if (s.k_grew) {
+    uint32_t* w = (uint32_t*)kc;
+    for (int e = tid; e < p.lo * dq; e += threads) w[e] = moved(w[e], s.k_by);
+  }
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int e = tid + k * threads;
+    if (e < tokens * units) {
+      const Unit w = unit_of(c.D, a.rot, a.interleaved, e % units);
+      uint8_t* y = kc + (p.lo + e / units) * c.D;
+      uint32_t r[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[i >> 2] |= coded(x0[k][i], s.k) << (8 * (i & 3));
+        r[2 + (i >> 2)] |= coded(x1[k][i], s.k) << (8 * (i & 3));
+      }
+      *(u32x2*)(y + w.d0) = u32x2{r[0], r[1]};
+      if (w.two) *(u32x2*)(y + w.d1) = u32x2{r[2], r[3]};
+    }
+  }
+  // values: older tokens of the block in the dwords before the first patch
+  if (s.v_grew) {
+    const int per = c.P >> 2;
+    for (int e = tid; e < c.D * t_lo; e += threads) {
+      uint32_t* w = (uint32_t*)vc + (e / t_lo) * per + e % t_lo;
+      *w = moved(*w, s.v_by);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int e = tid + k * threads;
+    if (e < t_n * dq) {
+      const int d = e % dq, t = 4 * (t_lo + e / dq);
+      const bool whole = t >= p.lo && t + 4 <= p.hi;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        uint32_t* y = (uint32_t*)(vc + (4 * d + m) * c.P + t);
+        uint32_t r = 0;
+        if (!whole) {   // older tokens of the patch, and places past the sequence's end
+          r = *y;
+          if (s.v_grew && t < p.lo) r = moved(r, s.v_by);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t + i >= p.lo && t + i < p.hi)
+            r = (r & ~(255u << (8 * i))) | coded(to_f32(v[k][i][m]), s.v) << (8 * i);
+        *y = r;
+      }
+    }
+  }
+  if (tid == 0) {
+    c.k_steps[blk] = s.k;
+    c.v_steps[blk] = s.v;
+  }
 }
 
 template <class S>
@@ -41,27 +262,22 @@ __device__ __forceinline__ void load_pair(const AppendArgs& a, const S* x, int64
   rotate(x1, x2, cs.x, cs.y);
 }
 
+// Any rot: pairs one by one, read twice.
 template <class TI, class TQ>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   typedef typename TI::storage SI;
   typedef typename TQ::storage SQ;
-  __shared__ uint32_t red[kThreads / 64];
+  __shared__ uint2 red[kThreads / 64];
   const KvArgs& c = a.c;
   int g = blockIdx.x;
   const int j = g % a.pages_per_seq;
   g /= a.pages_per_seq;
   const int h = g % c.Hkv, b = g / c.Hkv;
-  int64_t row0;
-  int n;
-  rows_of(c, b, row0, n);
-  const int64_t len = a.lens[b], first = len - n;   // places [first, len) are new
-  const int64_t p = ((first < 0 ? 0 : first) >> c.p_shift) + j;
-  const int64_t base = p << c.p_shift;
-  if (n == 0 || base >= len) return;
-  const int lo = (int)((first > base ? first : base) - base);       // first new place of the page
-  const int hi = (int)((len < base + c.P ? len : base + c.P) - base);
+  Place p;
+  if (!find_place(a, b, j, p)) return;
+  const int lo = p.lo, hi = p.hi;
+  const int64_t row_lo = p.row_lo;
   const int half = a.rot >> 1, units = half + (c.D - a.rot);
-  const int64_t row_lo = row0 + (base + lo - first);
   const int tid = threadIdx.x;
 
   if (a.q) {   // this page's rows of the queries that share this head
@@ -77,7 +293,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
         y[d] = from_f32<SQ>(to_f32(x[d]));
         continue;
       }
-      const int64_t pos = a.positions ? (int64_t)a.positions[row] : row - row0 + first;
+      const int64_t pos = position_of(a, p, row);
       int i1, i2;
       float x1, x2;
       load_pair(a, x, pos, u, i1, i2, x1, x2);
@@ -86,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
     }
   }
 
-  const int id = page_id(c, b, p);
+  const int id = page_id(c, b, p.page);
   if (id < 0) return;   // no such page: its tokens are not kept
   const int64_t blk = (int64_t)id * c.Hkv + h;
   uint8_t* kc = c.k_codes + blk * c.P * c.D;
@@ -100,37 +316,27 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
     const int64_t row = row_lo + r;
     const SI* x = (const SI*)a.k + row * a.ks[0] + h * a.ks[1];
     if (u >= half) {
-      const uint32_t m = abs_bits(to_f32(x[a.rot + (u - half)]));
-      km = km > m ? km : m;
+      km = umax(km, abs_bits(to_f32(x[a.rot + (u - half)])));
       continue;
     }
-    const int64_t pos = a.positions ? (int64_t)a.positions[row] : row - row0 + first;
+    const int64_t pos = position_of(a, p, row);
     int i1, i2;
     float x1, x2;
     load_pair(a, x, pos, u, i1, i2, x1, x2);
-    const uint32_t m1 = abs_bits(x1), m2 = abs_bits(x2);
-    km = km > m1 ? km : m1;
-    km = km > m2 ? km : m2;
+    km = umax(km, umax(abs_bits(x1), abs_bits(x2)));
   }
   for (int e = tid; e < (hi - lo) * c.D; e += kThreads) {
     const int d = e % c.D, r = e / c.D;
     const SI* x = (const SI*)a.v + (row_lo + r) * a.vs[0] + h * a.vs[1];
-    const uint32_t m = abs_bits(to_f32(x[d]));
-    vm = vm > m ? vm : m;
+    vm = umax(vm, abs_bits(to_f32(x[d])));
   }
-  km = block_max(km, red);
-  vm = block_max(vm, red);
-  // a NaN's bits are above every number's, so a NaN among the values gives a NaN step
-  const float kt = __uint_as_float(km) / 127.0f, vt = __uint_as_float(vm) / 127.0f;
-  const float k_step = __float_as_uint(kt) > __float_as_uint(k_was) ? kt : k_was;
-  const float v_step = __float_as_uint(vt) > __float_as_uint(v_was) ? vt : v_was;
-  const bool k_grew = old && k_step != k_was, v_grew = old && v_step != v_was;
+  block_max(km, vm, red);
+  const Steps s = steps_after(p, k_was, v_was, km, vm);
 
   // keys: older rows to the new step, then the new rows
-  if (k_grew) {
-    const float r = k_was / k_step;
+  if (s.k_grew) {
     for (int e = tid; e < lo * c.D; e += kThreads)
-      kc[e] = (uint8_t)(code_of((float)((int)kc[e] - 128) * r) + 128);
+      kc[e] = (uint8_t)(code_of((float)((int)kc[e] - 128) * s.k_by) + 128);
   }
   for (int e = tid; e < (hi - lo) * units; e += kThreads) {
     const int u = e % units, r = e / units;
@@ -139,41 +345,44 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
     uint8_t* y = kc + (int64_t)(lo + r) * c.D;
     if (u >= half) {
       const int d = a.rot + (u - half);
-      y[d] = (uint8_t)((k_step > 0.0f ? code_of(to_f32(x[d]) / k_step) : 0) + 128);
+      y[d] = (uint8_t)coded(to_f32(x[d]), s.k);
       continue;
     }
-    const int64_t pos = a.positions ? (int64_t)a.positions[row] : row - row0 + first;
+    const int64_t pos = position_of(a, p, row);
     int i1, i2;
     float x1, x2;
     load_pair(a, x, pos, u, i1, i2, x1, x2);
-    y[i1] = (uint8_t)((k_step > 0.0f ? code_of(x1 / k_step) : 0) + 128);
-    y[i2] = (uint8_t)((k_step > 0.0f ? code_of(x2 / k_step) : 0) + 128);
+    y[i1] = (uint8_t)coded(x1, s.k);
+    y[i2] = (uint8_t)coded(x2, s.k);
   }
   // values: a row of the block is one column of the tokens
   for (int e = tid; e < c.D * hi; e += kThreads) {
     const int d = e % c.D, t = e / c.D;
     uint8_t* y = vc + (int64_t)d * c.P + t;
     if (t < lo) {
-      if (v_grew) *y = (uint8_t)(code_of((float)((int)*y - 128) * (v_was / v_step)) + 128);
+      if (s.v_grew) *y = (uint8_t)(code_of((float)((int)*y - 128) * s.v_by) + 128);
     } else {
       const SI* x = (const SI*)a.v + (row_lo + (t - lo)) * a.vs[0] + h * a.vs[1];
-      *y = (uint8_t)((v_step > 0.0f ? code_of(to_f32(x[d]) / v_step) : 0) + 128);
+      *y = (uint8_t)coded(to_f32(x[d]), s.v);
     }
   }
   if (tid == 0) {
-    c.k_steps[blk] = k_step;
-    c.v_steps[blk] = v_step;
+    c.k_steps[blk] = s.k;
+    c.v_steps[blk] = s.v;
   }
 }
 
+// A thread takes four tokens by eight columns.  The values' four tokens are one
+// dword of a column, so eight dwords and no transposition give four rows of
+// eight; a workgroup runs over the heads of a page.
 template <class TO>
-__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
+__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) {
   typedef typename TO::storage SO;
   const KvArgs& c = a.c;
   int g = blockIdx.x;
-  const int j = g % a.pages_per_seq;
-  g /= a.pages_per_seq;
-  const int h = g % c.Hkv, b = g / c.Hkv;
+  const int part = g % blocks;
+  g /= blocks;
+  const int j = g % a.pages_per_seq, b = g / a.pages_per_seq;
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
@@ -182,25 +391,67 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
   if (n == 0 || base >= end) return;
   const int lo = (int)((first > base ? first : base) - base);
   const int hi = (int)((end < base + c.P ? end : base + c.P) - base);
+  const int d8 = c.D >> 3, t4 = c.P >> 2;
+  const int e = part * kThreads + threadIdx.x;
+  const int h = e / (d8 * t4);
+  const int t = 4 * (e / d8 % t4), d = 8 * (e % d8);
+  if (h >= c.Hkv || t >= hi || t + 4 <= lo) return;
   const int id = page_id(c, b, p);
   const int64_t blk = (int64_t)(id < 0 ? 0 : id) * c.Hkv + h;
-  const uint8_t* kc = c.k_codes + blk * c.P * c.D;
-  const uint8_t* vc = c.v_codes + blk * c.P * c.D;
+  const uint8_t* kc = c.k_codes + (blk * c.P + t) * c.D + d;
+  const uint8_t* vc = c.v_codes + (blk * c.D + d) * c.P + t;
   const float ks = c.k_steps[blk], vs = c.v_steps[blk];
-  for (int e = threadIdx.x; e < (hi - lo) * c.D; e += kThreads) {
-    const int d = e % c.D, t = lo + e / c.D;
-    const int64_t o = ((row0 + (base + t - first)) * c.Hkv + h) * c.D + d;
-    ((SO*)a.k_out)[o] = from_f32<SO>(id < 0 ? 0.0f : fp32_value((float)((int)kc[(int64_t)t * c.D + d] - 128) * ks));
-    ((SO*)a.v_out)[o] = from_f32<SO>(id < 0 ? 0.0f : fp32_value((float)((int)vc[(int64_t)d * c.P + t] - 128) * vs));
+  u32x2 k[4];
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k[i] = *(const u32x2*)(kc + i * c.D);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = *(const uint32_t*)(vc + i * c.P);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (t + i < lo || t + i >= hi) continue;
+    float x[8], y[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const uint32_t w = k[i][m >> 2];
+      x[m] = id < 0 ? 0.0f : fp32_value((float)((int)((w >> (8 * (m & 3))) & 255) - 128) * ks);
+      y[m] = id < 0 ? 0.0f : fp32_value((float)((int)((v[m] >> (8 * i)) & 255) - 128) * vs);
+    }
+    const int64_t o = ((row0 + (base + t + i - first)) * c.Hkv + h) * c.D + d;
+    store8((SO*)a.k_out + o, x);
+    store8((SO*)a.v_out + o, y);
+  }
+}
+
+template <class TI, class TQ>
+void go_append(const AppendArgs& a, hipStream_t st) {
+  const int64_t grid = (int64_t)a.pages_per_seq * a.c.Hkv * a.c.B;
+  if (a.rot % 16 != 0) {
+    append_kernel<TI, TQ><<<(unsigned)grid, kThreads, 0, st>>>(a);
+    return;
+  }
+  // as many threads as hold a page's new tokens: two units or patches each, four where
+  // a page has more than 2 x 1024 (256 tokens of more than 128 columns)
+  const int64_t tokens = a.max_new < a.c.P ? a.max_new : a.c.P;
+  const int64_t quads = (tokens + 6) / 4 < a.c.P / 4 ? (tokens + 6) / 4 : a.c.P / 4;
+  const int64_t k_items = tokens * units_of(a.c.D, a.rot), v_items = quads * (a.c.D / 4);
+  const int64_t items = k_items > v_items ? k_items : v_items;
+  const unsigned blocks = (unsigned)(a.q ? 2 * grid : grid);
+  if (items <= 2048) {
+    // one token: enough threads for all of it at once
+    const int threads = a.max_new == 1 ? 128 : (int)((items + 1) / 2 + 63) / 64 * 64;
+    append_units_kernel<TI, TQ, 2><<<blocks, threads, 0, st>>>(a);
+  } else {
+    append_units_kernel<TI, TQ, 4><<<blocks, 1024, 0, st>>>(a);
   }
 }
 
 template <class TI>
-hipError_t go_append(const AppendArgs& a, awq_dtype_t q_out, unsigned grid, hipStream_t st) {
+hipError_t go_append_q(const AppendArgs& a, awq_dtype_t q_out, hipStream_t st) {
   ProfScope prof("awq_kv_append", st);
-  if (q_out == AWQ_F32) append_kernel<TI, F32T><<<grid, kThreads, 0, st>>>(a);
-  else if (q_out == AWQ_F16) append_kernel<TI, F16T><<<grid, kThreads, 0, st>>>(a);
-  else append_kernel<TI, BF16T><<<grid, kThreads, 0, st>>>(a);
+  if (q_out == AWQ_F32) go_append<TI, F32T>(a, st);
+  else if (q_out == AWQ_F16) go_append<TI, F16T>(a, st);
+  else go_append<TI, BF16T>(a, st);
   return hipGetLastError();
 }
 
@@ -208,18 +459,18 @@ hipError_t go_append(const AppendArgs& a, awq_dtype_t q_out, unsigned grid, hipS
 
 hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, awq_dtype_t q_out,
                             hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.pages_per_seq * a.c.Hkv * a.c.B);
-  if (in == AWQ_F32) return go_append<F32T>(a, q_out, grid, st);
-  if (in == AWQ_F16) return go_append<F16T>(a, q_out, grid, st);
-  return go_append<BF16T>(a, q_out, grid, st);
+  if (in == AWQ_F32) return go_append_q<F32T>(a, q_out, st);
+  if (in == AWQ_F16) return go_append_q<F16T>(a, q_out, st);
+  return go_append_q<BF16T>(a, q_out, st);
 }
 
 hipError_t launch_kv_read(const ReadArgs& a, awq_dtype_t out, hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.pages_per_seq * a.c.Hkv * a.c.B);
+  const int blocks = (int)(((int64_t)a.c.Hkv * (a.c.P / 4) * (a.c.D / 8) + kThreads - 1) / kThreads);
+  const unsigned grid = (unsigned)((int64_t)a.pages_per_seq * blocks * a.c.B);
   ProfScope prof("awq_kv_read", st);
-  if (out == AWQ_F32) read_kernel<F32T><<<grid, kThreads, 0, st>>>(a);
-  else if (out == AWQ_F16) read_kernel<F16T><<<grid, kThreads, 0, st>>>(a);
-  else read_kernel<BF16T><<<grid, kThreads, 0, st>>>(a);
+  if (out == AWQ_F32) read_kernel<F32T><<<grid, kThreads, 0, st>>>(a, blocks);
+  else if (out == AWQ_F16) read_kernel<F16T><<<grid, kThreads, 0, st>>>(a, blocks);
+  else read_kernel<BF16T><<<grid, kThreads, 0, st>>>(a, blocks);
   return hipGetLastError();
 }
 

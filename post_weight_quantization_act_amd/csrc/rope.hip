@@ -24,6 +24,58 @@ __global__ __launch_bounds__(256) void rope_table_kernel(int64_t n_pos, int half
   table[e] = make_float2((float)(c * fr.magnitude), (float)(s * fr.magnitude));
 }
 
+// rot % 16 == 0: a thread takes one unit of HB heads of a row, so that the row's
+// cosines and sines are read once for them and HB heads' loads are in flight.
+template <class TI, class TO, int HB>
+__global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int rows_per_block) {
+  typedef typename TI::storage SI;
+  typedef typename TO::storage SO;
+  const int units = units_of(a.D, a.rot);
+  const int blocks = (int)((a.H + HB - 1) / HB);
+  const uint32_t work = (uint32_t)units * (uint32_t)blocks;     // threads' items of a row
+  const uint32_t per_row = work < 256 ? work : 256;
+  const uint32_t r = threadIdx.x / per_row;
+  const int64_t row = (int64_t)blockIdx.x * rows_per_block + r;
+  if ((int)r >= rows_per_block || row >= a.B * a.S) return;
+  int64_t b, s;
+  if ((uint64_t)(a.B * a.S) >> 32) {
+    b = row / a.S;
+    s = row % a.S;
+  } else {
+    b = (uint32_t)row / (uint32_t)a.S;
+    s = (uint32_t)row % (uint32_t)a.S;
+  }
+  const SI* xr = (const SI*)a.x + b * a.xs[0] + s * a.xs[1];
+  SO* yr = (SO*)a.out + b * a.os[0] + s * a.os[1];
+  const int64_t pos = a.positions ? (int64_t)a.positions[b * a.pos_stride + s] : s;
+  for (uint32_t e = threadIdx.x % per_row; e < work; e += per_row) {
+    const int u = (int)(e % (uint32_t)units);
+    const int64_t h0 = (int64_t)(e / (uint32_t)units) * HB;
+    const Unit c = unit_of(a.D, a.rot, a.interleaved, u);
+    Eight<SI> m0[HB], m1[HB];
+#pragma unroll
+    for (int k = 0; k < HB; ++k) {
+      const int64_t h = h0 + k < a.H ? h0 + k : h0;
+      m0[k] = load8(xr + h * a.xs[2] + c.d0);
+      m1[k] = load8(xr + h * a.xs[2] + (c.two ? c.d1 : c.d0));
+    }
+    Turns t;
+    if (c.turn) t = turns_at(a.table, a.n_pos, a.rot >> 1, pos, u);
+#pragma unroll
+    for (int k = 0; k < HB; ++k) {
+      if (h0 + k >= a.H) break;
+      float x0[8], x1[8];
+      widen(m0[k], x0);
+      widen(m1[k], x1);
+      if (c.turn) turn_unit(x0, x1, t, a.interleaved, a.transpose);
+      SO* y = yr + (h0 + k) * a.os[2];
+      store8(y + c.d0, x0);
+      if (c.two) store8(y + c.d1, x1);
+    }
+  }
+}
+
+// Any rot: one pair, or one column that is left as it is, a thread.
 template <class TI, class TO>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   typedef typename TI::storage SI;
@@ -53,11 +105,25 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   y[i2] = from_f32<SO>(x2);
 }
 
+template <class TI, class TO, int HB>
+void go_units(const RopeArgs& a, hipStream_t st) {
+  const int64_t work = (int64_t)units_of(a.D, a.rot) * ((a.H + HB - 1) / HB);
+  const int rows = work < 256 ? (int)(256 / work) : 1;
+  const int64_t blocks = (a.B * a.S + rows - 1) / rows;
+  rope_units_kernel<TI, TO, HB><<<(unsigned)blocks, 256, 0, st>>>(a, rows);
+}
+
 template <class TI, class TO>
 hipError_t go(const RopeArgs& a, hipStream_t st) {
-  const int64_t n = a.B * a.S * a.H * (a.rot / 2 + a.D - a.rot);
   ProfScope prof("awq_rope", st);
-  rope_kernel<TI, TO><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+  if (a.rot % 16 == 0 && a.D % 8 == 0) {
+    // four heads a thread once one head a thread would make more threads than run at a time
+    if (a.B * a.S * a.H * units_of(a.D, a.rot) >= 4 * 256 * 2048) go_units<TI, TO, 4>(a, st);
+    else go_units<TI, TO, 1>(a, st);
+  } else {
+    const int64_t n = a.B * a.S * a.H * (a.rot / 2 + a.D - a.rot);
+    rope_kernel<TI, TO><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 
