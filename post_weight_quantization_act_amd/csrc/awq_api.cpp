@@ -197,7 +197,7 @@ awq_status_t kv_args(const awq_kv_cache_t* cache, int64_t T, const int32_t* star
     if (!aligned(pages, 4) || !aligned(starts, 4))
       return fail(AWQ_ERR_UNSUPPORTED, "pages and starts must be 4-byte aligned");
     const int64_t pps = (max_new + cache->page - 2) / cache->page + 1;
-    if (B > kMaxGrid / (pps * cache->kv_heads))
+    if (B > kMaxGrid / 4 / (pps * cache->kv_heads))   // queries double it, and eights round it up
       return fail(AWQ_ERR_UNSUPPORTED, "too many sequences, heads and pages for one launch");
   }
   a->k_codes = cache->k_codes;

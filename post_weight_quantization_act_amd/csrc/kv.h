@@ -209,6 +209,7 @@ struct AppendArgs {
   int64_t ks[2], vs[2], qs[2];   // strides over rows and heads in elements
   int64_t n_pos;
   int rot, interleaved, Hq, pages_per_seq, max_new;
+  int kv_blocks, q_parts;        // the launch's own
 };
 
 struct ReadArgs {

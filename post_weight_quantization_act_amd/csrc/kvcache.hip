@@ -44,6 +44,34 @@ __device__ __forceinline__ uint32_t coded(float x, float step) {
   return (uint32_t)((step > 0.0f ? code_of(x / step) : 0) + 128);
 }
 
+// The codes of a block's new values.  A step that is a number bounds the values by
+// about 127 of it, so none is NaN and the quotient comes from the step's reciprocal
+// (correctly rounded, five operations against eleven); a step of 0, or one that is not
+// finite, makes every code 0, as the definition does.  Clamped, a quotient plus
+// 2^23 + 128 is rounded to the nearest integer, ties to even, and its lowest byte is
+// the stored code.
+struct Coder {
+  float step, inverse;
+  bool plain;      // the reciprocal and the remainders are normal numbers
+  bool none;
+
+  __device__ __forceinline__ explicit Coder(float s) : step(s), inverse(1.0f / s) {
+    plain = s >= 0x1p-100f && s <= 0x1p100f;
+    none = !(s > 0.0f && s < INFINITY);
+  }
+  __device__ __forceinline__ uint32_t four(float a, float b, float c, float d) const {
+    if (none) return 0x80808080u;
+    if (!plain)
+      return coded(a, step) | coded(b, step) << 8 | coded(c, step) << 16 | coded(d, step) << 24;
+    const uint32_t lo = __builtin_amdgcn_perm(bits(b), bits(a), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(bits(d), bits(c), 0x04000c0cu);
+    return lo | hi;
+  }
+  __device__ __forceinline__ uint32_t bits(float x) const {
+    return __float_as_uint(__builtin_amdgcn_fmed3f(div_rn(x, step, inverse), -127.0f, 127.0f) + 8388736.0f);
+  }
+};
+
 // Codes of one dword to a step `by` times as coarse.
 __device__ __forceinline__ uint32_t moved(uint32_t w, float by) {
   uint32_t r = 0;
@@ -98,32 +126,37 @@ __device__ __forceinline__ Steps steps_after(const Place& p, float k_was, float 
 }
 
 // rot % 16 == 0 (or no table).  A workgroup takes a page and head's keys and values, or
-// the queries that share the head.  The turned keys and the values stay in
-// registers between the search for the largest and the rounding: HOLD units of
-// sixteen keys, or patches of four tokens by four columns of values, a thread.
+// (blocks from a.kv_blocks on) a part of the queries of a page's tokens.  The turned
+// keys and the values stay in registers between the search for the largest and the
+// rounding: HOLD units of sixteen keys, or patches of four tokens by four columns of
+// values, a thread.
+//
+// Workgroups are dealt to the eight XCDs in turn: page number modulo 8 is the lowest
+// digit, so the heads of a page, which turn by the same rows of the table, share an L2.
 template <class TI, class TQ, int HOLD>
 __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   typedef typename TI::storage SI;
   typedef typename TQ::storage SQ;
   __shared__ uint2 red[16];
   const KvArgs& c = a.c;
-  int g = blockIdx.x;
-  const int h = g % c.Hkv;
-  g /= c.Hkv;
-  const int j = g % a.pages_per_seq;
-  g /= a.pages_per_seq;
-  const int b = g % c.B;
-  const bool queries = g >= c.B;
+  const bool queries = (int)blockIdx.x >= a.kv_blocks;
+  uint32_t g = queries ? blockIdx.x - a.kv_blocks : blockIdx.x;
+  const uint32_t fan = queries ? a.q_parts : c.Hkv, low = g & 7;
+  g >>= 3;
+  const int h = (int)(g % fan);       // or the part of the queries
+  const uint32_t at = g / fan * 8 + low;
+  if (at >= (uint32_t)c.B * (uint32_t)a.pages_per_seq) return;
+  const int j = (int)(at % (uint32_t)a.pages_per_seq), b = (int)(at / (uint32_t)a.pages_per_seq);
   Place p;
   if (!find_place(a, b, j, p)) return;
   const int tid = threadIdx.x, threads = blockDim.x;
   const int units = units_of(c.D, a.rot), tokens = p.hi - p.lo, half = a.rot >> 1;
 
   if (queries) {
-    const int G = a.Hq / c.Hkv;
-    for (int e = tid; e < tokens * G * units; e += threads) {
-      const int u = e % units, r = e / units, hq = h * G + r % G;
-      const int64_t row = p.row_lo + r / G;
+    const int work = tokens * a.Hq * units;
+    for (int e = h * threads + tid; e < work; e += a.q_parts * threads) {
+      const int u = e % units, r = e / units, hq = r % a.Hq;
+      const int64_t row = p.row_lo + r / a.Hq;
       const Unit w = unit_of(c.D, a.rot, a.interleaved, u);
       const SI* x = (const SI*)a.q + row * a.qs[0] + hq * a.qs[1];
       float x0[8], x1[8];
@@ -144,7 +177,8 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   const int64_t blk = (int64_t)id * c.Hkv + h;
   const float k_was = p.lo > 0 ? c.k_steps[blk] : 0.0f, v_was = p.lo > 0 ? c.v_steps[blk] : 0.0f;
 
-  // patches of values: tokens 4 t .. 4 t + 3 of the page, columns 4 d .. 4 d + 3
+  // patches of values: tokens 4 t .. 4 t + 3 of the page, columns 4 d .. 4 d + 3, neighbours
+  // along the tokens, so that a column's codes leave as one run
   const int t_lo = p.lo >> 2, t_n = ((p.hi + 3) >> 2) - t_lo, dq = c.D >> 2;
   const SI* v_rows = (const SI*)a.v + h * a.vs[1];
   SI v[HOLD][4][4];
@@ -153,7 +187,7 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   for (int k = 0; k < HOLD; ++k) {
     const int e = tid + k * threads;
     if (e < t_n * dq) {
-      const int d = e % dq, t = 4 * (t_lo + e / dq);
+      const int d = e / t_n, t = 4 * (t_lo + e % t_n);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool in = t + i >= p.lo && t + i < p.hi;
@@ -191,6 +225,7 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
       for (int i = 0; i < 16; ++i) vm = umax(vm, abs_bits(to_f32(v[k][i >> 2][i & 3])));
   block_max(km, vm, red);
   const Steps s = steps_after(p, k_was, v_was, km, vm);
+  const Coder key(s.k), value(s.v);
 
   uint8_t* kc = c.k_codes + blk * c.P * c.D;
   uint8_t* vc = c.v_codes + blk * c.P * c.D;
@@ -204,14 +239,10 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
     if (e < tokens * units) {
       const Unit w = unit_of(c.D, a.rot, a.interleaved, e % units);
       uint8_t* y = kc + (p.lo + e / units) * c.D;
-      uint32_t r[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r[i >> 2] |= coded(x0[k][i], s.k) << (8 * (i & 3));
-        r[2 + (i >> 2)] |= coded(x1[k][i], s.k) << (8 * (i & 3));
-      }
-      *(u32x2*)(y + w.d0) = u32x2{r[0], r[1]};
-      if (w.two) *(u32x2*)(y + w.d1) = u32x2{r[2], r[3]};
+      const float *m = x0[k], *n = x1[k];
+      *(u32x2*)(y + w.d0) = u32x2{key.four(m[0], m[1], m[2], m[3]), key.four(m[4], m[5], m[6], m[7])};
+      if (w.two)
+        *(u32x2*)(y + w.d1) = u32x2{key.four(n[0], n[1], n[2], n[3]), key.four(n[4], n[5], n[6], n[7])};
     }
   }
   // values: older tokens of the block in the dwords before the first patch
@@ -226,21 +257,24 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   for (int k = 0; k < HOLD; ++k) {
     const int e = tid + k * threads;
     if (e < t_n * dq) {
-      const int d = e % dq, t = 4 * (t_lo + e / dq);
+      const int d = e / t_n, t = 4 * (t_lo + e % t_n);
       const bool whole = t >= p.lo && t + 4 <= p.hi;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        uint32_t* y = (uint32_t*)(vc + (4 * d + m) * c.P + t);
-        uint32_t r = 0;
-        if (!whole) {   // older tokens of the patch, and places past the sequence's end
-          r = *y;
-          if (s.v_grew && t < p.lo) r = moved(r, s.v_by);
+        uint8_t* y = vc + (4 * d + m) * c.P + t;
+        const uint32_t r = value.four(to_f32(v[k][0][m]), to_f32(v[k][1][m]), to_f32(v[k][2][m]),
+                                      to_f32(v[k][3][m]));
+        if (whole) {
+          *(uint32_t*)y = r;
+          continue;
         }
+        // a patch that the new tokens fill in part: older tokens before, nobody's places after
+        const uint32_t old = s.v_grew && t < p.lo ? moved(*(const uint32_t*)y, s.v_by) : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t + i >= p.lo && t + i < p.hi)
-            r = (r & ~(255u << (8 * i))) | coded(to_f32(v[k][i][m]), s.v) << (8 * i);
-        *y = r;
+        for (int i = 0; i < 4; ++i) {
+          if (t + i >= p.lo && t + i < p.hi) y[i] = (uint8_t)(r >> (8 * i));
+          else if (s.v_grew && t + i < p.lo) y[i] = (uint8_t)(old >> (8 * i));
+        }
       }
     }
   }
@@ -414,8 +448,8 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) 
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
       const uint32_t w = k[i][m >> 2];
-      x[m] = id < 0 ? 0.0f : fp32_value((float)((int)((w >> (8 * (m & 3))) & 255) - 128) * ks);
-      y[m] = id < 0 ? 0.0f : fp32_value((float)((int)((v[m] >> (8 * i)) & 255) - 128) * vs);
+      x[m] = id < 0 ? 0.0f : fp32_value(((float)((w >> (8 * (m & 3))) & 255) - 128.0f) * ks);
+      y[m] = id < 0 ? 0.0f : fp32_value(((float)((v[m] >> (8 * i)) & 255) - 128.0f) * vs);
     }
     const int64_t o = ((row0 + (base + t + i - first)) * c.Hkv + h) * c.D + d;
     store8((SO*)a.k_out + o, x);
@@ -424,26 +458,28 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) 
 }
 
 template <class TI, class TQ>
-void go_append(const AppendArgs& a, hipStream_t st) {
-  const int64_t grid = (int64_t)a.pages_per_seq * a.c.Hkv * a.c.B;
+void go_append(AppendArgs a, hipStream_t st) {
+  const int64_t pages = (int64_t)a.pages_per_seq * a.c.B;
   if (a.rot % 16 != 0) {
-    append_kernel<TI, TQ><<<(unsigned)grid, kThreads, 0, st>>>(a);
+    append_kernel<TI, TQ><<<(unsigned)(pages * a.c.Hkv), kThreads, 0, st>>>(a);
     return;
   }
   // as many threads as hold a page's new tokens: two units or patches each, four where
   // a page has more than 2 x 1024 (256 tokens of more than 128 columns)
   const int64_t tokens = a.max_new < a.c.P ? a.max_new : a.c.P;
   const int64_t quads = (tokens + 6) / 4 < a.c.P / 4 ? (tokens + 6) / 4 : a.c.P / 4;
-  const int64_t k_items = tokens * units_of(a.c.D, a.rot), v_items = quads * (a.c.D / 4);
+  const int64_t units = units_of(a.c.D, a.rot);
+  const int64_t k_items = tokens * units, v_items = quads * (a.c.D / 4);
   const int64_t items = k_items > v_items ? k_items : v_items;
-  const unsigned blocks = (unsigned)(a.q ? 2 * grid : grid);
-  if (items <= 2048) {
-    // one token: enough threads for all of it at once
-    const int threads = a.max_new == 1 ? 128 : (int)((items + 1) / 2 + 63) / 64 * 64;
-    append_units_kernel<TI, TQ, 2><<<blocks, threads, 0, st>>>(a);
-  } else {
-    append_units_kernel<TI, TQ, 4><<<blocks, 1024, 0, st>>>(a);
-  }
+  const int threads = items > 2048 ? 1024 : (int)((items + 1) / 2 + 63) / 64 * 64;
+  const int64_t eights = (pages + 7) / 8;
+  a.kv_blocks = (int)(eights * a.c.Hkv * 8);
+  a.q_parts = (int)((tokens * a.Hq * units + 4 * threads - 1) / (4 * threads));   // four units a thread
+  if (a.q_parts > a.c.Hkv) a.q_parts = a.c.Hkv;
+  const unsigned blocks = (unsigned)(a.kv_blocks + eights * a.q_parts * 8);
+  if (items <= threads) append_units_kernel<TI, TQ, 1><<<blocks, threads, 0, st>>>(a);   // one token
+  else if (items <= 2048) append_units_kernel<TI, TQ, 2><<<blocks, threads, 0, st>>>(a);
+  else append_units_kernel<TI, TQ, 4><<<blocks, threads, 0, st>>>(a);
 }
 
 template <class TI>
