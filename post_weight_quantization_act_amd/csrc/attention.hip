@@ -68,6 +68,12 @@ __device__ __forceinline__ half8 surplus(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(half8, r);
 }
 
+// Eight codes as fp16 values u - 128.
+__device__ __forceinline__ half8 centred(uint32_t lo, uint32_t hi) {
+  const half8 less = {1152, 1152, 1152, 1152, 1152, 1152, 1152, 1152};
+  return surplus(lo, hi) - less;
+}
+
 // One row tile's queries, bounds and running state.
 template <int DB>
 struct Rows {
@@ -129,6 +135,74 @@ __device__ __forceinline__ void load_rows(const AttArgs& a, Rows<DB>& w, int64_t
     }
   w.bias = -1152.0f * xor_sum(sum);
   w.f = ldexpf(a.scale * kLog2e, e);
+}
+
+// The steps of a lane's sixteen tokens.  One that is not finite is NaN for everything
+// that its block touches.
+struct Steps {
+  float ks, log_sv, inv_sv;
+  bool zero, there;    // a value step of 0 weighs in the sum and adds nothing
+
+  __device__ __forceinline__ Steps(float k, float v, int page) {
+    ks = k + (k - k);
+    v += v - v;
+    zero = v < kLeastStep;
+    v = zero ? kLeastStep : v;
+    log_sv = __builtin_amdgcn_logf(v);
+    inv_sv = __builtin_amdgcn_rcpf(v);
+    there = page != 0;
+  }
+};
+
+// Scores of a row tile to probabilities: lane 16 g + q holds row q and tokens tok ..
+// tok + 15, score 4 i + j of them in s[i][j].  The reference follows the largest and
+// takes what has been summed with it.
+template <int DB>
+__device__ __forceinline__ void probabilities(Rows<DB>& r, f32x4 (&s)[4], half8 (&p)[2],
+                                              const Steps& st, int tok) {
+  // a row that sees none of the lane's tokens takes nothing from their block, NaN or not
+  const bool some = st.there && r.lo < tok + 16 && tok < r.hi;
+  const bool whole = st.there && r.lo <= tok && tok + 16 <= r.hi;
+  const float f = some ? r.f * st.ks : 1.0f, lg = some ? st.log_sv : 0.0f;
+  if (__any(!whole)) {
+    const uint32_t from = (uint32_t)(tok - r.lo), span = some ? (uint32_t)(r.hi - r.lo) : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s[i][j] = from + (uint32_t)(4 * i + j) < span ? s[i][j] : -INFINITY;
+  }
+  float top = s[0][0];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = fmaxf(top, s[i][j]);
+  // a factor of 0 would make NaN of the -inf of tokens that are not seen
+  const float fp = f < kLeastFactor ? kLeastFactor : f;
+  top = xor_max(top * fp + lg);
+  if (__any(top > r.r + kTop)) {
+    const float to = top > r.r + kTop ? top - kRest : r.r;
+    const float by = to == r.r ? 1.0f : __builtin_amdgcn_exp2f(r.r - to);
+    r.r = to;
+    r.l *= by;
+#pragma unroll
+    for (int dt = 0; dt < 2 * DB; ++dt) r.o[dt] *= by;
+  }
+  const float off = lg - (r.r == -INFINITY ? 0.0f : r.r);
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float e = __builtin_amdgcn_exp2f(fmaf(s[i][j], fp, off));
+      sum += e;
+      p[i >> 1][4 * (i & 1) + j] = (_Float16)e;
+    }
+  if (__any(st.zero)) {
+    p[0] = st.zero ? half8{} : p[0];
+    p[1] = st.zero ? half8{} : p[1];
+  }
+  r.l += some ? sum * st.inv_sv : 0.0f;
 }
 
 // The codes and steps of one 64-token tile on their way in.
@@ -256,71 +330,19 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
           s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w[qt].q[ks], s[qt][i], 0, 0, 0);
       }
     }
-    // a step that is not finite is NaN for everything that its block touches
-    const float ks = kt.ks + (kt.ks - kt.ks);
-    float sv = kt.sv + (kt.sv - kt.sv);
-    const bool zero = sv < kLeastStep;   // weighs in the sum, adds nothing
-    sv = zero ? kLeastStep : sv;
-    const int there = kt.there;
+    const Steps st(kt.ks, kt.sv, kt.there);
     const int tok = tile * kTile + 16 * g;
     if (tile + NW < s1) {
       id = next;
       load_keys<DB, W16>(a, kt, id, h, tile + NW, lane);
       next = tile_ids(a, b, tile + 2 * NW, lane);
     }
-    const float lsv = __builtin_amdgcn_logf(sv), rsv = __builtin_amdgcn_rcpf(sv);
     half8 p[QT][2];
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      Rows<DB>& r = w[qt];
-      // a row that sees none of the lane's tokens takes nothing from their block, NaN or not
-      const bool some = there && r.lo < tok + 16 && tok < r.hi;
-      const bool whole = there && r.lo <= tok && tok + 16 <= r.hi;
-      const float f = some ? r.f * ks : 1.0f, lg = some ? lsv : 0.0f;
-      if (__any(!whole)) {
-        const uint32_t from = (uint32_t)(tok - r.lo), span = some ? (uint32_t)(r.hi - r.lo) : 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s[qt][i][j] = from + (uint32_t)(4 * i + j) < span ? s[qt][i][j] : -INFINITY;
-      }
-      float top = s[qt][0][0];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = fmaxf(top, s[qt][i][j]);
-      // a factor of 0 would make NaN of the -inf of tokens that are not seen
-      const float fp = f < kLeastFactor ? kLeastFactor : f;
-      top = xor_max(top * fp + lg);
-      if (__any(top > r.r + kTop)) {
-        const float to = top > r.r + kTop ? top - kRest : r.r;
-        const float by = to == r.r ? 1.0f : __builtin_amdgcn_exp2f(r.r - to);
-        r.r = to;
-        r.l *= by;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) r.o[dt] *= by;
-      }
-      const float off = lg - (r.r == -INFINITY ? 0.0f : r.r);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(s[qt][i][j], fp, off));
-          sum += e;
-          p[qt][i >> 1][4 * (i & 1) + j] = (_Float16)e;
-        }
-      if (__any(zero)) {
-        p[qt][0] = zero ? half8{} : p[qt][0];
-        p[qt][1] = zero ? half8{} : p[qt][1];
-      }
-      r.l += some ? sum * rsv : 0.0f;
-    }
+    for (int qt = 0; qt < QT; ++qt) probabilities<DB>(w[qt], s[qt], p[qt], st, tok);
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
-      const half8 less = {1152, 1152, 1152, 1152, 1152, 1152, 1152, 1152};
-      const half8 v0 = surplus(v[dt][0], v[dt][1]) - less, v1 = surplus(v[dt][2], v[dt][3]) - less;
+      const half8 v0 = centred(v[dt][0], v[dt][1]), v1 = centred(v[dt][2], v[dt][3]);
 #pragma unroll
       for (int qt = 0; qt < QT; ++qt) {
         w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[qt][0], w[qt].o[dt], 0, 0, 0);
@@ -366,6 +388,178 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
       const int64_t part = split * c.T * a.Hq + out;
       *(f32x4*)(sp.o + part * c.D + d) = o;
       if (d == 0) sp.rl[part] = make_float2(top, l);
+    }
+  }
+}
+
+// Many rows: NW waves of 32 rows each share every tile, which is turned into fp16
+// fragments in LDS once for all of them; two buffers and one barrier a tile.  Each wave
+// fetches its part of the codes a tile ahead into registers.
+template <class T, int DB, int NW, bool W16>
+__global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel(AttArgs a, Split sp) {
+  typedef typename T::storage S;
+  constexpr int QT = 2, DT = 2 * DB;
+  constexpr int KU = W16 ? 2 * DB : 4 * DB;                     // parts of a tile's keys: 1 KB or 512 bytes each
+  constexpr int KN = (KU + NW - 1) / NW, VN = (DT + NW - 1) / NW;   // parts of a wave
+  __shared__ half8 kf[2][4 * DB][64], vf[2][2 * DT][64];
+  const KvArgs& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, g = lane >> 4;
+
+  int bid = blockIdx.x;
+  const int h = bid % c.Hkv;
+  bid /= c.Hkv;
+  const int b = bid % c.B;
+  bid /= c.B;
+  const int split = bid / sp.row_tiles, rt = sp.row_tiles - 1 - bid % sp.row_tiles;   // the longest first
+  int64_t row0;
+  int n;
+  rows_of(c, b, row0, n);
+  n = n < a.max_new ? n : a.max_new;
+  const int G = a.Hq / c.Hkv, base = rt * 32 * NW, rows = n * G;
+  if (base >= rows) return;
+  const int len = a.lens[b];
+  int lo, hi, unused;
+  seen_by(a, len, n, base / G, lo, unused);
+  seen_by(a, len, n, (base + 32 * NW < rows ? base + 32 * NW - 1 : rows - 1) / G, unused, hi);
+  const int t0 = lo / kTile, nt = hi > lo ? (hi + kTile - 1) / kTile - t0 : 0;
+  const int s0 = t0 + split * sp.tiles;
+  const int s1 = s0 + sp.tiles < t0 + nt ? s0 + sp.tiles : t0 + nt;
+  if (split > 0 && s0 >= s1) return;
+  const bool alone = nt <= sp.tiles;
+  const int mine = base + 32 * wave;     // this wave's first row, and the tokens that its rows see
+  int w_lo = 0, w_hi = 0;
+  if (mine < rows) {
+    seen_by(a, len, n, mine / G, w_lo, unused);
+    seen_by(a, len, n, (mine + 32 < rows ? mine + 31 : rows - 1) / G, unused, w_hi);
+  }
+
+  Rows<DB> w[QT];
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt)
+    load_rows<T, DB, W16>(a, w[qt], row0, n, len, h, mine + 16 * qt + col, g);
+
+  u32x4 kr[KN], vr[VN];
+  float ks = 0.0f, sv = 0.0f, next_ks = 0.0f, next_sv = 0.0f;
+  int there = 0, next_there = 0;
+  auto fetch = [&](int tile) {
+    const Ids id = tile_ids(a, b, tile, lane);
+    const int k_slot = (tile * kTile + 16 * (col >> 2) + (col & 3)) & (c.P - 1);
+    const uint8_t* kp = c.k_codes + (((int64_t)(id.k < 0 ? 0 : id.k) * c.Hkv + h) * c.P + k_slot) * c.D;
+    const int v_slot = (tile * kTile + 16 * g) & (c.P - 1);
+    const int64_t blk = (int64_t)(id.v < 0 ? 0 : id.v) * c.Hkv + h;
+    const uint8_t* vp = c.v_codes + blk * c.D * c.P + v_slot;
+#pragma unroll
+    for (int k = 0; k < KN; ++k) {
+      const int u = wave + k * NW;
+      if (KU % NW != 0 && u >= KU) break;
+      if (W16) {
+        kr[k] = *(const u32x4*)(kp + 4 * (u / (DB / 2)) * c.D + 64 * (u % (DB / 2)) + 16 * g);
+      } else {
+        const int d = column<false>(u % DB, g);
+        const u32x2 x = *(const u32x2*)(kp + 4 * (u / DB) * c.D + (d < c.D ? d : 0));
+        kr[k][0] = x[0];
+        kr[k][1] = x[1];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < VN; ++k) {
+      const int dt = wave + k * NW, d = 16 * dt + col;
+      if (DT % NW != 0 && dt >= DT) break;
+      vr[k] = *(const u32x4*)(vp + (d < c.D ? d : 0) * c.P);
+    }
+    next_ks = c.k_steps[blk];
+    next_sv = c.v_steps[blk];
+    next_there = id.v >= 0;
+  };
+  auto place = [&](int buf) {
+#pragma unroll
+    for (int k = 0; k < KN; ++k) {
+      const int u = wave + k * NW;
+      if (KU % NW != 0 && u >= KU) break;
+      if (W16) {
+        kf[buf][2 * u][lane] = surplus(kr[k][0], kr[k][1]);
+        kf[buf][2 * u + 1][lane] = surplus(kr[k][2], kr[k][3]);
+      } else {
+        kf[buf][u][lane] = surplus(kr[k][0], kr[k][1]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < VN; ++k) {
+      const int dt = wave + k * NW;
+      if (DT % NW != 0 && dt >= DT) break;
+      vf[buf][2 * dt][lane] = centred(vr[k][0], vr[k][1]);
+      vf[buf][2 * dt + 1][lane] = centred(vr[k][2], vr[k][3]);
+    }
+    ks = next_ks;
+    sv = next_sv;
+    there = next_there;
+  };
+  if (s0 < s1) {
+    fetch(s0);
+    place(0);
+    if (s0 + 1 < s1) fetch(s0 + 1);
+  }
+  int buf = 0;
+  for (int tile = s0; tile < s1; ++tile, buf ^= 1) {
+    __syncthreads();   // this tile's fragments are there, and the other buffer's readers are done
+    const Steps st(ks, sv, there);
+    if (tile + 1 < s1) {
+      place(buf ^ 1);
+      if (tile + 2 < s1) fetch(tile + 2);
+    }
+    if (tile * kTile >= w_hi || tile * kTile + kTile <= w_lo) continue;
+    const int tok = tile * kTile + 16 * g;
+    f32x4 s[QT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) s[qt][i] = f32x4{w[qt].bias, w[qt].bias, w[qt].bias, w[qt].bias};
+#pragma unroll
+      for (int k = 0; k < DB; ++k) {
+        const half8 k8 = kf[buf][i * DB + k][lane];
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt)
+          s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w[qt].q[k], s[qt][i], 0, 0, 0);
+      }
+    }
+    half8 p[QT][2];
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) probabilities<DB>(w[qt], s[qt], p[qt], st, tok);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      const half8 v0 = vf[buf][2 * dt][lane], v1 = vf[buf][2 * dt + 1][lane];
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) {
+        w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[qt][0], w[qt].o[dt], 0, 0, 0);
+        w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[qt][1], w[qt].o[dt], 0, 0, 0);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) {
+    const float l = xor_sum(w[qt].l);
+    const int rr = mine + 16 * qt + col;
+    if (rr >= rows) continue;
+    const int64_t out = (row0 + rr / G) * a.Hq + h * G + rr % G, part = split * c.T * a.Hq + out;
+    const float by = l == 0.0f ? 0.0f : 1.0f / l;
+    if (g == 0) {
+      if (!alone) sp.rl[part] = make_float2(w[qt].r, l);
+      else if (a.lse) a.lse[out] = l == 0.0f ? -INFINITY : (w[qt].r + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      const int d = 16 * dt + 4 * g;
+      if (d >= c.D) continue;
+      if (alone) {
+        struct { S v[4]; } y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y.v[j] = from_f32<S>(w[qt].o[dt][j] * by);
+        *(u32x2*)((S*)a.out + out * c.D + d) = __builtin_bit_cast(u32x2, y);
+      } else {
+        *(f32x4*)(sp.o + part * c.D + d) = w[qt].o[dt];
+      }
     }
   }
 }
@@ -438,26 +632,31 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows
 
 // How a call is split, from its sizes alone.
 struct Plan {
-  int QT, NW, splits, tiles, row_tiles;
+  bool shared;       // attention_rows_kernel
+  int QT, NW, splits, tiles, row_tiles, tile_rows;
 };
 
 Plan plan(int64_t B, int Hq, int Hkv, int max_new, int max_len) {
   Plan p;
   const int64_t rows = (int64_t)max_new * (Hq / Hkv);
-  p.QT = rows > 16 ? 2 : 1;
-  p.row_tiles = (int)((rows + 16 * p.QT - 1) / (16 * p.QT));
   const int tiles = (max_len + kTile - 1) / kTile;
+  p.shared = rows > 64;
+  p.QT = rows > 16 ? 2 : 1;
+  p.NW = 4;
+  p.tile_rows = p.shared ? 32 * p.NW : 16 * p.QT;
+  p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   const int64_t groups = B * Hkv * (int64_t)p.row_tiles;
   // Few short sequences: eight waves a workgroup and no second launch.
-  p.NW = p.QT == 1 && groups <= 256 && tiles <= 16 ? 8 : 4;
+  if (p.QT == 1 && groups <= 256 && tiles <= 16) p.NW = 8;
   // One sequence: all workgroups alike, so as many as run at once (two on a compute
   // unit).  Several: lengths differ, and finer splits even them out.
-  const int64_t target = B == 1 ? 512 : 4096;
+  const int64_t target = B == 1 || p.shared ? 512 : 4096;
   int64_t want = groups >= target ? 1 : target / groups;
+  const int per = p.shared ? 1 : p.NW;     // tiles are dealt to a workgroup's waves, or shared by them
   const int64_t most = (tiles + 2 * p.NW - 1) / (2 * p.NW);
   want = want < most ? want : most;
   p.tiles = (int)((tiles + want - 1) / want);
-  p.tiles = (p.tiles + p.NW - 1) / p.NW * p.NW;
+  p.tiles = (p.tiles + per - 1) / per * per;
   p.splits = (tiles + p.tiles - 1) / p.tiles;
   return p;
 }
@@ -475,6 +674,16 @@ void go_w(const AttArgs& a, const Split& sp, unsigned grid, hipStream_t st) {
 
 template <class T, int DB>
 void go_q(const AttArgs& a, const Plan& p, const Split& sp, unsigned grid, hipStream_t st) {
+  if (p.shared) {
+    if constexpr (DB % 2 == 0) {
+      if (a.c.D % 64 == 0) {
+        attention_rows_kernel<T, DB, 4, true><<<grid, 256, 0, st>>>(a, sp);
+        return;
+      }
+    }
+    attention_rows_kernel<T, DB, 4, false><<<grid, 256, 0, st>>>(a, sp);
+    return;
+  }
   if (p.QT == 1 && p.NW == 8) go_w<T, DB, 1, 8>(a, sp, grid, st);
   else if (p.QT == 1) go_w<T, DB, 1, 4>(a, sp, grid, st);
   else go_w<T, DB, 2, 4>(a, sp, grid, st);
@@ -500,7 +709,7 @@ hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) 
   if (e != hipSuccess || p.splits == 1) return e;
   ProfScope prof("awq_kv_attention_join", st);
   const int64_t rows = (int64_t)a.c.B * a.max_new * a.Hq;
-  join_kernel<T><<<(unsigned)rows, 256, 0, st>>>(a, sp, 16 * p.QT);
+  join_kernel<T><<<(unsigned)rows, 256, 0, st>>>(a, sp, p.tile_rows);
   return hipGetLastError();
 }
 
