@@ -14,8 +14,9 @@
 // value step.
 //
 // Codes become fp16 exactly: the byte u under 0x64 reads 1024 + u.  For the
-// scores the surplus, 1152 sum_d q_d, is the accumulators' first value; for the
-// values 1152 is subtracted (a packed fp16 operation, exact).  Queries are scaled
+// scores the surplus, 1152 sum_d q_d, goes into the constant of the multiply-add
+// before the exponential; for the values 1152 is subtracted (a packed fp16
+// operation, exact).  Queries are scaled
 // by a power of two of their row to |q| < 2 and are exact in fp16 but for bf16
 // elements more than 2^-14 below their row's largest, which keep 24 bits below 1.
 //
@@ -143,14 +144,14 @@ struct Steps {
   float ks, log_sv, inv_sv;
   bool zero, there;    // a value step of 0 weighs in the sum and adds nothing
 
-  __device__ __forceinline__ Steps(float k, float v, int page) {
+  __device__ __forceinline__ Steps(float k, float v, bool page) {
     ks = k + (k - k);
     v += v - v;
     zero = v < kLeastStep;
     v = zero ? kLeastStep : v;
     log_sv = __builtin_amdgcn_logf(v);
     inv_sv = __builtin_amdgcn_rcpf(v);
-    there = page != 0;
+    there = page;
   }
 };
 
@@ -179,7 +180,8 @@ __device__ __forceinline__ void probabilities(Rows<DB>& r, f32x4 (&s)[4], half8 
     for (int j = 0; j < 4; ++j) top = fmaxf(top, s[i][j]);
   // a factor of 0 would make NaN of the -inf of tokens that are not seen
   const float fp = f < kLeastFactor ? kLeastFactor : f;
-  top = xor_max(top * fp + lg);
+  const float surplus_off = lg + r.bias * fp;
+  top = xor_max(fmaf(top, fp, surplus_off));
   if (__any(top > r.r + kTop)) {
     const float to = top > r.r + kTop ? top - kRest : r.r;
     const float by = to == r.r ? 1.0f : __builtin_amdgcn_exp2f(r.r - to);
@@ -188,7 +190,7 @@ __device__ __forceinline__ void probabilities(Rows<DB>& r, f32x4 (&s)[4], half8 
 #pragma unroll
     for (int dt = 0; dt < 2 * DB; ++dt) r.o[dt] *= by;
   }
-  const float off = lg - (r.r == -INFINITY ? 0.0f : r.r);
+  const float off = surplus_off - (r.r == -INFINITY ? 0.0f : r.r);
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -199,6 +201,7 @@ __device__ __forceinline__ void probabilities(Rows<DB>& r, f32x4 (&s)[4], half8 
       p[i >> 1][4 * (i & 1) + j] = (_Float16)e;
     }
   if (__any(st.zero)) {
+    asm volatile("");    // a branch, and not sixteen selects
     p[0] = st.zero ? half8{} : p[0];
     p[1] = st.zero ? half8{} : p[1];
   }
@@ -210,27 +213,63 @@ template <int DB>
 struct Keys {
   u32x4 k[4][(DB + 1) / 2];
   float ks, sv;
-  int there;         // the lane's sixteen tokens have a page
+  bool there;        // the lane's sixteen tokens have a page
 };
 
-struct Ids {
-  int k, v;          // pages of the lane's key rows and of its sixteen tokens
-};
+// Where a lane finds its keys (rows 16 (c / 4) + 4 i + c % 4 of a tile) and its values and
+// steps (tokens 16 g .. 16 g + 15).
+struct Finder {
+  const uint8_t *k, *v;          // of page 0
+  const float *ks, *vs;
+  const int32_t* row;            // the sequence's page table
+  uint32_t page_bytes, heads, n_pages;
+  int last, shift, mask, k_tok, v_tok, D, P;
 
-__device__ __forceinline__ Ids tile_ids(const AttArgs& a, int b, int tile, int lane) {
-  const int64_t t = (int64_t)tile * kTile;
-  Ids id;
-  id.k = page_id(a.c, b, (t + 16 * ((lane & 15) >> 2)) >> a.c.p_shift);
-  id.v = page_id(a.c, b, (t + 16 * (lane >> 4)) >> a.c.p_shift);
-  return id;
-}
+  __device__ __forceinline__ Finder(const KvArgs& c, int b, int h, int lane) {
+    const int col = lane & 15, g = lane >> 4;
+    row = c.pages + (int64_t)b * c.max_pages;
+    last = c.max_pages - 1;
+    shift = c.p_shift;
+    mask = c.P - 1;
+    n_pages = (uint32_t)c.n_pages;
+    heads = (uint32_t)c.Hkv;
+    page_bytes = (uint32_t)c.Hkv * (uint32_t)c.P * (uint32_t)c.D;   // below 2^31
+    D = c.D;
+    P = c.P;
+    k_tok = 16 * (col >> 2);
+    v_tok = 16 * g;
+    k = c.k_codes + (uint32_t)h * c.P * c.D;
+    v = c.v_codes + (uint32_t)h * c.P * c.D;
+    ks = c.k_steps + h;
+    vs = c.v_steps + h;
+  }
+  __device__ __forceinline__ int page(int tile, int tok) const { return (tile * kTile + tok) >> shift; }
+  // Entries for a tile, inside the table; used a tile later, when they have come.
+  __device__ __forceinline__ int2 entries(int tile) const {
+    const int pk = page(tile, k_tok), pv = page(tile, v_tok);
+    return make_int2(row[pk < last ? pk : last], row[pv < last ? pv : last]);
+  }
+  __device__ __forceinline__ bool there(int entry, int tile, int tok) const {
+    return page(tile, tok) <= last && (uint32_t)entry < n_pages;
+  }
+  // Pointers into the tile; a page that is not there reads as page 0 and is masked.
+  __device__ __forceinline__ const uint8_t* keys(int2 e, int tile, int col) const {
+    const uint32_t id = there(e.x, tile, k_tok) ? (uint32_t)e.x : 0u;
+    return k + (uint64_t)id * page_bytes + (uint32_t)(((tile * kTile + k_tok + (col & 3)) & mask) * D);
+  }
+  __device__ __forceinline__ const uint8_t* values(int2 e, int tile) const {
+    const uint32_t id = there(e.y, tile, v_tok) ? (uint32_t)e.y : 0u;
+    return v + (uint64_t)id * page_bytes + (uint32_t)((tile * kTile + v_tok) & mask);
+  }
+  __device__ __forceinline__ uint64_t block(int2 e, int tile) const {
+    return (uint64_t)(there(e.y, tile, v_tok) ? (uint32_t)e.y : 0u) * heads;
+  }
+};
 
 template <int DB, bool W16>
-__device__ __forceinline__ void load_keys(const AttArgs& a, Keys<DB>& k, Ids id, int h, int tile,
-                                          int lane) {
-  const int c = lane & 15, g = lane >> 4, D = a.c.D;
-  const int slot = (tile * kTile + 16 * (c >> 2) + (c & 3)) & (a.c.P - 1);
-  const uint8_t* p = a.c.k_codes + (((int64_t)(id.k < 0 ? 0 : id.k) * a.c.Hkv + h) * a.c.P + slot) * D;
+__device__ __forceinline__ void load_keys(const Finder& f, Keys<DB>& k, int2 e, int tile, int lane) {
+  const int col = lane & 15, g = lane >> 4, D = f.D;
+  const uint8_t* p = f.keys(e, tile, col);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint8_t* r = p + 4 * i * D;
@@ -247,10 +286,10 @@ __device__ __forceinline__ void load_keys(const AttArgs& a, Keys<DB>& k, Ids id,
       }
     }
   }
-  const int64_t blk = (int64_t)(id.v < 0 ? 0 : id.v) * a.c.Hkv + h;
-  k.there = id.v >= 0;
-  k.ks = a.c.k_steps[blk];
-  k.sv = a.c.v_steps[blk];
+  const uint64_t blk = f.block(e, tile);
+  k.there = f.there(e.y, tile, f.v_tok);
+  k.ks = f.ks[blk];
+  k.sv = f.vs[blk];
 }
 
 // NW waves share the tokens of one row tile (QT x 16 rows) and split; their
@@ -297,19 +336,19 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
     load_rows<T, DB, W16>(a, w[qt], row0, n, len, h, base + 16 * qt + col, g);
 
   Keys<DB> kt;
-  Ids id = {-1, -1}, next = {-1, -1};
+  const Finder find(c, b, h, lane);
+  int2 id = make_int2(0, 0), next = id;
   int tile = s0 + wave;
   if (tile < s1) {
-    id = tile_ids(a, b, tile, lane);
-    load_keys<DB, W16>(a, kt, id, h, tile, lane);
-    next = tile_ids(a, b, tile + NW, lane);
+    id = find.entries(tile);
+    next = find.entries(tile + NW);
+    load_keys<DB, W16>(find, kt, id, tile, lane);
   }
   for (; tile < s1; tile += NW) {
     // values of this tile: sixteen tokens of column 16 dt + col
     u32x4 v[DT];
     {
-      const int slot = (tile * kTile + 16 * g) & (c.P - 1);
-      const uint8_t* p = c.v_codes + ((int64_t)(id.v < 0 ? 0 : id.v) * c.Hkv + h) * c.D * c.P + slot;
+      const uint8_t* p = find.values(id, tile);
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         const int d = 16 * dt + col;
@@ -320,7 +359,7 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) s[qt][i] = f32x4{w[qt].bias, w[qt].bias, w[qt].bias, w[qt].bias};
+      for (int qt = 0; qt < QT; ++qt) s[qt][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int ks = 0; ks < DB; ++ks) {
         const u32x4 raw = kt.k[i][ks >> 1];
@@ -334,8 +373,8 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
     const int tok = tile * kTile + 16 * g;
     if (tile + NW < s1) {
       id = next;
-      load_keys<DB, W16>(a, kt, id, h, tile + NW, lane);
-      next = tile_ids(a, b, tile + 2 * NW, lane);
+      load_keys<DB, W16>(find, kt, id, tile + NW, lane);
+      next = find.entries(tile + 2 * NW);
     }
     half8 p[QT][2];
 #pragma unroll
@@ -441,14 +480,13 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
 
   u32x4 kr[KN], vr[VN];
   float ks = 0.0f, sv = 0.0f, next_ks = 0.0f, next_sv = 0.0f;
-  int there = 0, next_there = 0;
+  bool there = false, next_there = false;
+  const Finder find(c, b, h, lane);
+  int2 entry = make_int2(0, 0);       // of the tile after the one that is on its way
   auto fetch = [&](int tile) {
-    const Ids id = tile_ids(a, b, tile, lane);
-    const int k_slot = (tile * kTile + 16 * (col >> 2) + (col & 3)) & (c.P - 1);
-    const uint8_t* kp = c.k_codes + (((int64_t)(id.k < 0 ? 0 : id.k) * c.Hkv + h) * c.P + k_slot) * c.D;
-    const int v_slot = (tile * kTile + 16 * g) & (c.P - 1);
-    const int64_t blk = (int64_t)(id.v < 0 ? 0 : id.v) * c.Hkv + h;
-    const uint8_t* vp = c.v_codes + blk * c.D * c.P + v_slot;
+    const int2 e = entry;
+    entry = find.entries(tile + 1);
+    const uint8_t *kp = find.keys(e, tile, col), *vp = find.values(e, tile);
 #pragma unroll
     for (int k = 0; k < KN; ++k) {
       const int u = wave + k * NW;
@@ -468,9 +506,10 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
       if (DT % NW != 0 && dt >= DT) break;
       vr[k] = *(const u32x4*)(vp + (d < c.D ? d : 0) * c.P);
     }
-    next_ks = c.k_steps[blk];
-    next_sv = c.v_steps[blk];
-    next_there = id.v >= 0;
+    const uint64_t blk = find.block(e, tile);
+    next_ks = find.ks[blk];
+    next_sv = find.vs[blk];
+    next_there = find.there(e.y, tile, find.v_tok);
   };
   auto place = [&](int buf) {
 #pragma unroll
@@ -496,6 +535,7 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
     there = next_there;
   };
   if (s0 < s1) {
+    entry = find.entries(s0);
     fetch(s0);
     place(0);
     if (s0 + 1 < s1) fetch(s0 + 1);
@@ -511,17 +551,22 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
     if (tile * kTile >= w_hi || tile * kTile + kTile <= w_lo) continue;
     const int tok = tile * kTile + 16 * g;
     f32x4 s[QT][4];
+    half8 k0[DB], k1[DB];
+#pragma unroll
+    for (int k = 0; k < DB; ++k) k0[k] = kf[buf][k][lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      half8 *now = i & 1 ? k1 : k0, *then = i & 1 ? k0 : k1;
+      if (i < 3)
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) s[qt][i] = f32x4{w[qt].bias, w[qt].bias, w[qt].bias, w[qt].bias};
+        for (int k = 0; k < DB; ++k) then[k] = kf[buf][(i + 1) * DB + k][lane];
 #pragma unroll
-      for (int k = 0; k < DB; ++k) {
-        const half8 k8 = kf[buf][i * DB + k][lane];
+      for (int qt = 0; qt < QT; ++qt) s[qt][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < DB; ++k)
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt)
-          s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w[qt].q[k], s[qt][i], 0, 0, 0);
-      }
+          s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now[k], w[qt].q[k], s[qt][i], 0, 0, 0);
     }
     half8 p[QT][2];
 #pragma unroll
