@@ -39,11 +39,109 @@ constexpr float kLeastStep = 7.888609052210118e-31f;   // 2^-100: a value step b
 
 struct Split {
   int splits;        // workgroups along the tokens of one row tile
-  int tiles;         // 64-token tiles of each
+  int tiles;         // 64-token tiles of each; where `chosen` is set, the least, a power of two
   int row_tiles;     // row tiles of a sequence and kv head
   float* o;          // [splits][T * Hq][D], null when splits == 1
   float2* rl;        // [splits][T * Hq]: reference and sum
+  int* chosen;       // where the first kernel tells the second what it took for `tiles`; or null
 };
+
+constexpr int kSlots = 512;      // workgroups of attention_kernel that run at once, two on a compute unit
+constexpr int kChoices = 5;
+
+// 64-token tiles that the rows of a sequence see, so at least as many as any of its row
+// tiles does; -1: it has no rows.
+__device__ __forceinline__ int tiles_of(const AttArgs& a, int b) {
+  int64_t row0;
+  int n, lo, hi, unused;
+  rows_of(a.c, b, row0, n);
+  if (n == 0) return -1;
+  n = n < a.max_new ? n : a.max_new;
+  seen_by(a, a.lens[b], n, 0, lo, unused);
+  seen_by(a, a.lens[b], n, n - 1, unused, hi);
+  return hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 0;
+}
+
+__device__ __forceinline__ int splits_of(int nt, int tiles_log) {
+  return nt > 0 ? ((nt - 1) >> tiles_log) + 1 : nt + 1;
+}
+
+// Sequences differ in length and the host does not know them: every workgroup looks at
+// all lengths, takes for the tiles of a split the least power of two times sp.tiles
+// for which all splits run at once, or that is twice a slot's share of all tiles,
+// and finds its own split by counting: no workgroup but the last few is empty.
+// (A grid of sequences x most splits costs a round of two empty workgroups a
+// compute unit, about a microsecond, for every 512 of them.)
+struct Unit2 {
+  int tiles, b, split;    // b = -1: nothing is left for this workgroup
+};
+
+template <int THREADS>
+__device__ __forceinline__ Unit2 choose(const AttArgs& a, const Split& sp, int want) {
+  constexpr int W = THREADS / 64;
+  __shared__ int sums[W][kChoices + 1], scan[W], found[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int log = 31 - __builtin_clz(sp.tiles);
+  int count[kChoices] = {}, all = 0, first = -1;
+  for (int b = tid; b < a.c.B; b += THREADS) {
+    const int nt = tiles_of(a, b);
+    if (b == tid) first = nt;
+    all += nt > 0 ? nt : 0;
+#pragma unroll
+    for (int k = 0; k < kChoices; ++k) count[k] += splits_of(nt, log + k);
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    all += __shfl_xor(all, m);
+#pragma unroll
+    for (int k = 0; k < kChoices; ++k) count[k] += __shfl_xor(count[k], m);
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < kChoices; ++k) sums[wave][k] = count[k];
+    sums[wave][kChoices] = all;
+  }
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+  all = 0;
+  for (int w = 0; w < W; ++w) all += sums[w][kChoices];
+  const int64_t groups = (int64_t)a.c.Hkv * sp.row_tiles;
+  int take = log;
+#pragma unroll
+  for (int k = 0; k < kChoices; ++k) {
+    int units = 0;
+    for (int w = 0; w < W; ++w) units += sums[w][k];
+    take = log + k;
+    if (units * groups <= kSlots || ((int64_t)kSlots << take) >= 2 * all * groups) break;
+  }
+  int before = 0;
+  for (int b0 = 0; b0 < a.c.B && before <= want; b0 += THREADS) {
+    const int b = b0 + tid;
+    const int mine = b < a.c.B ? splits_of(b0 == 0 ? first : tiles_of(a, b), take) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int x = __shfl_up(upto, m);
+      upto += lane >= m ? x : 0;
+    }
+    if (lane == 63) scan[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < W; ++w) {
+      if (w < wave) upto += scan[w];
+    }
+    const int at = want - before - (upto - mine);
+    if (at >= 0 && at < mine) {
+      found[0] = b;
+      found[1] = at;
+    }
+    int total = 0;
+    for (int w = 0; w < W; ++w) total += scan[w];
+    before += total;
+    __syncthreads();
+  }
+  return {1 << __builtin_amdgcn_readfirstlane(take), __builtin_amdgcn_readfirstlane(found[0]),
+          __builtin_amdgcn_readfirstlane(found[1])};
+}
 
 __device__ __forceinline__ float xor_max(float x) {   // over the four lane groups
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -308,12 +406,23 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp)
   // heads first, splits last: workgroups are dealt to the eight XCDs in turn, so a
   // sequence's splits, of which only the first few may hold tokens, never fall on one
   // XCD, and with 8 heads the row tiles of a head read its keys through one L2
-  int bid = blockIdx.x;
+  int bid = blockIdx.x, b, rt, split;
   const int h = bid % c.Hkv;
   bid /= c.Hkv;
-  const int b = bid % c.B;
-  bid /= c.B;
-  const int rt = bid % sp.row_tiles, split = bid / sp.row_tiles;
+  if (sp.chosen) {
+    rt = bid % sp.row_tiles;
+    const Unit2 u = choose<NW * 64>(a, sp, bid / sp.row_tiles);
+    if (blockIdx.x == 0 && tid == 0) *sp.chosen = u.tiles;
+    if (u.b < 0) return;
+    sp.tiles = u.tiles;
+    b = u.b;
+    split = u.split;
+  } else {
+    b = bid % c.B;
+    bid /= c.B;
+    rt = bid % sp.row_tiles;
+    split = bid / sp.row_tiles;
+  }
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
@@ -611,7 +720,8 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
 
 // Joins the splits of a row and head that had more than one: a workgroup each, its
 // threads in groups of D / 4 that share the splits, so that the loads of many
-// splits are in flight at once.
+// splits are in flight at once.  Four waves for one sequence's many splits, one wave for
+// many sequences, most of which have few or one.
 template <class T>
 __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows_per_tile) {
   typedef typename T::storage S;
@@ -629,6 +739,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows
   rows_of(c, b, row0, n);
   n = n < a.max_new ? n : a.max_new;
   if (i >= n) return;
+  if (sp.chosen) sp.tiles = *sp.chosen;
   const int G = a.Hq / c.Hkv, len = a.lens[b], rows = n * G;
   const int base = (i * G + hq % G) / rows_per_tile * rows_per_tile;
   int lo, hi, unused;
@@ -639,13 +750,15 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows
   const int active = (nt + sp.tiles - 1) / sp.tiles;
   const int64_t out = (row0 + i) * a.Hq + hq, step = c.T * a.Hq;
   float top = -INFINITY;
-  for (int s = tid; s < active; s += 256) top = fmaxf(top, sp.rl[s * step + out].x);
+  for (int s = tid; s < active; s += blockDim.x) top = fmaxf(top, sp.rl[s * step + out].x);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-  if ((tid & 63) == 0) stop[tid >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(stop[0], stop[1]), fmaxf(stop[2], stop[3]));
-  const int quads = c.D / 4, groups = 256 / quads, group = tid / quads, d = 4 * (tid % quads);
+  if (blockDim.x > 64) {
+    if ((tid & 63) == 0) stop[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(stop[0], stop[1]), fmaxf(stop[2], stop[3]));
+  }
+  const int quads = c.D / 4, groups = blockDim.x / quads, group = tid / quads, d = 4 * (tid % quads);
   float l = 0.0f;
   f32x4 o = {0, 0, 0, 0};
   if (group < groups) {
@@ -678,6 +791,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows
 // How a call is split, from its sizes alone.
 struct Plan {
   bool shared;       // attention_rows_kernel
+  bool chosen;       // the kernel chooses the tiles of a split
+  int64_t blocks;
   int QT, NW, splits, tiles, row_tiles, tile_rows;
 };
 
@@ -693,16 +808,26 @@ Plan plan(int64_t B, int Hq, int Hkv, int max_new, int max_len) {
   const int64_t groups = B * Hkv * (int64_t)p.row_tiles;
   // Few short sequences: eight waves a workgroup and no second launch.
   if (p.QT == 1 && groups <= 256 && tiles <= 16) p.NW = 8;
-  // One sequence: all workgroups alike, so as many as run at once (two on a compute
-  // unit).  Several: lengths differ, and finer splits even them out.
-  const int64_t target = B == 1 || p.shared ? 512 : 4096;
-  int64_t want = groups >= target ? 1 : target / groups;
-  const int per = p.shared ? 1 : p.NW;     // tiles are dealt to a workgroup's waves, or shared by them
-  const int64_t most = (tiles + 2 * p.NW - 1) / (2 * p.NW);
-  want = want < most ? want : most;
-  p.tiles = (int)((tiles + want - 1) / want);
-  p.tiles = (p.tiles + per - 1) / per * per;
+  p.chosen = B > 1 && !p.shared && p.NW == 4 && tiles > 8;
+  if (p.chosen) {
+    // lengths differ: the kernel chooses among kChoices powers of two, up to what all
+    // sequences at their longest would take
+    p.tiles = 8;
+    while (p.tiles << (kChoices - 1) < 2 * tiles * groups / kSlots && p.tiles < tiles) p.tiles *= 2;
+    while (tiles / p.tiles * groups > 8192) p.tiles *= 2;     // bounds the workspace
+    p.blocks = kSlots + groups;   // splits that run at once, or half of that and one for each sequence
+  } else {
+    // as many workgroups as run at once, two on a compute unit
+    int64_t want = groups >= kSlots ? 1 : kSlots / groups;
+    const int per = p.shared ? 1 : p.NW;   // tiles are dealt to a workgroup's waves, or shared by them
+    const int64_t most = (tiles + 2 * p.NW - 1) / (2 * p.NW);
+    want = want < most ? want : most;
+    p.tiles = (int)((tiles + want - 1) / want);
+    p.tiles = (p.tiles + per - 1) / per * per;
+  }
   p.splits = (tiles + p.tiles - 1) / p.tiles;
+  p.chosen = p.chosen && p.splits > 1;
+  if (!p.chosen) p.blocks = groups * p.splits;
   return p;
 }
 
@@ -736,7 +861,7 @@ void go_q(const AttArgs& a, const Plan& p, const Split& sp, unsigned grid, hipSt
 
 template <class T>
 hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.c.B * a.c.Hkv * p.row_tiles * p.splits);
+  const unsigned grid = (unsigned)p.blocks;
   {
     ProfScope prof("awq_kv_attention", st);
     switch ((a.c.D + 31) / 32) {
@@ -754,7 +879,7 @@ hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) 
   if (e != hipSuccess || p.splits == 1) return e;
   ProfScope prof("awq_kv_attention_join", st);
   const int64_t rows = (int64_t)a.c.B * a.max_new * a.Hq;
-  join_kernel<T><<<(unsigned)rows, 256, 0, st>>>(a, sp, p.tile_rows);
+  join_kernel<T><<<(unsigned)rows, p.chosen ? 64 : 256, 0, st>>>(a, sp, p.tile_rows);
   return hipGetLastError();
 }
 
@@ -763,24 +888,24 @@ hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) 
 size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
                              int max_len) {
   const Plan p = plan(B, Hq, Hkv, max_new, max_len);
-  return p.splits == 1 ? 0 : (size_t)p.splits * T * Hq * (D + 2) * 4;
+  return p.splits == 1 ? 0 : (size_t)p.splits * T * Hq * (D + 2) * 4 + 4;
 }
 
 int64_t kv_attention_blocks(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
                             int max_len) {
   if (max_new > (int64_t)INT32_MAX / Hq) return INT64_MAX;
-  const Plan p = plan(B, Hq, Hkv, max_new, max_len);
-  const int64_t a = p.row_tiles * (int64_t)p.splits, rows = (int64_t)max_new * Hq;
-  if (B * Hkv > INT32_MAX || B * Hkv > INT32_MAX / a || B > INT32_MAX / rows) return INT64_MAX;
-  return B * Hkv * a;
+  const int64_t rows = (int64_t)max_new * Hq;
+  if (B > INT32_MAX / rows) return INT64_MAX;
+  return plan(B, Hq, Hkv, max_new, max_len).blocks;
 }
 
 hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipStream_t st) {
   const Plan p = plan(a.c.B, a.Hq, a.c.Hkv, a.max_new, a.max_len);
-  Split sp = {p.splits, p.tiles, p.row_tiles, nullptr, nullptr};
+  Split sp = {p.splits, p.tiles, p.row_tiles, nullptr, nullptr, nullptr};
   if (p.splits > 1) {
     sp.o = (float*)ws;
     sp.rl = (float2*)(sp.o + (size_t)p.splits * a.c.T * a.Hq * a.c.D);
+    if (p.chosen) sp.chosen = (int*)(sp.rl + (size_t)p.splits * a.c.T * a.Hq);
   }
   return dt == AWQ_F16 ? go<F16T>(a, p, sp, st) : go<BF16T>(a, p, sp, st);
 }

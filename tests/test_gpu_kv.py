@@ -476,6 +476,44 @@ def test_attention_long_and_split():
     check_attention(dev, ref, q, [10000], table, None, "f16", window=4097)
 
 
+UNEVEN = [   # sequences, rows of each, shortest, longest, q heads, kv heads, D, page, window
+    (3, 1, 1, 2300, 8, 2, 64, 64, 0), (300, 1, 0, 1100, 4, 1, 32, 16, 0), (40, 1, 700, 1500, 6, 6, 64, 128, 0),
+    (7, 3, 2, 1300, 16, 2, 40, 32, 0), (5, 2, 600, 1800, 24, 1, 128, 64, 900), (2, 45, 700, 1400, 4, 2, 64, 16, 0),
+    (1, 40, 2500, 2500, 4, 1, 64, 64, 0), (1, 33, 1100, 1100, 3, 1, 96, 64, 300), (600, 1, 0, 700, 1, 1, 16, 64, 0),
+]
+
+
+@pytest.mark.parametrize("shape", UNEVEN)
+def test_attention_of_uneven_sequences(shape):
+    """Splits that the device chooses by the lengths, sequences of every length among them."""
+    B, n, lo, hi, hq, heads, dim, page, window = shape
+    rng = np.random.default_rng(B + hi)
+    lens = rng.permutation(np.linspace(max(lo, n if lo else 0), hi, B).astype(int)).tolist()
+    per_seq = -(-hi // page)
+    dev, ref = new_cache(rng, min(B * per_seq, 3000) + 1, heads, page, dim)
+    table = np.full((B, per_seq), -1, np.int32)
+    free = rng.permutation(dev.n_pages)
+    at = 0
+    for b, length in enumerate(lens):      # only the pages that a sequence holds; read pages may be shared
+        held = -(-length // page)
+        table[b, :held] = free[(at + np.arange(held)) % dev.n_pages]
+        at += held
+    q = torch.from_numpy(rng.standard_normal((B * n, hq, dim)).astype(f32)).half().cuda()
+    starts = None if n == 1 else (np.arange(B + 1) * n).tolist()
+    check_attention(dev, ref, q, lens, table, starts, "f16", window, max_new=n, max_len=hi)
+
+
+@pytest.mark.parametrize("longest", [515, 1030, 2051])
+def test_attention_whose_last_rows_alone_reach_another_split(longest):
+    """64 rows of a head in two row tiles: the tokens that only the second one sees begin a split."""
+    rng = np.random.default_rng(longest)
+    lens = [longest, 513, 600, 1025, 8]
+    dev, ref = new_cache(rng, 5 * 33, 1, 64, 32)
+    table = page_table(rng, 5, 165, 33)
+    q = torch.from_numpy(rng.standard_normal((40, 8, 32)).astype(f32)).half().cuda()
+    check_attention(dev, ref, q, lens, table, list(range(0, 41, 8)), "f16", max_new=8, max_len=max(lens))
+
+
 def test_cache_past_four_gibibytes():
     """Pages whose codes lie beyond a 32-bit offset."""
     n, heads, page, dim = 5 * (1 << 30) // (2 * 128 * 128), 2, 128, 128
