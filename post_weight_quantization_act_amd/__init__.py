@@ -510,62 +510,66 @@ def awq_lowbit_gemm(Xs: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tenso
     return out
 
 
-def _on_gpu(t: torch.Tensor, name: str) -> int:
-    """The GPU that t is on."""
+# The calls below are part of a decode step of some ten microseconds, so their checks are
+# written to cost little: one condition over the cheap attributes, and a function that
+# says what is wrong only where it fails.
+_Tensor = torch.Tensor
+
+
+def _refuse(t, name: str, gpu: int, what: str) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
-    return t.get_device()
-
-
-def _beside(t: torch.Tensor, name: str, gpu: int) -> torch.Tensor:
-    if _on_gpu(t, name) != gpu:
+    if gpu >= 0 and t.get_device() != gpu:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{gpu}")
-    return t
+    raise ValueError(f"{name} must be {what}, got {t.dtype} {list(t.shape)} with strides "
+                     f"{list(t.stride())}")
 
 
-def _heads(t: torch.Tensor, name: str, gpu: int, dims: int = 3) -> torch.Tensor:
-    """A GPU tensor [rows, heads, D] (or [B, S, H, D]) whose heads' columns lie together."""
-    _beside(t, name, gpu)
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t
+def _heads(t: torch.Tensor, name: str, gpu: int) -> None:
+    """[rows, heads, D] whose heads' columns lie together."""
+    if not isinstance(t, _Tensor) or t.get_device() != gpu or gpu < 0 or t.dim() != 3 \
+            or (t.stride(2) != 1 and t.shape[2] > 1):
+        _refuse(t, name, gpu, "[rows, heads, D] with contiguous columns")
 
 
 def _ints(t: torch.Tensor, name: str, gpu: int, shape: tuple) -> int:
-    _beside(t, name, gpu)
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {list(shape)}, got {t.dtype} "
-                         f"{list(t.shape)}")
+    if not isinstance(t, _Tensor) or t.get_device() != gpu or t.dtype is not torch.int32 \
+            or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, gpu, f"contiguous int32 {list(shape)}")
     return t.data_ptr()
 
 
-def _dense(t: torch.Tensor, name: str, gpu: int, like: torch.Tensor, dtype: torch.dtype) -> int:
-    _beside(t, name, gpu)
-    if t.shape != like.shape or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} {list(like.shape)}, got {t.dtype} "
-                         f"{list(t.shape)}")
+def _dense(t: torch.Tensor, name: str, gpu: int, shape: tuple, dtype: torch.dtype) -> int:
+    if not isinstance(t, _Tensor) or t.get_device() != gpu or t.dtype is not dtype \
+            or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, gpu, f"contiguous {dtype} {list(shape)}")
     return t.data_ptr()
+
+
+def _empty(like: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
+    """A dense tensor of like's shape."""
+    if like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
+    return torch.empty(like.shape, dtype=dtype, device=like.device)
+
+
+# the current stream's handle and the current GPU, without objects around them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(fn: str, gpu: int, *args) -> None:
     """Calls fn on the tensors' GPU and its current stream."""
-    f = getattr(library(), fn)
-    if torch.cuda.current_device() == gpu:
+    f = getattr(_LIB or library(), fn)
+    if _current_gpu() == gpu:
         status = f(*args, _raw_stream(gpu))
     else:
         with torch.cuda.device(gpu):
             status = f(*args, _raw_stream(gpu))
     if status != 0:
         _check(status)
-
-
-# the current stream's handle without a Stream object around it (a few calls in a
-# decode step's few microseconds each)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
 
 
 def awq_rope_table(n_pos: int, rot: int, base: float = 10000.0, scaling: str = "none",
@@ -577,16 +581,17 @@ def awq_rope_table(n_pos: int, rot: int, base: float = 10000.0, scaling: str = "
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
     sc = RopeScaling(_ROPE_SCALING[scaling], factor, original, low, high, magnitude)
     table = torch.empty((max(n_pos, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device=device)
-    _run("awq_rope_table", _on_gpu(table, "table"), n_pos, rot, base, ctypes.byref(sc),
+    if not table.is_cuda:
+        _refuse(table, "table", -1, "on a GPU")
+    _run("awq_rope_table", table.get_device(), n_pos, rot, base, ctypes.byref(sc),
          table.data_ptr())
     return table
 
 
 def _table(table: torch.Tensor, gpu: int):
-    _beside(table, "table", gpu)
-    if table.dim() != 3 or table.shape[2] != 2 or table.dtype is not torch.float32 \
-            or not table.is_contiguous():
-        raise ValueError("table must be contiguous fp32 [positions, rot/2, 2] (awq_rope_table)")
+    if not isinstance(table, _Tensor) or table.get_device() != gpu or table.dim() != 3 \
+            or table.dtype is not torch.float32 or table.shape[2] != 2 or not table.is_contiguous():
+        _refuse(table, "table", gpu, "contiguous fp32 [positions, rot/2, 2] (awq_rope_table)")
     n_pos, half, _ = table.shape
     return table.data_ptr(), n_pos, 2 * half
 
@@ -598,25 +603,31 @@ def awq_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor | Non
     head's first 2 * table.shape[1] columns turned by the row's position; transpose=True gives the
     gradient with respect to x.  positions int32 [T], [S] or [B, S]; None: the row's index.
     out may be x."""
-    gpu = _on_gpu(x, "x")
-    dims = 4 if x.dim() == 4 else 3
-    _heads(x, "x", gpu, dims)
+    if not isinstance(x, _Tensor) or not x.is_cuda:
+        _refuse(x, "x", -1, "on a GPU")
+    gpu, shape, xs, dtype = x.get_device(), x.shape, x.stride(), x.dtype
+    if len(shape) == 4:
+        B, S, H, D = shape
+    elif len(shape) == 3:
+        S, H, D = shape
+        B, xs = 1, (0, *xs)
+    else:
+        _refuse(x, "x", gpu, "[T, H, D] or [B, S, H, D]")
+    if xs[3] != 1 and D > 1:
+        _refuse(x, "x", gpu, "[T, H, D] or [B, S, H, D] with contiguous columns")
     tp, n_pos, rot = _table(table, gpu)
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    else:
-        _heads(out, "out", gpu, dims)
-        if out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError("out must have x's shape and out_dtype")
-    xs, os_ = x.stride(), out.stride()
-    if dims == 4:
-        B, S, H, D = x.shape
-    else:
-        (S, H, D), B = x.shape, 1
-        xs, os_ = (0, *xs), (0, *os_)
+        out = _empty(x, out_dtype or dtype)
+    elif not isinstance(out, _Tensor) or out.get_device() != gpu or out.shape != shape \
+            or (out_dtype is not None and out.dtype != out_dtype) \
+            or (out.stride(-1) != 1 and D > 1):
+        _refuse(out, "out", gpu, f"{list(shape)} of out_dtype with contiguous columns")
+    os_ = out.stride()
+    if len(os_) == 3:
+        os_ = (0, *os_)
     pp, ps = None, 0
     if positions is not None:
-        ps = S if positions.dim() == 2 else 0
+        ps = S if isinstance(positions, _Tensor) and positions.dim() == 2 else 0
         pp = _ints(positions, "positions", gpu, (B, S) if ps else (S,))
     _run("awq_rope", gpu, x.data_ptr(), _dtype(x), B, S, H, D, _I64x4(*xs), pp, ps, tp, n_pos, rot,
          (AWQ_ROPE_INTERLEAVED if interleaved else 0) | (AWQ_ROPE_TRANSPOSE if transpose else 0),
@@ -630,16 +641,14 @@ class KvCache:
     Holds the tensors; which page is whose is the caller's (page tables)."""
 
     def __init__(self, k_codes, v_codes, k_steps, v_steps):
-        self.gpu = _on_gpu(k_codes, "k_codes")
-        if k_codes.dim() != 4 or k_codes.dtype is not torch.uint8 or not k_codes.is_contiguous():
-            raise ValueError("k_codes must be contiguous uint8 [n_pages, kv_heads, page, D]")
+        if not isinstance(k_codes, _Tensor) or not k_codes.is_cuda or k_codes.dim() != 4:
+            _refuse(k_codes, "k_codes", -1, "uint8 [n_pages, kv_heads, page, D]")
+        self.gpu = k_codes.get_device()
         n, h, p, d = k_codes.shape
-        for t, name, dtype, shape in ((v_codes, "v_codes", torch.uint8, (n, h, d, p)),
-                                      (k_steps, "k_steps", torch.float32, (n, h)),
-                                      (v_steps, "v_steps", torch.float32, (n, h))):
-            _beside(t, name, self.gpu)
-            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
+        _dense(k_codes, "k_codes", self.gpu, (n, h, p, d), torch.uint8)
+        _dense(v_codes, "v_codes", self.gpu, (n, h, d, p), torch.uint8)
+        _dense(k_steps, "k_steps", self.gpu, (n, h), torch.float32)
+        _dense(v_steps, "v_steps", self.gpu, (n, h), torch.float32)
         self.k_codes, self.v_codes, self.k_steps, self.v_steps = k_codes, v_codes, k_steps, v_steps
         self.n_pages, self.kv_heads, self.page, self.head_dim = n, h, p, d
         self.device = k_codes.device
@@ -660,10 +669,10 @@ def _paged(cache: KvCache, pages, starts, per_sequence, name):
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache")
     gpu = cache.gpu
-    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
-        raise ValueError("pages must be an int32 tensor [sequences, pages]")
-    B, most = pages.shape
-    return (gpu, B, most, _ints(pages, "pages", gpu, (B, most)),
+    if not isinstance(pages, _Tensor) or pages.dim() != 2:
+        _refuse(pages, "pages", gpu, "int32 [sequences, pages]")
+    B, most = shape = pages.shape
+    return (gpu, B, most, _ints(pages, "pages", gpu, shape),
             None if starts is None else _ints(starts, "starts", gpu, (B + 1,)),
             _ints(per_sequence, name, gpu, (B,)))
 
@@ -682,29 +691,29 @@ def awq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.
     _heads(k, "k", gpu)
     _heads(v, "v", gpu)
     shape, dtype = k.shape, k.dtype
-    T = shape[0]
-    if shape != (T, cache.kv_heads, cache.head_dim) or v.shape != shape or v.dtype is not dtype:
+    T, heads, D = shape
+    if heads != cache.kv_heads or D != cache.head_dim or v.shape != shape or v.dtype is not dtype:
         raise ValueError(f"k and v must be [T, {cache.kv_heads}, {cache.head_dim}] of one dtype")
     tp, n_pos, rot = (None, 0, 0) if table is None else _table(table, gpu)
     qp, op, Hq, qs, odt = None, None, 0, None, AWQ_F32
     if q is not None:
         _heads(q, "q", gpu)
-        Hq = q.shape[1]
-        if q.shape != (T, Hq, cache.head_dim) or q.dtype is not dtype:
+        rows, Hq, cols = shape = q.shape
+        if rows != T or cols != D or q.dtype is not dtype:
             raise ValueError(f"q must be [T, Hq, {cache.head_dim}] of k's dtype")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q_dtype or dtype, device=cache.device)
+            q_out = _empty(q, q_dtype or dtype)
             op = q_out.data_ptr()
         else:
-            op = _dense(q_out, "q_out", gpu, q, q_dtype or q_out.dtype)
-        qp, odt = q.data_ptr(), _dtype(q_out)
-        qs = _I64x4(*q.stride()[:2])
+            op = _dense(q_out, "q_out", gpu, shape,
+                        q_dtype or (q_out.dtype if isinstance(q_out, _Tensor) else dtype))
+        qp, odt, qs = q.data_ptr(), _dtype(q_out), _I64x4(*q.stride())
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if max_new is None:
-        max_new = 1 if starts is None else T
+    ks, vs = k.stride(), v.stride()
     _run("awq_kv_append", gpu, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k), T,
-         _I64x4(*k.stride()[:2], *v.stride()[:2]), sp, lp, B, pp, most, max_new, tp, n_pos, rot,
+         _I64x4(ks[0], ks[1], vs[0], vs[1]), sp, lp, B, pp, most,
+         (1 if starts is None else T) if max_new is None else max_new, tp, n_pos, rot,
          AWQ_ROPE_INTERLEAVED if interleaved else 0,
          None if positions is None else _ints(positions, "positions", gpu, (T,)), qp, Hq, qs, op,
          odt)
@@ -747,33 +756,32 @@ def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages:
     longest length (None: what the page table can hold); scale None: D ** -0.5."""
     gpu, B, most, pp, sp, lp = _paged(cache, pages, starts, lens, "lens")
     _heads(q, "q", gpu)
-    T, Hq, D = q.shape
+    T, Hq, D = shape = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q must be [T, Hq, {cache.head_dim}]")
     if max_len is None or max_len > most * cache.page:
         max_len = most * cache.page
     if max_new is None:
         max_new = 1 if starts is None else T
-    if scale is None:
-        scale = D ** -0.5
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
+        out = _empty(q, q.dtype)
         op = out.data_ptr()
     else:
-        op = _dense(out, "out", gpu, q, q.dtype)
+        op = _dense(out, "out", gpu, shape, q.dtype)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=cache.device) if return_lse else None
-    ws, size = None, 0
     if workspace is not None:
-        ws, size = _dev(_beside(workspace, "workspace", gpu), "workspace").data_ptr(), workspace.nbytes
+        ws = _dense(workspace, "workspace", gpu, workspace.shape, workspace.dtype)
+        size = workspace.nbytes
     else:
-        size = library().awq_kv_attention_workspace_size(T, B, Hq, cache.kv_heads, D, max_new,
-                                                         max_len)
+        ws, size = None, (_LIB or library()).awq_kv_attention_workspace_size(
+            T, B, Hq, cache.kv_heads, D, max_new, max_len)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
             ws = workspace.data_ptr()
     _run("awq_kv_attention", gpu, cache._ref, q.data_ptr(), _dtype(q), T, Hq,
-         _I64x4(*q.stride()[:2]), sp, lp, B, pp, most, max_new, max_len, scale, window,
-         0 if causal else AWQ_ATT_FULL, op, None if lse is None else lse.data_ptr(), ws, size)
+         _I64x4(*q.stride()), sp, lp, B, pp, most, max_new, max_len,
+         D ** -0.5 if scale is None else scale, window, 0 if causal else AWQ_ATT_FULL, op,
+         None if lse is None else lse.data_ptr(), ws, size)
     return (out, lse) if return_lse else out
 
 

@@ -17,14 +17,15 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // Largest of two values over the workgroup (red: one pair for each wave).
+template <bool WAVE = false>
 __device__ __forceinline__ void block_max(uint32_t& k, uint32_t& v, uint2* red) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) {
     k = umax(k, (uint32_t)__shfl_xor((int)k, m));
     v = umax(v, (uint32_t)__shfl_xor((int)v, m));
   }
+  if (WAVE) return;
   const int waves = blockDim.x >> 6;
-  if (waves == 1) return;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = make_uint2(k, v);
   __syncthreads();
   for (int w = 0; w < waves; ++w) {
@@ -46,29 +47,29 @@ __device__ __forceinline__ uint32_t coded(float x, float step) {
 
 // The codes of a block's new values.  A step that is a number bounds the values by
 // about 127 of it, so none is NaN and the quotient comes from the step's reciprocal
-// (correctly rounded, five operations against eleven); a step of 0, or one that is not
-// finite, makes every code 0, as the definition does.  Clamped, a quotient plus
-// 2^23 + 128 is rounded to the nearest integer, ties to even, and its lowest byte is
-// the stored code.
+// (correctly rounded, five operations against eleven; both sides scaled by a power of
+// two where the step is so small or large that a remainder would not be a normal
+// number); a step of 0, or one that is not finite, makes every code 0, as the
+// definition does.  Clamped, a quotient plus 2^23 + 128 is rounded to the nearest
+// integer, ties to even, and its lowest byte is the stored code.
 struct Coder {
-  float step, inverse;
-  bool plain;      // the reciprocal and the remainders are normal numbers
+  float step, inverse, scale;
   bool none;
 
-  __device__ __forceinline__ explicit Coder(float s) : step(s), inverse(1.0f / s) {
-    plain = s >= 0x1p-100f && s <= 0x1p100f;
+  __device__ __forceinline__ explicit Coder(float s) {
     none = !(s > 0.0f && s < INFINITY);
+    scale = s < 0x1p-60f ? 0x1p100f : s > 0x1p60f ? 0x1p-100f : 1.0f;
+    step = s * scale;
+    inverse = 1.0f / step;
   }
   __device__ __forceinline__ uint32_t four(float a, float b, float c, float d) const {
-    if (none) return 0x80808080u;
-    if (!plain)
-      return coded(a, step) | coded(b, step) << 8 | coded(c, step) << 16 | coded(d, step) << 24;
     const uint32_t lo = __builtin_amdgcn_perm(bits(b), bits(a), 0x0c0c0400u);
     const uint32_t hi = __builtin_amdgcn_perm(bits(d), bits(c), 0x04000c0cu);
-    return lo | hi;
+    return none ? 0x80808080u : lo | hi;
   }
   __device__ __forceinline__ uint32_t bits(float x) const {
-    return __float_as_uint(__builtin_amdgcn_fmed3f(div_rn(x, step, inverse), -127.0f, 127.0f) + 8388736.0f);
+    const float q = div_rn(x * scale, step, inverse);
+    return __float_as_uint(__builtin_amdgcn_fmed3f(q, -127.0f, 127.0f) + 8388736.0f);
   }
 };
 
@@ -139,22 +140,22 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   typedef typename TQ::storage SQ;
   __shared__ uint2 red[16];
   const KvArgs& c = a.c;
+  constexpr bool kWave = HOLD == 1;   // one token: a wave takes a head, a workgroup four
   const bool queries = (int)blockIdx.x >= a.kv_blocks;
   uint32_t g = queries ? blockIdx.x - a.kv_blocks : blockIdx.x;
-  const uint32_t fan = queries ? a.q_parts : c.Hkv, low = g & 7;
+  const uint32_t fan = queries ? a.q_parts : kWave ? (c.Hkv + 3) / 4 : c.Hkv, low = g & 7;
   g >>= 3;
-  const int h = (int)(g % fan);       // or the part of the queries
+  const int part = (int)(g % fan);
   const uint32_t at = g / fan * 8 + low;
   if (at >= (uint32_t)c.B * (uint32_t)a.pages_per_seq) return;
   const int j = (int)(at % (uint32_t)a.pages_per_seq), b = (int)(at / (uint32_t)a.pages_per_seq);
   Place p;
   if (!find_place(a, b, j, p)) return;
-  const int tid = threadIdx.x, threads = blockDim.x;
   const int units = units_of(c.D, a.rot), tokens = p.hi - p.lo, half = a.rot >> 1;
 
   if (queries) {
-    const int work = tokens * a.Hq * units;
-    for (int e = h * threads + tid; e < work; e += a.q_parts * threads) {
+    const int work = tokens * a.Hq * units, step = blockDim.x;
+    for (int e = part * step + threadIdx.x; e < work; e += a.q_parts * step) {
       const int u = e % units, r = e / units, hq = r % a.Hq;
       const int64_t row = p.row_lo + r / a.Hq;
       const Unit w = unit_of(c.D, a.rot, a.interleaved, u);
@@ -172,10 +173,12 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
     return;
   }
 
+  const int tid = kWave ? threadIdx.x & 63 : threadIdx.x, threads = kWave ? 64 : blockDim.x;
+  const int h = kWave ? part * 4 + (threadIdx.x >> 6) : part;
+  if (kWave && h >= c.Hkv) return;
+  // the page's entry and steps, and the new rows: asked for together, looked at later
   const int id = page_id(c, b, p.page);
-  if (id < 0) return;   // no such page: its tokens are not kept
-  const int64_t blk = (int64_t)id * c.Hkv + h;
-  const float k_was = p.lo > 0 ? c.k_steps[blk] : 0.0f, v_was = p.lo > 0 ? c.v_steps[blk] : 0.0f;
+  const int64_t blk = (int64_t)(id < 0 ? 0 : id) * c.Hkv + h;
 
   // patches of values: tokens 4 t .. 4 t + 3 of the page, columns 4 d .. 4 d + 3, neighbours
   // along the tokens, so that a column's codes leave as one run
@@ -223,7 +226,9 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
     if (tid + k * threads < t_n * dq)
 #pragma unroll
       for (int i = 0; i < 16; ++i) vm = umax(vm, abs_bits(to_f32(v[k][i >> 2][i & 3])));
-  block_max(km, vm, red);
+  if (id < 0) return;   // no such page: its tokens are not kept
+  const float k_was = p.lo > 0 ? c.k_steps[blk] : 0.0f, v_was = p.lo > 0 ? c.v_steps[blk] : 0.0f;
+  block_max<kWave>(km, vm, red);
   const Steps s = steps_after(p, k_was, v_was, km, vm);
   const Coder key(s.k), value(s.v);
 
@@ -245,35 +250,33 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
         *(u32x2*)(y + w.d1) = u32x2{key.four(n[0], n[1], n[2], n[3]), key.four(n[4], n[5], n[6], n[7])};
     }
   }
-  // values: older tokens of the block in the dwords before the first patch
+  // values: the dwords that hold older tokens, then the new ones over what of the last
+  // such dword is theirs
   if (s.v_grew) {
-    const int per = c.P >> 2;
-    for (int e = tid; e < c.D * t_lo; e += threads) {
-      uint32_t* w = (uint32_t*)vc + (e / t_lo) * per + e % t_lo;
+    const int per = c.P >> 2, n = (p.lo + 3) >> 2;
+    for (int e = tid; e < c.D * n; e += threads) {
+      uint32_t* w = (uint32_t*)vc + (e / n) * per + e % n;
       *w = moved(*w, s.v_by);
     }
+    __threadfence_block();
+    if (!kWave) __syncthreads();
   }
 #pragma unroll
   for (int k = 0; k < HOLD; ++k) {
     const int e = tid + k * threads;
     if (e < t_n * dq) {
       const int d = e / t_n, t = 4 * (t_lo + e % t_n);
-      const bool whole = t >= p.lo && t + 4 <= p.hi;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         uint8_t* y = vc + (4 * d + m) * c.P + t;
         const uint32_t r = value.four(to_f32(v[k][0][m]), to_f32(v[k][1][m]), to_f32(v[k][2][m]),
                                       to_f32(v[k][3][m]));
-        if (whole) {
+        if (t >= p.lo && t + 4 <= p.hi) {
           *(uint32_t*)y = r;
-          continue;
-        }
-        // a patch that the new tokens fill in part: older tokens before, nobody's places after
-        const uint32_t old = s.v_grew && t < p.lo ? moved(*(const uint32_t*)y, s.v_by) : 0;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (t + i >= p.lo && t + i < p.hi) y[i] = (uint8_t)(r >> (8 * i));
-          else if (s.v_grew && t + i < p.lo) y[i] = (uint8_t)(old >> (8 * i));
+          for (int i = 0; i < 4; ++i)
+            if (t + i >= p.lo && t + i < p.hi) y[i] = (uint8_t)(r >> (8 * i));
         }
       }
     }
@@ -434,7 +437,8 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) 
   const int64_t blk = (int64_t)(id < 0 ? 0 : id) * c.Hkv + h;
   const uint8_t* kc = c.k_codes + (blk * c.P + t) * c.D + d;
   const uint8_t* vc = c.v_codes + (blk * c.D + d) * c.P + t;
-  const float ks = c.k_steps[blk], vs = c.v_steps[blk];
+  // a page that is not there reads as zero
+  const float ks = id < 0 ? 0.0f : c.k_steps[blk], vs = id < 0 ? 0.0f : c.v_steps[blk];
   u32x2 k[4];
   uint32_t v[8];
 #pragma unroll
@@ -448,8 +452,8 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) 
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
       const uint32_t w = k[i][m >> 2];
-      x[m] = id < 0 ? 0.0f : fp32_value(((float)((w >> (8 * (m & 3))) & 255) - 128.0f) * ks);
-      y[m] = id < 0 ? 0.0f : fp32_value(((float)((v[m] >> (8 * i)) & 255) - 128.0f) * vs);
+      x[m] = fp32_value(((float)((w >> (8 * (m & 3))) & 255) - 128.0f) * ks);
+      y[m] = fp32_value(((float)((v[m] >> (8 * i)) & 255) - 128.0f) * vs);
     }
     const int64_t o = ((row0 + (base + t + i - first)) * c.Hkv + h) * c.D + d;
     store8((SO*)a.k_out + o, x);
@@ -471,13 +475,14 @@ void go_append(AppendArgs a, hipStream_t st) {
   const int64_t units = units_of(a.c.D, a.rot);
   const int64_t k_items = tokens * units, v_items = quads * (a.c.D / 4);
   const int64_t items = k_items > v_items ? k_items : v_items;
-  const int threads = items > 2048 ? 1024 : (int)((items + 1) / 2 + 63) / 64 * 64;
+  const bool wave = items <= 64;       // one token, or a few of a narrow head
+  const int threads = wave ? 256 : items > 2048 ? 1024 : (int)((items + 1) / 2 + 63) / 64 * 64;
   const int64_t eights = (pages + 7) / 8;
-  a.kv_blocks = (int)(eights * a.c.Hkv * 8);
+  a.kv_blocks = (int)(eights * (wave ? (a.c.Hkv + 3) / 4 : a.c.Hkv) * 8);
   a.q_parts = (int)((tokens * a.Hq * units + 4 * threads - 1) / (4 * threads));   // four units a thread
   if (a.q_parts > a.c.Hkv) a.q_parts = a.c.Hkv;
   const unsigned blocks = (unsigned)(a.kv_blocks + eights * a.q_parts * 8);
-  if (items <= threads) append_units_kernel<TI, TQ, 1><<<blocks, threads, 0, st>>>(a);   // one token
+  if (wave) append_units_kernel<TI, TQ, 1><<<blocks, threads, 0, st>>>(a);
   else if (items <= 2048) append_units_kernel<TI, TQ, 2><<<blocks, threads, 0, st>>>(a);
   else append_units_kernel<TI, TQ, 4><<<blocks, threads, 0, st>>>(a);
 }
