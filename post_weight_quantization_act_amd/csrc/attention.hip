@@ -796,12 +796,12 @@ struct Plan {
   int QT, NW, splits, tiles, row_tiles, tile_rows;
 };
 
-Plan plan(int64_t B, int Hq, int Hkv, int max_new, int max_len) {
+Plan plan(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
   Plan p;
   const int64_t rows = (int64_t)max_new * (Hq / Hkv);
   const int tiles = (max_len + kTile - 1) / kTile;
   p.shared = rows > 64;
-  p.QT = rows > 16 ? 2 : 1;
+  p.QT = rows > 16 && D <= 192 ? 2 : 1;    // wider heads' two row tiles do not fit the registers
   p.NW = 4;
   p.tile_rows = p.shared ? 32 * p.NW : 16 * p.QT;
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
@@ -856,7 +856,7 @@ void go_q(const AttArgs& a, const Plan& p, const Split& sp, unsigned grid, hipSt
   }
   if (p.QT == 1 && p.NW == 8) go_w<T, DB, 1, 8>(a, sp, grid, st);
   else if (p.QT == 1) go_w<T, DB, 1, 4>(a, sp, grid, st);
-  else go_w<T, DB, 2, 4>(a, sp, grid, st);
+  else if constexpr (DB <= 6) go_w<T, DB, 2, 4>(a, sp, grid, st);
 }
 
 template <class T>
@@ -887,7 +887,7 @@ hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) 
 
 size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
                              int max_len) {
-  const Plan p = plan(B, Hq, Hkv, max_new, max_len);
+  const Plan p = plan(B, Hq, Hkv, D, max_new, max_len);
   return p.splits == 1 ? 0 : (size_t)p.splits * T * Hq * (D + 2) * 4 + 4;
 }
 
@@ -896,11 +896,11 @@ int64_t kv_attention_blocks(int64_t T, int64_t B, int Hq, int Hkv, int D, int ma
   if (max_new > (int64_t)INT32_MAX / Hq) return INT64_MAX;
   const int64_t rows = (int64_t)max_new * Hq;
   if (B > INT32_MAX / rows) return INT64_MAX;
-  return plan(B, Hq, Hkv, max_new, max_len).blocks;
+  return plan(B, Hq, Hkv, D, max_new, max_len).blocks;
 }
 
 hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipStream_t st) {
-  const Plan p = plan(a.c.B, a.Hq, a.c.Hkv, a.max_new, a.max_len);
+  const Plan p = plan(a.c.B, a.Hq, a.c.Hkv, a.c.D, a.max_new, a.max_len);
   Split sp = {p.splits, p.tiles, p.row_tiles, nullptr, nullptr, nullptr};
   if (p.splits > 1) {
     sp.o = (float*)ws;

@@ -318,7 +318,7 @@ ATTENTION = [   # new rows, lengths, q heads, kv heads, D, page
     ([1], [1], 1, 1, 8, 16), ([1], [513], 32, 32, 128, 16), ([1, 1, 1, 1], [0, 1, 64, 777], 8, 1, 128, 64),
     ([1, 1], [1000, 65], 14, 2, 80, 32), ([1, 1, 1], [300, 40, 129], 32, 2, 64, 16), ([1], [515], 48, 2, 128, 128),
     ([1, 1], [700, 31], 4, 4, 256, 256), ([3, 0, 4], [130, 90, 4], 8, 2, 96, 32), ([70, 1, 33], [70, 200, 97], 6, 3, 128, 64),
-    ([129], [300], 2, 1, 40, 16), ([20, 5], [10, 5], 4, 2, 64, 16), ([65], [1100], 16, 2, 24, 32),
+    ([129], [300], 2, 1, 40, 16), ([5, 2], [333, 90], 16, 2, 256, 64), ([40], [150], 8, 2, 248, 16), ([80], [200], 1, 1, 192, 32), ([20, 5], [10, 5], 4, 2, 64, 16), ([65], [1100], 16, 2, 24, 32),
 ]
 
 
