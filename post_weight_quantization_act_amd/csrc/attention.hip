@@ -41,12 +41,12 @@ struct Split {
   int splits;        // workgroups along the tokens of one row tile
   int tiles;         // 64-token tiles of each; where `chosen` is set, the least, a power of two
   int row_tiles;     // row tiles of a sequence and kv head
+  int slots;         // workgroups that run at once
   float* o;          // [splits][T * Hq][D], null when splits == 1
   float2* rl;        // [splits][T * Hq]: reference and sum
   int* chosen;       // where the first kernel tells the second what it took for `tiles`; or null
 };
 
-constexpr int kSlots = 512;      // workgroups of attention_kernel that run at once, two on a compute unit
 constexpr int kChoices = 5;
 
 // 64-token tiles that the rows of a sequence see, so at least as many as any of its row
@@ -70,8 +70,8 @@ __device__ __forceinline__ int splits_of(int nt, int tiles_log) {
 // all lengths, takes for the tiles of a split the least power of two times sp.tiles
 // for which all splits run at once, or that is twice a slot's share of all tiles,
 // and finds its own split by counting: no workgroup but the last few is empty.
-// (A grid of sequences x most splits costs a round of two empty workgroups a
-// compute unit, about a microsecond, for every 512 of them.)
+// (A grid of sequences x most splits costs about a microsecond for every 512 empty ones:
+// registers let only two at a time onto a compute unit.)
 struct Unit2 {
   int tiles, b, split;    // b = -1: nothing is left for this workgroup
 };
@@ -112,7 +112,7 @@ __device__ __forceinline__ Unit2 choose(const AttArgs& a, const Split& sp, int w
     int units = 0;
     for (int w = 0; w < W; ++w) units += sums[w][k];
     take = log + k;
-    if (units * groups <= kSlots || ((int64_t)kSlots << take) >= 2 * all * groups) break;
+    if (units * groups <= sp.slots || ((int64_t)sp.slots << take) >= 2 * all * groups) break;
   }
   int before = 0;
   for (int b0 = 0; b0 < a.c.B && before <= want; b0 += THREADS) {
@@ -393,7 +393,7 @@ __device__ __forceinline__ void load_keys(const Finder& f, Keys<DB>& k, int2 e, 
 // NW waves share the tokens of one row tile (QT x 16 rows) and split; their
 // results meet in LDS.
 template <class T, int DB, int QT, int NW, bool W16>
-__global__ __launch_bounds__(NW * 64) void attention_kernel(AttArgs a, Split sp) {
+__global__ __launch_bounds__(NW * 64, DB <= 6 ? 2 : 1) void attention_kernel(AttArgs a, Split sp) {
   typedef typename T::storage S;
   constexpr int DT = 2 * DB;
   constexpr int kPitch = 32 * DB + 4;
@@ -793,6 +793,7 @@ struct Plan {
   bool shared;       // attention_rows_kernel
   bool chosen;       // the kernel chooses the tiles of a split
   int64_t blocks;
+  int slots;         // workgroups that run at once on 256 compute units
   int QT, NW, splits, tiles, row_tiles, tile_rows;
 };
 
@@ -806,6 +807,11 @@ Plan plan(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
   p.tile_rows = p.shared ? 32 * p.NW : 16 * p.QT;
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   const int64_t groups = B * Hkv * (int64_t)p.row_tiles;
+  const int wide = (D + 31) / 32;
+  // Two workgroups on a compute unit, one where the registers or LDS hold no more (256 columns,
+  // 8 sequences: 36 us with 256 against 60 with 512; counting the four that 64 columns
+  // would allow splits too finely, 21.6 against 19.0 us).
+  p.slots = 256 * (wide <= (p.shared || p.QT == 2 ? 4 : 6) ? 2 : 1);
   // Few short sequences: eight waves a workgroup and no second launch.
   if (p.QT == 1 && groups <= 256 && tiles <= 16) p.NW = 8;
   p.chosen = B > 1 && !p.shared && p.NW == 4 && tiles > 8;
@@ -813,12 +819,12 @@ Plan plan(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
     // lengths differ: the kernel chooses among kChoices powers of two, up to what all
     // sequences at their longest would take
     p.tiles = 8;
-    while (p.tiles << (kChoices - 1) < 2 * tiles * groups / kSlots && p.tiles < tiles) p.tiles *= 2;
+    while (p.tiles << (kChoices - 1) < 2 * tiles * groups / p.slots && p.tiles < tiles) p.tiles *= 2;
     while (tiles / p.tiles * groups > 8192) p.tiles *= 2;     // bounds the workspace
-    p.blocks = kSlots + groups;   // splits that run at once, or half of that and one for each sequence
+    p.blocks = p.slots + groups;   // splits that run at once, or half of that and one for each sequence
   } else {
-    // as many workgroups as run at once, two on a compute unit
-    int64_t want = groups >= kSlots ? 1 : kSlots / groups;
+    // as many workgroups as run at once
+    int64_t want = groups >= p.slots ? 1 : p.slots / groups;
     const int per = p.shared ? 1 : p.NW;   // tiles are dealt to a workgroup's waves, or shared by them
     const int64_t most = (tiles + 2 * p.NW - 1) / (2 * p.NW);
     want = want < most ? want : most;
@@ -901,7 +907,7 @@ int64_t kv_attention_blocks(int64_t T, int64_t B, int Hq, int Hkv, int D, int ma
 
 hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipStream_t st) {
   const Plan p = plan(a.c.B, a.Hq, a.c.Hkv, a.c.D, a.max_new, a.max_len);
-  Split sp = {p.splits, p.tiles, p.row_tiles, nullptr, nullptr, nullptr};
+  Split sp = {p.splits, p.tiles, p.row_tiles, p.slots, nullptr, nullptr, nullptr};
   if (p.splits > 1) {
     sp.o = (float*)ws;
     sp.rl = (float2*)(sp.o + (size_t)p.splits * a.c.T * a.Hq * a.c.D);
