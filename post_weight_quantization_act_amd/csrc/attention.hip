@@ -67,29 +67,26 @@ __device__ __forceinline__ int splits_of(int nt, int tiles_log) {
 }
 
 // Sequences differ in length and the host does not know them: every workgroup looks at
-// all lengths, takes for the tiles of a split the least power of two times sp.tiles
-// for which all splits run at once, or that is twice a slot's share of all tiles,
-// and finds its own split by counting: no workgroup but the last few is empty.
-// (A grid of sequences x most splits costs about a microsecond for every 512 empty ones:
-// registers let only two at a time onto a compute unit.)
-struct Unit2 {
+// all lengths (at most one a thread), takes for the tiles of a split the least power of
+// two times sp.tiles for which all splits run at once, or that is twice a slot's share
+// of all tiles, and finds its own split by counting: no workgroup but the last few is
+// empty.  (A grid of sequences x most splits costs about a microsecond for every 512
+// empty ones: registers let only two at a time onto a compute unit.)  64 sequences of
+// 1 to 8192 tokens, 8 heads: 29 us, against 33 with a fixed 20 tiles a split.
+struct Part {
   int tiles, b, split;    // b = -1: nothing is left for this workgroup
 };
 
 template <int THREADS>
-__device__ __forceinline__ Unit2 choose(const AttArgs& a, const Split& sp, int want) {
+__device__ __forceinline__ Part choose(const AttArgs& a, const Split& sp, int want) {
   constexpr int W = THREADS / 64;
   __shared__ int sums[W][kChoices + 1], scan[W], found[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int log = 31 - __builtin_clz(sp.tiles);
-  int count[kChoices] = {}, all = 0, first = -1;
-  for (int b = tid; b < a.c.B; b += THREADS) {
-    const int nt = tiles_of(a, b);
-    if (b == tid) first = nt;
-    all += nt > 0 ? nt : 0;
+  const int nt = tid < a.c.B ? tiles_of(a, tid) : -1;
+  int count[kChoices], all = nt > 0 ? nt : 0;
 #pragma unroll
-    for (int k = 0; k < kChoices; ++k) count[k] += splits_of(nt, log + k);
-  }
+  for (int k = 0; k < kChoices; ++k) count[k] = splits_of(nt, log + k);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) {
     all += __shfl_xor(all, m);
@@ -114,31 +111,22 @@ __device__ __forceinline__ Unit2 choose(const AttArgs& a, const Split& sp, int w
     take = log + k;
     if (units * groups <= sp.slots || ((int64_t)sp.slots << take) >= 2 * all * groups) break;
   }
-  int before = 0;
-  for (int b0 = 0; b0 < a.c.B && before <= want; b0 += THREADS) {
-    const int b = b0 + tid;
-    const int mine = b < a.c.B ? splits_of(b0 == 0 ? first : tiles_of(a, b), take) : 0;
-    int upto = mine;
+  const int mine = splits_of(nt, take);
+  int upto = mine;
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int x = __shfl_up(upto, m);
-      upto += lane >= m ? x : 0;
-    }
-    if (lane == 63) scan[wave] = upto;
-    __syncthreads();
-    for (int w = 0; w < W; ++w) {
-      if (w < wave) upto += scan[w];
-    }
-    const int at = want - before - (upto - mine);
-    if (at >= 0 && at < mine) {
-      found[0] = b;
-      found[1] = at;
-    }
-    int total = 0;
-    for (int w = 0; w < W; ++w) total += scan[w];
-    before += total;
-    __syncthreads();
+  for (int m = 1; m < 64; m <<= 1) {
+    const int x = __shfl_up(upto, m);
+    upto += lane >= m ? x : 0;
   }
+  if (lane == 63) scan[wave] = upto;
+  __syncthreads();
+  for (int w = 0; w < W; ++w) upto += w < wave ? scan[w] : 0;
+  const int at = want - (upto - mine);
+  if (at >= 0 && at < mine) {
+    found[0] = tid;
+    found[1] = at;
+  }
+  __syncthreads();
   return {1 << __builtin_amdgcn_readfirstlane(take), __builtin_amdgcn_readfirstlane(found[0]),
           __builtin_amdgcn_readfirstlane(found[1])};
 }
@@ -411,7 +399,7 @@ __global__ __launch_bounds__(NW * 64, DB <= 6 ? 2 : 1) void attention_kernel(Att
   bid /= c.Hkv;
   if (sp.chosen) {
     rt = bid % sp.row_tiles;
-    const Unit2 u = choose<NW * 64>(a, sp, bid / sp.row_tiles);
+    const Part u = choose<NW * 64>(a, sp, bid / sp.row_tiles);
     if (blockIdx.x == 0 && tid == 0) *sp.chosen = u.tiles;
     if (u.b < 0) return;
     sp.tiles = u.tiles;
@@ -540,6 +528,22 @@ __global__ __launch_bounds__(NW * 64, DB <= 6 ? 2 : 1) void attention_kernel(Att
   }
 }
 
+// The order of a block of N fragment reads that feed M matrix instructions each: four
+// reads ahead of their use (left alone, the compiler waits for each just before it;
+// 128 columns 470 -> 455 us for 2 x 2047 rows, eight ahead 463).  Narrow heads, whose
+// registers let three workgroups onto a compute unit, are 1% faster without.
+template <int N, int M>
+__device__ __forceinline__ void reads_ahead() {
+  constexpr int kAhead = N < 4 ? N : 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+  for (int i = 0; i < N - kAhead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, M * kAhead, 0);
+}
+
 // Many rows: NW waves of 32 rows each share every tile, which is turned into fp16
 // fragments in LDS once for all of them; two buffers and one barrier a tile.  Each wave
 // fetches its part of the codes a tile ahead into registers.
@@ -660,23 +664,19 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
     if (tile * kTile >= w_hi || tile * kTile + kTile <= w_lo) continue;
     const int tok = tile * kTile + 16 * g;
     f32x4 s[QT][4];
-    half8 k0[DB], k1[DB];
-#pragma unroll
-    for (int k = 0; k < DB; ++k) k0[k] = kf[buf][k][lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      half8 *now = i & 1 ? k1 : k0, *then = i & 1 ? k0 : k1;
-      if (i < 3)
-#pragma unroll
-        for (int k = 0; k < DB; ++k) then[k] = kf[buf][(i + 1) * DB + k][lane];
 #pragma unroll
       for (int qt = 0; qt < QT; ++qt) s[qt][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < DB; ++k)
+      for (int k = 0; k < DB; ++k) {
+        const half8 k8 = kf[buf][i * DB + k][lane];
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt)
-          s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now[k], w[qt].q[k], s[qt][i], 0, 0, 0);
+          s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w[qt].q[k], s[qt][i], 0, 0, 0);
+      }
     }
+    if constexpr (DB > 2) reads_ahead<4 * DB, QT>();
     half8 p[QT][2];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) probabilities<DB>(w[qt], s[qt], p[qt], st, tok);
@@ -684,11 +684,11 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
     for (int dt = 0; dt < DT; ++dt) {
       const half8 v0 = vf[buf][2 * dt][lane], v1 = vf[buf][2 * dt + 1][lane];
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
-        w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[qt][0], w[qt].o[dt], 0, 0, 0);
-        w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[qt][1], w[qt].o[dt], 0, 0, 0);
-      }
+      for (int qt = 0; qt < QT; ++qt) w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[qt][0], w[qt].o[dt], 0, 0, 0);
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) w[qt].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[qt][1], w[qt].o[dt], 0, 0, 0);
     }
+    if constexpr (DB > 2) reads_ahead<2 * DT, QT>();
   }
 
 #pragma unroll
@@ -814,7 +814,7 @@ Plan plan(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
   p.slots = 256 * (wide <= (p.shared || p.QT == 2 ? 4 : 6) ? 2 : 1);
   // Few short sequences: eight waves a workgroup and no second launch.
   if (p.QT == 1 && groups <= 256 && tiles <= 16) p.NW = 8;
-  p.chosen = B > 1 && !p.shared && p.NW == 4 && tiles > 8;
+  p.chosen = B > 1 && B <= 64 * p.NW && !p.shared && p.NW == 4 && tiles > 8;
   if (p.chosen) {
     // lengths differ: the kernel chooses among kChoices powers of two, up to what all
     // sequences at their longest would take
@@ -822,6 +822,10 @@ Plan plan(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
     while (p.tiles << (kChoices - 1) < 2 * tiles * groups / p.slots && p.tiles < tiles) p.tiles *= 2;
     while (tiles / p.tiles * groups > 8192) p.tiles *= 2;     // bounds the workspace
     p.blocks = p.slots + groups;   // splits that run at once, or half of that and one for each sequence
+  } else if (B > 64 * p.NW && !p.shared) {
+    // enough sequences to fill the chip: splits only bound what the longest take (16 tiles a
+    // wave, about 35 us), eight of them at most (the workspace)
+    p.tiles = tiles > 512 ? (tiles + 31) / 32 * 4 : 64;
   } else {
     // as many workgroups as run at once
     int64_t want = groups >= p.slots ? 1 : p.slots / groups;

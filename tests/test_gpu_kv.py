@@ -179,7 +179,8 @@ APPENDS = [   # new tokens of each sequence, tokens before, kv heads, q heads, D
     ([1], [0], 1, 1, 8, 8, 16), ([1], [15], 2, 8, 64, 64, 16), ([1, 1, 1], [16, 0, 37], 8, 8, 128, 128, 32),
     ([5, 0, 70], [3, 9, 60], 2, 4, 96, 48, 32), ([200], [0], 3, 0, 80, 80, 64), ([33, 1], [100, 255], 1, 7, 256, 64, 256),
     ([17, 16, 15], [15, 16, 17], 4, 4, 40, 24, 16), ([129], [127], 2, 2, 128, 128, 128),
-    ([64, 300], [64, 20], 1, 2, 72, 72, 64), ([3], [29], 2, 6, 24, 0, 32),
+    ([64, 300], [64, 20], 1, 2, 72, 72, 64), ([300, 256], [10, 0], 1, 1, 256, 256, 256),
+    ([250, 3], [255, 6], 1, 2, 256, 16, 256), ([3], [29], 2, 6, 24, 0, 32),
 ]
 
 
@@ -478,7 +479,7 @@ def test_attention_long_and_split():
 
 UNEVEN = [   # sequences, rows of each, shortest, longest, q heads, kv heads, D, page, window
     (3, 1, 1, 2300, 8, 2, 64, 64, 0), (300, 1, 0, 1100, 4, 1, 32, 16, 0), (40, 1, 700, 1500, 6, 6, 64, 128, 0),
-    (7, 3, 2, 1300, 16, 2, 40, 32, 0), (5, 2, 600, 1800, 24, 1, 128, 64, 900), (2, 45, 700, 1400, 4, 2, 64, 16, 0),
+    (7, 3, 2, 1300, 16, 2, 40, 32, 0), (5, 2, 600, 1800, 24, 1, 128, 64, 900), (2, 45, 700, 1400, 4, 2, 64, 16, 0), (256, 1, 1, 800, 2, 2, 16, 32, 0), (257, 2, 0, 5000, 2, 1, 8, 256, 4700),
     (1, 40, 2500, 2500, 4, 1, 64, 64, 0), (1, 33, 1100, 1100, 3, 1, 96, 64, 300), (600, 1, 0, 700, 1, 1, 16, 64, 0),
 ]
 
