@@ -13,18 +13,28 @@
 // multiple of 16 tokens, so those sixteen share one page, one key step and one
 // value step.
 //
-// Codes become fp16 exactly: the byte u under 0x64 reads 1024 + u.  For the
-// scores the surplus, 1152 sum_d q_d, goes into the constant of the multiply-add
-// before the exponential; for the values 1152 is subtracted (a packed fp16
-// operation, exact).  Queries are scaled
-// by a power of two of their row to |q| < 2 and are exact in fp16 but for bf16
-// elements more than 2^-14 below their row's largest, which keep 24 bits below 1.
+// Codes become fp16 exactly: the byte u under 0x64 reads 1024 + u, and a packed
+// subtraction of 1152 leaves u - 128.  (Scores could keep the surplus and subtract 1152
+// sum_d q_d at the end: 64 instructions fewer a tile, no faster where memory bounds
+// the kernel, and ten times the rounding, which shows in the lse of short rows.)
+// Queries are scaled by a power of two of their row to |q| < 2 and are exact in fp16
+// but for bf16 elements more than 2^-14 below their row's largest, which keep 24 bits
+// below 1.
 //
 // With t = log2 of (weight times value step), one reference R for each row serves
 // sums and values: p = exp2(t - R) weighs the codes, and the row's sum adds
 // p / step once for sixteen tokens, in fp32.  p is rounded to fp16 for the matrix
 // cores; R follows the largest t so that p stays below 2^15 and above 2^-14 with
 // full precision for everything within 2^-22 of the row's largest contribution.
+//
+// attention_kernel: few rows.  Bound by memory where the cache is long: one sequence of
+// 131071 tokens, 64 heads over 8, 53 us (5.1 TB/s, cold) and 5 us to join; by the latency of a
+// tile (2.3 us a wave: values, scores, exponentials, values' product) where sequences are
+// short or uneven: 64 of 1 to 8192 tokens 33 + 5 us; one of 513 tokens, 32 heads 8.5 us.
+// attention_rows_kernel: many rows, bound by neither unit alone: 2 x 2047 rows of 64 heads
+// over 3000 and 4096 tokens 455 us, 745 TFLOP/s (a large fp16 matrix product reaches 1140 to
+// 1180 here); the matrix units are busy 29% and the vector units 50% of the time, 1.5 waves
+// a SIMD on average.
 #include "kv.h"
 
 namespace awq {
@@ -145,27 +155,21 @@ __device__ __forceinline__ float xor_sum(float x) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// Eight codes as fp16 values 1024 + u.
-__device__ __forceinline__ half8 surplus(uint32_t lo, uint32_t hi) {
+// Eight codes as fp16 values u - 128.
+__device__ __forceinline__ half8 centred(uint32_t lo, uint32_t hi) {
   struct { uint32_t v[4]; } r;
   r.v[0] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u);
   r.v[1] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u);
   r.v[2] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u);
   r.v[3] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u);
-  return __builtin_bit_cast(half8, r);
-}
-
-// Eight codes as fp16 values u - 128.
-__device__ __forceinline__ half8 centred(uint32_t lo, uint32_t hi) {
   const half8 less = {1152, 1152, 1152, 1152, 1152, 1152, 1152, 1152};
-  return surplus(lo, hi) - less;
+  return __builtin_bit_cast(half8, r) - less;
 }
 
 // One row tile's queries, bounds and running state.
 template <int DB>
 struct Rows {
   half8 q[DB];       // 8 columns of each 32-block
-  float bias;        // -1152 sum q
   float f;           // scale log2(e) 2^e of the row
   int lo, hi;        // tokens that the row sees
   float r, l;        // reference, this lane's share of the sum
@@ -211,16 +215,10 @@ __device__ __forceinline__ void load_rows(const AttArgs& a, Rows<DB>& w, int64_t
   float m = xor_max(__uint_as_float(top > 0x7f7fffffu ? 0x3f800000u : top));
   int e = (int)(__float_as_uint(m) >> 23) - 127;
   e = m == 0.0f ? 0 : e;
-  float sum = 0.0f;
 #pragma unroll
   for (int ks = 0; ks < DB; ++ks)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const _Float16 v = (_Float16)ldexpf(x[ks][j], -e);
-      w.q[ks][j] = v;
-      sum += (float)v;
-    }
-  w.bias = -1152.0f * xor_sum(sum);
+    for (int j = 0; j < 8; ++j) w.q[ks][j] = (_Float16)ldexpf(x[ks][j], -e);
   w.f = ldexpf(a.scale * kLog2e, e);
 }
 
@@ -266,8 +264,7 @@ __device__ __forceinline__ void probabilities(Rows<DB>& r, f32x4 (&s)[4], half8 
     for (int j = 0; j < 4; ++j) top = fmaxf(top, s[i][j]);
   // a factor of 0 would make NaN of the -inf of tokens that are not seen
   const float fp = f < kLeastFactor ? kLeastFactor : f;
-  const float surplus_off = lg + r.bias * fp;
-  top = xor_max(fmaf(top, fp, surplus_off));
+  top = xor_max(fmaf(top, fp, lg));
   if (__any(top > r.r + kTop)) {
     const float to = top > r.r + kTop ? top - kRest : r.r;
     const float by = to == r.r ? 1.0f : __builtin_amdgcn_exp2f(r.r - to);
@@ -276,7 +273,7 @@ __device__ __forceinline__ void probabilities(Rows<DB>& r, f32x4 (&s)[4], half8 
 #pragma unroll
     for (int dt = 0; dt < 2 * DB; ++dt) r.o[dt] *= by;
   }
-  const float off = surplus_off - (r.r == -INFINITY ? 0.0f : r.r);
+  const float off = lg - (r.r == -INFINITY ? 0.0f : r.r);
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -460,7 +457,7 @@ __global__ __launch_bounds__(NW * 64, DB <= 6 ? 2 : 1) void attention_kernel(Att
 #pragma unroll
       for (int ks = 0; ks < DB; ++ks) {
         const u32x4 raw = kt.k[i][ks >> 1];
-        const half8 k8 = surplus(raw[2 * (ks & 1)], raw[2 * (ks & 1) + 1]);
+        const half8 k8 = centred(raw[2 * (ks & 1)], raw[2 * (ks & 1) + 1]);
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt)
           s[qt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w[qt].q[ks], s[qt][i], 0, 0, 0);
@@ -630,10 +627,10 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
       const int u = wave + k * NW;
       if (KU % NW != 0 && u >= KU) break;
       if (W16) {
-        kf[buf][2 * u][lane] = surplus(kr[k][0], kr[k][1]);
-        kf[buf][2 * u + 1][lane] = surplus(kr[k][2], kr[k][3]);
+        kf[buf][2 * u][lane] = centred(kr[k][0], kr[k][1]);
+        kf[buf][2 * u + 1][lane] = centred(kr[k][2], kr[k][3]);
       } else {
-        kf[buf][u][lane] = surplus(kr[k][0], kr[k][1]);
+        kf[buf][u][lane] = centred(kr[k][0], kr[k][1]);
       }
     }
 #pragma unroll

@@ -134,6 +134,13 @@ __device__ __forceinline__ Steps steps_after(const Place& p, float k_was, float 
 //
 // Workgroups are dealt to the eight XCDs in turn: page number modulo 8 is the lowest
 // digit, so the heads of a page, which turn by the same rows of the table, share an L2.
+//
+// 20005 tokens of 8 heads, 128 columns, pages of 64, bf16: 47 us with caches cold (123 MB
+// of rows and codes and 10 MB of table, 2.8 TB/s), 37 warm; bound by the latency of load,
+// largest, quotients, store in each workgroup, whose phases only other workgroups
+// hide; with a division for each code 51 us, values' codes stored in the rows' order
+// 51, one pair a thread 147.  One token of 192 sequences x 32 heads: 13.5 us, a chain
+// of length, page, row and table loads; of one sequence 6.7 us.
 template <class TI, class TQ, int HOLD>
 __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   typedef typename TI::storage SI;
@@ -299,7 +306,7 @@ __device__ __forceinline__ void load_pair(const AppendArgs& a, const S* x, int64
   rotate(x1, x2, cs.x, cs.y);
 }
 
-// Any rot: pairs one by one, read twice.
+// Any rot: pairs one by one, the rows read twice (20005 tokens as above 147 us).
 template <class TI, class TQ>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   typedef typename TI::storage SI;
@@ -411,7 +418,9 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
 
 // A thread takes four tokens by eight columns.  The values' four tokens are one
 // dword of a column, so eight dwords and no transposition give four rows of
-// eight; a workgroup runs over the heads of a page.
+// eight; a workgroup runs over the heads of a page.  Bound by memory: 32760 tokens of
+// 8 heads, 128 columns, to fp16 42 us, 4.8 TB/s, the rate of a copy (83 us with a value a
+// thread).
 template <class TO>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) {
   typedef typename TO::storage SO;

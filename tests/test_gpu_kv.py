@@ -325,11 +325,11 @@ ATTENTION = [   # new rows, lengths, q heads, kv heads, D, page
 
 def attention_bound(ref, q, scale, spread, top, out, kind, dim):
     """What the roundings of the kernel can make: the output's own, fp16 probabilities (half an ulp each,
-    numerator alone), and scores whose products sum_d q_d u_d (u <= 255, or 1024 + u) carry fp32 roundings:
+    numerator alone), and scores whose products sum_d q_d c_d (|c| <= 127, exact) carry fp32 roundings:
     (dim / 8 + 4) of the partial sums' size, an absolute error that a probability takes relatively
     (twice: numerator and denominator)."""
     step = top / 127
-    score = (dim / 8 + 4) * 2.0 ** -24 * 1280 * np.abs(q).sum(-1) * scale * step
+    score = (dim / 8 + 4) * 2.0 ** -24 * 127 * np.abs(q).sum(-1) * scale * step
     score = score + 8 * 2.0 ** -24 * (np.abs(q).sum(-1) * scale * top + 1)
     rel = 2.0 ** -11 + 2 * np.expm1(2 * score) + 2.0 ** -18
     return score, HALF_ULP[kind] * np.abs(out) + rel[..., None] * spread + TINY[kind]
