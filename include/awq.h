@@ -544,8 +544,9 @@ awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, 
  *   q [T, Hq, D] of dtype (AWQ_F16 or AWQ_BF16; strides q_strides[2]), out [T,
  *   Hq, D] dense of dtype.  A row that sees no token gives 0 and -inf.  Scores,
  *   sums and outputs are held in fp32; probabilities are rounded to fp16
- *   before they weigh the values; a value step below 2^-100 counts as 0.  scale finite and >= 0.  Results are
- *   reproducible.  workspace: awq_kv_attention_workspace_size(T, B, Hq,
+ *   before they weigh the values; a value step below 2^-100 counts as 0.  scale
+ *   finite and >= 0.  Rows that belong to no sequence are not written.  Results
+ *   are reproducible.  workspace: awq_kv_attention_workspace_size(T, B, Hq,
  *   kv_heads, D, max_new, max_len) bytes, 256-byte aligned, may be NULL when that is 0.
  * ------------------------------------------------------------------------ */
 typedef struct {

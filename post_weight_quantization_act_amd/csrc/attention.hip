@@ -28,11 +28,11 @@
 // full precision for everything within 2^-22 of the row's largest contribution.
 //
 // attention_kernel: few rows.  Bound by memory where the cache is long: one sequence of
-// 131071 tokens, 64 heads over 8, 53 us (5.1 TB/s, cold) and 5 us to join; by the latency of a
+// 131071 tokens, 64 heads over 8, 52 us (5.2 TB/s, cold) and 5 us to join; by the latency of a
 // tile (2.3 us a wave: values, scores, exponentials, values' product) where sequences are
 // short or uneven: 64 of 1 to 8192 tokens 33 + 5 us; one of 513 tokens, 32 heads 8.5 us.
 // attention_rows_kernel: many rows, bound by neither unit alone: 2 x 2047 rows of 64 heads
-// over 3000 and 4096 tokens 455 us, 745 TFLOP/s (a large fp16 matrix product reaches 1140 to
+// over 3000 and 4096 tokens 462 us, 733 TFLOP/s (a large fp16 matrix product reaches 1140 to
 // 1180 here); the matrix units are busy 29% and the vector units 50% of the time, 1.5 waves
 // a SIMD on average.
 #include "kv.h"
