@@ -951,9 +951,10 @@ awq_status_t awq_kv_append(const awq_kv_cache_t* cache, const void* k, const voi
   a.rot = rot;
   a.interleaved = (flags & AWQ_ROPE_INTERLEAVED) != 0;
   a.Hq = (int)Hq;
+  a.q_type = q ? q_out_dtype : AWQ_F32;
   a.max_new = (int)max_new;
   a.pages_per_seq = (int)((max_new + a.c.P - 2) / a.c.P + 1);
-  hipError_t e = awq::launch_kv_append(a, dtype, q ? q_out_dtype : AWQ_F32, stream);
+  hipError_t e = awq::launch_kv_append(a, dtype, stream);
   if (e != hipSuccess) return hip_fail(e, "kv_append launch");
   return AWQ_OK;
   AWQ_GUARD_END

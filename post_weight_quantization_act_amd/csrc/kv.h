@@ -58,29 +58,31 @@ __device__ __forceinline__ void rotate(float& x1, float& x2, float c, float s) {
   x2 = fp32_value(y2);
 }
 
-// A unit is sixteen values of a head in two runs of eight columns: eight pairs
-// (half layout: columns 8 u and rot/2 + 8 u; interleaved: 16 u), or, past rot, columns
-// that are not turned, where the second run may be missing.  Needs rot % 16 == 0
-// and D % 8 == 0.  Runs are read and written as vectors of any alignment.
+// A unit is W pairs of a head in two runs of W columns (half layout: columns W u and
+// rot/2 + W u; interleaved: 2 W u), or, past rot, columns that are not turned, where the
+// second run may be missing.  W = 8 needs rot % 16 == 0, W = 4 rot % 8 == 0, both D % 8 == 0.
+// Runs are read and written as vectors of any alignment.
 struct Unit {
   int d0, d1;
   bool turn, two;
 };
 
+template <int W>
 __host__ __device__ __forceinline__ int units_of(int D, int rot) {
-  return rot / 16 + (D - rot + 15) / 16;
+  return rot / (2 * W) + (D - rot + 2 * W - 1) / (2 * W);
 }
 
+template <int W>
 __device__ __forceinline__ Unit unit_of(int D, int rot, int interleaved, int u) {
   Unit r;
-  r.turn = u < rot / 16;
+  r.turn = u < rot / (2 * W);
   if (r.turn) {
-    r.d0 = interleaved ? 16 * u : 8 * u;
-    r.d1 = interleaved ? 16 * u + 8 : rot / 2 + 8 * u;
+    r.d0 = interleaved ? 2 * W * u : W * u;
+    r.d1 = interleaved ? 2 * W * u + W : rot / 2 + W * u;
     r.two = true;
   } else {
-    r.d0 = 16 * u;
-    r.d1 = 16 * u + 8;
+    r.d0 = 2 * W * u;
+    r.d1 = 2 * W * u + W;
     r.two = r.d1 < D;
   }
   return r;
@@ -88,71 +90,73 @@ __device__ __forceinline__ Unit unit_of(int D, int rot, int interleaved, int u) 
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_loose __attribute__((aligned(2)));   // any element's address: the caller's strides
+typedef u32x2 u32x2_loose __attribute__((aligned(2)));   // any element's address: the caller's strides
+typedef u32x4 u32x4_loose __attribute__((aligned(2)));
 typedef f32x4 f32x4_loose __attribute__((aligned(4)));
 
-typedef u32x2 u32x2_loose __attribute__((aligned(2)));
+template <int W, class S> struct Run { S v[W]; };
 
-template <class S> struct Four { S v[4]; };
-template <class S> struct Eight { S v[8]; };
-
-template <class S> __device__ __forceinline__ Four<S> load4(const S* p) {
-  return __builtin_bit_cast(Four<S>, *(const u32x2_loose*)p);
-}
-template <> __device__ __forceinline__ Four<float> load4(const float* p) {
-  return __builtin_bit_cast(Four<float>, *(const f32x4_loose*)p);
-}
-
-template <class S> __device__ __forceinline__ Eight<S> load8(const S* p) {
-  return __builtin_bit_cast(Eight<S>, *(const u32x4_loose*)p);
-}
-template <> __device__ __forceinline__ Eight<float> load8(const float* p) {
-  struct { f32x4 a, b; } r = {*(const f32x4_loose*)p, *(const f32x4_loose*)(p + 4)};
-  return __builtin_bit_cast(Eight<float>, r);
-}
-template <class S> __device__ __forceinline__ void store8(S* p, const float* x) {
-  Eight<S> r;
+template <int W, class S> __device__ __forceinline__ Run<W, S> load_run(const S* p) {
+  if constexpr (sizeof(S) == 4) {
+    struct { f32x4 v[W / 4]; } r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = from_f32<S>(x[i]);
-  *(u32x4_loose*)p = __builtin_bit_cast(u32x4, r);
+    for (int i = 0; i < W / 4; ++i) r.v[i] = *(const f32x4_loose*)(p + 4 * i);
+    return __builtin_bit_cast(Run<W, S>, r);
+  } else if constexpr (W == 8) {
+    return __builtin_bit_cast(Run<W, S>, *(const u32x4_loose*)p);
+  } else {
+    return __builtin_bit_cast(Run<W, S>, *(const u32x2_loose*)p);
+  }
 }
-template <> __device__ __forceinline__ void store8(float* p, const float* x) {
-  *(f32x4_loose*)p = f32x4{x[0], x[1], x[2], x[3]};
-  *(f32x4_loose*)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
-}
-template <class S> __device__ __forceinline__ void widen(const Eight<S>& r, float* x) {
+template <int W, class S> __device__ __forceinline__ void store_run(S* p, const float* x) {
+  if constexpr (sizeof(S) == 4) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_f32(r.v[i]);
+    for (int i = 0; i < W; i += 4) *(f32x4_loose*)(p + i) = f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+  } else {
+    Run<W, S> r;
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.v[i] = from_f32<S>(x[i]);
+    if constexpr (W == 8) *(u32x4_loose*)p = __builtin_bit_cast(u32x4, r);
+    else *(u32x2_loose*)p = __builtin_bit_cast(u32x2, r);
+  }
+}
+template <int W, class S> __device__ __forceinline__ void widen(const Run<W, S>& r, float* x) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) x[i] = to_f32(r.v[i]);
 }
 
-// cos and sin of a unit's eight pairs.
+// cos and sin of a unit's pairs.
+template <int W>
 struct Turns {
-  float2 cs[8];
+  float2 cs[W];
 };
-__device__ __forceinline__ Turns turns_at(const float* table, int64_t n_pos, int half, int64_t pos, int u) {
-  Turns t;
+template <int W>
+__device__ __forceinline__ Turns<W> turns_at(const float* table, int64_t n_pos, int half, int64_t pos,
+                                             int u) {
+  Turns<W> t;
   const bool in = pos >= 0 && pos < n_pos;
-  const float* p = table + 2 * ((in ? pos : 0) * half + 8 * u);
+  const float* p = table + 2 * ((in ? pos : 0) * half + W * u);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < W / 2; ++i) {
     const f32x4 v = *(const f32x4_loose*)(p + 4 * i);
     t.cs[2 * i] = make_float2(v[0], v[1]);
     t.cs[2 * i + 1] = make_float2(v[2], v[3]);
   }
   if (!in) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t.cs[i] = make_float2(__builtin_nanf(""), __builtin_nanf(""));
+    for (int i = 0; i < W; ++i) t.cs[i] = make_float2(__builtin_nanf(""), __builtin_nanf(""));
   }
   return t;
 }
 
-__device__ __forceinline__ void turn_unit(float* m0, float* m1, const Turns& t, int interleaved,
+template <int W>
+__device__ __forceinline__ void turn_unit(float* m0, float* m1, const Turns<W>& t, int interleaved,
                                           bool transpose) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < W; ++i) {
     const float s = transpose ? -t.cs[i].y : t.cs[i].y;
     if (interleaved) {
-      float* m = i < 4 ? m0 + 2 * i : m1 + 2 * (i - 4);
+      float* m = i < W / 2 ? m0 + 2 * i : m1 + 2 * (i - W / 2);
       rotate(m[0], m[1], t.cs[i].x, s);
     } else {
       rotate(m0[i], m1[i], t.cs[i].x, s);
@@ -210,6 +214,7 @@ struct AppendArgs {
   int64_t n_pos;
   int rot, interleaved, Hq, pages_per_seq, max_new;
   int kv_blocks, q_parts;        // the launch's own
+  awq_dtype_t q_type;            // of q_out
 };
 
 struct ReadArgs {
@@ -245,7 +250,7 @@ __device__ __forceinline__ void seen_by(const AttArgs& a, int len, int n, int i,
 hipError_t launch_rope_table(int64_t n_pos, int rot, const RopeFreqs& fr, float* table,
                              hipStream_t st);
 hipError_t launch_rope(const RopeArgs& a, awq_dtype_t in, awq_dtype_t out, hipStream_t st);
-hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, awq_dtype_t q_out, hipStream_t st);
+hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, hipStream_t st);
 hipError_t launch_kv_read(const ReadArgs& a, awq_dtype_t out, hipStream_t st);
 size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
                              int max_len);

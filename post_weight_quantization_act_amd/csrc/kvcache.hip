@@ -126,10 +126,23 @@ __device__ __forceinline__ Steps steps_after(const Place& p, float k_was, float 
   return s;
 }
 
-// rot % 16 == 0 (or no table).  A workgroup takes a page and head's keys and values, or
+// Turned queries leave in their own type (the same for a whole call).
+template <int W>
+__device__ __forceinline__ void store_query(const AppendArgs& a, int64_t at, const float* x) {
+  if (a.q_type == AWQ_F16) store_run<W>((_Float16*)a.q_out + at, x);
+  else if (a.q_type == AWQ_BF16) store_run<W>((__bf16*)a.q_out + at, x);
+  else store_run<W>((float*)a.q_out + at, x);
+}
+__device__ __forceinline__ void store_query(const AppendArgs& a, int64_t at, float x) {
+  if (a.q_type == AWQ_F16) ((_Float16*)a.q_out)[at] = from_f32<_Float16>(x);
+  else if (a.q_type == AWQ_BF16) ((__bf16*)a.q_out)[at] = from_f32<__bf16>(x);
+  else ((float*)a.q_out)[at] = x;
+}
+
+// rot % 8 == 0 (or no table).  A workgroup takes a page and head's keys and values, or
 // (blocks from a.kv_blocks on) a part of the queries of a page's tokens.  The turned
 // keys and the values stay in registers between the search for the largest and the
-// rounding: HOLD units of sixteen keys, or patches of four tokens by four columns of
+// rounding: HOLD units of 2 W keys, or patches of four tokens by four columns of
 // values, a thread.
 //
 // Workgroups are dealt to the eight XCDs in turn: page number modulo 8 is the lowest
@@ -141,10 +154,9 @@ __device__ __forceinline__ Steps steps_after(const Place& p, float k_was, float 
 // hide; with a division for each code 51 us, values' codes stored in the rows' order
 // 51, one pair a thread 147.  One token of 192 sequences x 32 heads: 13.5 us, a chain
 // of length, page, row and table loads; of one sequence 6.7 us.
-template <class TI, class TQ, int HOLD>
+template <class TI, int W, int HOLD>
 __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   typedef typename TI::storage SI;
-  typedef typename TQ::storage SQ;
   __shared__ uint2 red[16];
   const KvArgs& c = a.c;
   constexpr bool kWave = HOLD == 1;   // one token: a wave takes a head, a workgroup four
@@ -158,24 +170,24 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   const int j = (int)(at % (uint32_t)a.pages_per_seq), b = (int)(at / (uint32_t)a.pages_per_seq);
   Place p;
   if (!find_place(a, b, j, p)) return;
-  const int units = units_of(c.D, a.rot), tokens = p.hi - p.lo, half = a.rot >> 1;
+  const int units = units_of<W>(c.D, a.rot), tokens = p.hi - p.lo, half = a.rot >> 1;
 
   if (queries) {
     const int work = tokens * a.Hq * units, step = blockDim.x;
     for (int e = part * step + threadIdx.x; e < work; e += a.q_parts * step) {
       const int u = e % units, r = e / units, hq = r % a.Hq;
       const int64_t row = p.row_lo + r / a.Hq;
-      const Unit w = unit_of(c.D, a.rot, a.interleaved, u);
+      const Unit w = unit_of<W>(c.D, a.rot, a.interleaved, u);
       const SI* x = (const SI*)a.q + row * a.qs[0] + hq * a.qs[1];
-      float x0[8], x1[8];
-      widen(load8(x + w.d0), x0);
-      widen(load8(x + (w.two ? w.d1 : w.d0)), x1);
+      float x0[W], x1[W];
+      widen(load_run<W>(x + w.d0), x0);
+      widen(load_run<W>(x + (w.two ? w.d1 : w.d0)), x1);
       if (w.turn)
-        turn_unit(x0, x1, turns_at(a.table, a.n_pos, half, position_of(a, p, row), u),
-                  a.interleaved, false);
-      SQ* y = (SQ*)a.q_out + (row * a.Hq + hq) * c.D;
-      store8(y + w.d0, x0);
-      if (w.two) store8(y + w.d1, x1);
+        turn_unit<W>(x0, x1, turns_at<W>(a.table, a.n_pos, half, position_of(a, p, row), u),
+                     a.interleaved, false);
+      const int64_t y = (row * a.Hq + hq) * c.D;
+      store_query<W>(a, y + w.d0, x0);
+      if (w.two) store_query<W>(a, y + w.d1, x1);
     }
     return;
   }
@@ -202,13 +214,13 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
       for (int i = 0; i < 4; ++i) {
         const bool in = t + i >= p.lo && t + i < p.hi;
         const SI* x = v_rows + (p.row_lo + (in ? t + i - p.lo : 0)) * a.vs[0] + 4 * d;
-        const Four<SI> r = load4(x);
+        const Run<4, SI> r = load_run<4>(x);
 #pragma unroll
         for (int m = 0; m < 4; ++m) v[k][i][m] = in ? r.v[m] : (SI)0.0f;
       }
     }
   }
-  float x0[HOLD][8], x1[HOLD][8];
+  float x0[HOLD][W], x1[HOLD][W];
   uint32_t km = 0;
   const SI* k_rows = (const SI*)a.k + h * a.ks[1];
 #pragma unroll
@@ -217,15 +229,15 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
     if (e < tokens * units) {
       const int u = e % units;
       const int64_t row = p.row_lo + e / units;
-      const Unit w = unit_of(c.D, a.rot, a.interleaved, u);
+      const Unit w = unit_of<W>(c.D, a.rot, a.interleaved, u);
       const SI* x = k_rows + row * a.ks[0];
-      widen(load8(x + w.d0), x0[k]);
-      widen(load8(x + (w.two ? w.d1 : w.d0)), x1[k]);
+      widen(load_run<W>(x + w.d0), x0[k]);
+      widen(load_run<W>(x + (w.two ? w.d1 : w.d0)), x1[k]);
       if (w.turn)
-        turn_unit(x0[k], x1[k], turns_at(a.table, a.n_pos, half, position_of(a, p, row), u),
-                  a.interleaved, false);
+        turn_unit<W>(x0[k], x1[k], turns_at<W>(a.table, a.n_pos, half, position_of(a, p, row), u),
+                     a.interleaved, false);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) km = umax(km, umax(abs_bits(x0[k][i]), abs_bits(x1[k][i])));
+      for (int i = 0; i < W; ++i) km = umax(km, umax(abs_bits(x0[k][i]), abs_bits(x1[k][i])));
     }
   }
 #pragma unroll
@@ -249,12 +261,14 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   for (int k = 0; k < HOLD; ++k) {
     const int e = tid + k * threads;
     if (e < tokens * units) {
-      const Unit w = unit_of(c.D, a.rot, a.interleaved, e % units);
+      const Unit w = unit_of<W>(c.D, a.rot, a.interleaved, e % units);
       uint8_t* y = kc + (p.lo + e / units) * c.D;
       const float *m = x0[k], *n = x1[k];
-      *(u32x2*)(y + w.d0) = u32x2{key.four(m[0], m[1], m[2], m[3]), key.four(m[4], m[5], m[6], m[7])};
-      if (w.two)
-        *(u32x2*)(y + w.d1) = u32x2{key.four(n[0], n[1], n[2], n[3]), key.four(n[4], n[5], n[6], n[7])};
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        *(uint32_t*)(y + w.d0 + i) = key.four(m[i], m[i + 1], m[i + 2], m[i + 3]);
+        if (w.two) *(uint32_t*)(y + w.d1 + i) = key.four(n[i], n[i + 1], n[i + 2], n[i + 3]);
+      }
     }
   }
   // values: the dwords that hold older tokens, then the new ones over what of the last
@@ -306,11 +320,11 @@ __device__ __forceinline__ void load_pair(const AppendArgs& a, const S* x, int64
   rotate(x1, x2, cs.x, cs.y);
 }
 
-// Any rot: pairs one by one, the rows read twice (20005 tokens as above 147 us).
-template <class TI, class TQ>
+// Any rot, and prompts into pages of 256 tokens of more than 128 columns (more than a
+// workgroup's registers hold): pairs one by one, the rows read twice (20005 tokens as above 147 us).
+template <class TI>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   typedef typename TI::storage SI;
-  typedef typename TQ::storage SQ;
   __shared__ uint2 red[kThreads / 64];
   const KvArgs& c = a.c;
   int g = blockIdx.x;
@@ -331,18 +345,18 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
       const int u = e % units, r = e / units, hq = h * G + r % G;
       const int64_t row = row_lo + r / G;
       const SI* x = (const SI*)a.q + row * a.qs[0] + hq * a.qs[1];
-      SQ* y = (SQ*)a.q_out + (row * a.Hq + hq) * c.D;
+      const int64_t y = (row * a.Hq + hq) * c.D;
       if (u >= half) {
         const int d = a.rot + (u - half);
-        y[d] = from_f32<SQ>(to_f32(x[d]));
+        store_query(a, y + d, to_f32(x[d]));
         continue;
       }
       const int64_t pos = position_of(a, p, row);
       int i1, i2;
       float x1, x2;
       load_pair(a, x, pos, u, i1, i2, x1, x2);
-      y[i1] = from_f32<SQ>(x1);
-      y[i2] = from_f32<SQ>(x2);
+      store_query(a, y + i1, x1);
+      store_query(a, y + i2, x2);
     }
   }
 
@@ -465,25 +479,24 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) 
       y[m] = fp32_value(((float)((v[m] >> (8 * i)) & 255) - 128.0f) * vs);
     }
     const int64_t o = ((row0 + (base + t + i - first)) * c.Hkv + h) * c.D + d;
-    store8((SO*)a.k_out + o, x);
-    store8((SO*)a.v_out + o, y);
+    store_run<8>((SO*)a.k_out + o, x);
+    store_run<8>((SO*)a.v_out + o, y);
   }
 }
 
-template <class TI, class TQ>
-void go_append(AppendArgs a, hipStream_t st) {
+// Units of W pairs, if a workgroup's registers hold a page's.
+template <class TI, int W>
+bool go_units(AppendArgs a, hipStream_t st) {
   const int64_t pages = (int64_t)a.pages_per_seq * a.c.B;
-  if (a.rot % 16 != 0) {
-    append_kernel<TI, TQ><<<(unsigned)(pages * a.c.Hkv), kThreads, 0, st>>>(a);
-    return;
-  }
-  // as many threads as hold a page's new tokens: two units or patches each, four where
-  // a page has more than 2 x 1024 (256 tokens of more than 128 columns)
+  // as many threads as hold a page's new tokens: two units or patches each, four units of
+  // four pairs where a page has more than 2 x 1024.  Four units of eight pairs and four
+  // patches are more than the 128 registers that 1024 threads have each.
   const int64_t tokens = a.max_new < a.c.P ? a.max_new : a.c.P;
   const int64_t quads = (tokens + 6) / 4 < a.c.P / 4 ? (tokens + 6) / 4 : a.c.P / 4;
-  const int64_t units = units_of(a.c.D, a.rot);
+  const int64_t units = units_of<W>(a.c.D, a.rot);
   const int64_t k_items = tokens * units, v_items = quads * (a.c.D / 4);
   const int64_t items = k_items > v_items ? k_items : v_items;
+  if (items > (W == 8 ? 2048 : 4096)) return false;
   const bool wave = items <= 64;       // one token, or a few of a narrow head
   const int threads = wave ? 256 : items > 2048 ? 1024 : (int)((items + 1) / 2 + 63) / 64 * 64;
   const int64_t eights = (pages + 7) / 8;
@@ -491,27 +504,29 @@ void go_append(AppendArgs a, hipStream_t st) {
   a.q_parts = (int)((tokens * a.Hq * units + 4 * threads - 1) / (4 * threads));   // four units a thread
   if (a.q_parts > a.c.Hkv) a.q_parts = a.c.Hkv;
   const unsigned blocks = (unsigned)(a.kv_blocks + eights * a.q_parts * 8);
-  if (wave) append_units_kernel<TI, TQ, 1><<<blocks, threads, 0, st>>>(a);
-  else if (items <= 2048) append_units_kernel<TI, TQ, 2><<<blocks, threads, 0, st>>>(a);
-  else append_units_kernel<TI, TQ, 4><<<blocks, threads, 0, st>>>(a);
+  if (wave) append_units_kernel<TI, W, 1><<<blocks, threads, 0, st>>>(a);
+  else if (W == 8 || items <= 2048) append_units_kernel<TI, W, 2><<<blocks, threads, 0, st>>>(a);
+  else append_units_kernel<TI, 4, 4><<<blocks, threads, 0, st>>>(a);
+  return true;
 }
 
 template <class TI>
-hipError_t go_append_q(const AppendArgs& a, awq_dtype_t q_out, hipStream_t st) {
+hipError_t go_append(const AppendArgs& a, hipStream_t st) {
   ProfScope prof("awq_kv_append", st);
-  if (q_out == AWQ_F32) go_append<TI, F32T>(a, st);
-  else if (q_out == AWQ_F16) go_append<TI, F16T>(a, st);
-  else go_append<TI, BF16T>(a, st);
+  const bool done = a.rot % 16 == 0  ? go_units<TI, 8>(a, st)
+                    : a.rot % 8 == 0 ? go_units<TI, 4>(a, st)
+                                     : false;
+  if (!done)
+    append_kernel<TI><<<(unsigned)((int64_t)a.pages_per_seq * a.c.Hkv * a.c.B), kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, awq_dtype_t q_out,
-                            hipStream_t st) {
-  if (in == AWQ_F32) return go_append_q<F32T>(a, q_out, st);
-  if (in == AWQ_F16) return go_append_q<F16T>(a, q_out, st);
-  return go_append_q<BF16T>(a, q_out, st);
+hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, hipStream_t st) {
+  if (in == AWQ_F32) return go_append<F32T>(a, st);
+  if (in == AWQ_F16) return go_append<F16T>(a, st);
+  return go_append<BF16T>(a, st);
 }
 
 hipError_t launch_kv_read(const ReadArgs& a, awq_dtype_t out, hipStream_t st) {

@@ -24,17 +24,18 @@ __global__ __launch_bounds__(256) void rope_table_kernel(int64_t n_pos, int half
   table[e] = make_float2((float)(c * fr.magnitude), (float)(s * fr.magnitude));
 }
 
-// rot % 16 == 0: a thread takes one unit of HB heads of a row, so that the row's
+// rot % 8 == 0 and D % 8 == 0: a thread takes one unit (of eight pairs, or of four where
+// rot % 16 is 8) of HB heads of a row, so that the row's
 // cosines and sines are read once for them and HB heads' loads are in flight.  Bound by
 // memory: 8191 rows x 64 heads x 128 columns, fp32 to bf16, 75 us, 5.4 TB/s (four heads;
 // 79 us with one); the gradient of 8188 x 32 heads in fp16 28 us, 4.7 TB/s.  A pair a
 // thread took 155 and 116 us.  Small calls take 3.2 us, one trip through memory and the
 // launch.
-template <class TI, class TO, int HB>
+template <class TI, class TO, int W, int HB>
 __global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int rows_per_block) {
   typedef typename TI::storage SI;
   typedef typename TO::storage SO;
-  const int units = units_of(a.D, a.rot);
+  const int units = units_of<W>(a.D, a.rot);
   const int blocks = (int)((a.H + HB - 1) / HB);
   const uint32_t work = (uint32_t)units * (uint32_t)blocks;     // threads' items of a row
   const uint32_t per_row = work < 256 ? work : 256;
@@ -55,32 +56,32 @@ __global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int rows_pe
   for (uint32_t e = threadIdx.x % per_row; e < work; e += per_row) {
     const int u = (int)(e % (uint32_t)units);
     const int64_t h0 = (int64_t)(e / (uint32_t)units) * HB;
-    const Unit c = unit_of(a.D, a.rot, a.interleaved, u);
-    Eight<SI> m0[HB], m1[HB];
+    const Unit c = unit_of<W>(a.D, a.rot, a.interleaved, u);
+    Run<W, SI> m0[HB], m1[HB];
 #pragma unroll
     for (int k = 0; k < HB; ++k) {
       const int64_t h = h0 + k < a.H ? h0 + k : h0;
-      m0[k] = load8(xr + h * a.xs[2] + c.d0);
-      m1[k] = load8(xr + h * a.xs[2] + (c.two ? c.d1 : c.d0));
+      m0[k] = load_run<W>(xr + h * a.xs[2] + c.d0);
+      m1[k] = load_run<W>(xr + h * a.xs[2] + (c.two ? c.d1 : c.d0));
     }
-    Turns t;
-    if (c.turn) t = turns_at(a.table, a.n_pos, a.rot >> 1, pos, u);
+    Turns<W> t;
+    if (c.turn) t = turns_at<W>(a.table, a.n_pos, a.rot >> 1, pos, u);
 #pragma unroll
     for (int k = 0; k < HB; ++k) {
       if (h0 + k >= a.H) break;
-      float x0[8], x1[8];
+      float x0[W], x1[W];
       widen(m0[k], x0);
       widen(m1[k], x1);
-      if (c.turn) turn_unit(x0, x1, t, a.interleaved, a.transpose);
+      if (c.turn) turn_unit<W>(x0, x1, t, a.interleaved, a.transpose);
       SO* y = yr + (h0 + k) * a.os[2];
-      store8(y + c.d0, x0);
-      if (c.two) store8(y + c.d1, x1);
+      store_run<W>(y + c.d0, x0);
+      if (c.two) store_run<W>(y + c.d1, x1);
     }
   }
 }
 
 // Any rot: one pair, or one column that is left as it is, a thread (the pairs of a rot
-// that is no multiple of 16 do not fall into vectors).
+// that is no multiple of 8 do not fall into vectors).
 template <class TI, class TO>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   typedef typename TI::storage SI;
@@ -110,12 +111,12 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   y[i2] = from_f32<SO>(x2);
 }
 
-template <class TI, class TO, int HB>
+template <class TI, class TO, int W, int HB>
 void go_units(const RopeArgs& a, hipStream_t st) {
-  const int64_t work = (int64_t)units_of(a.D, a.rot) * ((a.H + HB - 1) / HB);
+  const int64_t work = (int64_t)units_of<W>(a.D, a.rot) * ((a.H + HB - 1) / HB);
   const int rows = work < 256 ? (int)(256 / work) : 1;
   const int64_t blocks = (a.B * a.S + rows - 1) / rows;
-  rope_units_kernel<TI, TO, HB><<<(unsigned)blocks, 256, 0, st>>>(a, rows);
+  rope_units_kernel<TI, TO, W, HB><<<(unsigned)blocks, 256, 0, st>>>(a, rows);
 }
 
 template <class TI, class TO>
@@ -124,8 +125,11 @@ hipError_t go(const RopeArgs& a, hipStream_t st) {
   if (a.rot % 16 == 0 && a.D % 8 == 0) {
     // four heads a thread for 2M units and more (4M units 74.9 against 79.0 us); one for fewer,
     // which need the threads (1M units of fp32 17.6 against 19.1 us)
-    if (a.B * a.S * a.H * units_of(a.D, a.rot) >= 4 * 256 * 2048) go_units<TI, TO, 4>(a, st);
-    else go_units<TI, TO, 1>(a, st);
+    if (a.B * a.S * a.H * units_of<8>(a.D, a.rot) >= 2 << 20) go_units<TI, TO, 8, 4>(a, st);
+    else go_units<TI, TO, 8, 1>(a, st);
+  } else if (a.rot % 8 == 0 && a.D % 8 == 0) {
+    // 2 x 5066 rows x 64 heads x 80 columns of which 40 turn, bf16: 50 us (186 pair by pair)
+    go_units<TI, TO, 4, 1>(a, st);
   } else {
     const int64_t n = a.B * a.S * a.H * (a.rot / 2 + a.D - a.rot);
     rope_kernel<TI, TO><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);

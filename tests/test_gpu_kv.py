@@ -58,6 +58,8 @@ ROPE_SHAPES = [   # B, S, H, D, rot, order of the memory, offset of the first el
     (1, 1, 1, 8, 8, "bshd", 0), (1, 1, 40, 128, 128, "bshd", 0), (2, 33, 3, 96, 64, "bhsd", 0),
     (1, 257, 5, 80, 80, "bshd", 0), (3, 7, 2, 256, 32, "sbhd", 0), (1, 65, 4, 64, 62, "bshd", 0),
     (2, 19, 3, 33, 6, "bshd", 0), (1, 100, 2, 128, 128, "bshd", 1), (1, 70, 2, 128, 64, "bhsd", 8),
+    (2, 37, 5, 80, 40, "bhsd", 0), (1, 41, 3, 256, 8, "bshd", 1), (3, 9, 33, 72, 56, "sbhd", 0),
+    (2, 300, 64, 96, 72, "bshd", 0),
 ]
 
 
@@ -181,6 +183,8 @@ APPENDS = [   # new tokens of each sequence, tokens before, kv heads, q heads, D
     ([17, 16, 15], [15, 16, 17], 4, 4, 40, 24, 16), ([129], [127], 2, 2, 128, 128, 128),
     ([64, 300], [64, 20], 1, 2, 72, 72, 64), ([300, 256], [10, 0], 1, 1, 256, 256, 256),
     ([250, 3], [255, 6], 1, 2, 256, 16, 256), ([3], [29], 2, 6, 24, 0, 32),
+    ([1, 1], [64, 3], 5, 10, 80, 40, 64), ([90, 2], [6, 31], 2, 6, 80, 40, 64), ([300, 7], [250, 9], 2, 2, 96, 72, 256),
+    ([290], [3], 1, 2, 256, 8, 256), ([1], [5], 2, 2, 256, 248, 16), ([1], [5], 2, 2, 64, 6, 16),
 ]
 
 
