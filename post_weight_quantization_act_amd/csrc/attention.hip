@@ -810,7 +810,8 @@ Plan plan(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
   // would allow splits too finely, 21.6 against 19.0 us).
   p.slots = 256 * (wide <= (p.shared || p.QT == 2 ? 4 : 6) ? 2 : 1);
   // Few short sequences: eight waves a workgroup and no second launch.
-  if (p.QT == 1 && groups <= 256 && tiles <= 16) p.NW = 8;
+  // not for heads wider than 192, whose registers eight waves have no room for
+  if (p.QT == 1 && groups <= 256 && tiles <= 16 && D <= 192) p.NW = 8;
   p.chosen = B > 1 && B <= 64 * p.NW && !p.shared && p.NW == 4 && tiles > 8;
   if (p.chosen) {
     // lengths differ: the kernel chooses among kChoices powers of two, up to what all
@@ -861,9 +862,11 @@ void go_q(const AttArgs& a, const Plan& p, const Split& sp, unsigned grid, hipSt
     attention_rows_kernel<T, DB, 4, false><<<grid, 256, 0, st>>>(a, sp);
     return;
   }
-  if (p.QT == 1 && p.NW == 8) go_w<T, DB, 1, 8>(a, sp, grid, st);
-  else if (p.QT == 1) go_w<T, DB, 1, 4>(a, sp, grid, st);
-  else if constexpr (DB <= 6) go_w<T, DB, 2, 4>(a, sp, grid, st);
+  if constexpr (DB <= 6) {
+    if (p.QT == 2) return go_w<T, DB, 2, 4>(a, sp, grid, st);
+    if (p.NW == 8) return go_w<T, DB, 1, 8>(a, sp, grid, st);
+  }
+  go_w<T, DB, 1, 4>(a, sp, grid, st);
 }
 
 template <class T>
