@@ -59,6 +59,9 @@ struct Split {
 
 constexpr int kChoices = 5;
 
+// Rows of a sequence's n that the call takes: the first ones.
+__device__ __forceinline__ int taken(const AttArgs& a, int n) { return n < a.max_new ? n : a.max_new; }
+
 // 64-token tiles that the rows of a sequence see, so at least as many as any of its row
 // tiles does; -1: it has no rows.
 __device__ __forceinline__ int tiles_of(const AttArgs& a, int b) {
@@ -66,9 +69,8 @@ __device__ __forceinline__ int tiles_of(const AttArgs& a, int b) {
   int n, lo, hi, unused;
   rows_of(a.c, b, row0, n);
   if (n == 0) return -1;
-  n = n < a.max_new ? n : a.max_new;
   seen_by(a, a.lens[b], n, 0, lo, unused);
-  seen_by(a, a.lens[b], n, n - 1, unused, hi);
+  seen_by(a, a.lens[b], n, taken(a, n) - 1, unused, hi);
   return hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 0;
 }
 
@@ -194,7 +196,7 @@ __device__ __forceinline__ void load_rows(const AttArgs& a, Rows<DB>& w, int64_t
 #pragma unroll
   for (int dt = 0; dt < 2 * DB; ++dt) w.o[dt] = f32x4{0, 0, 0, 0};
   float x[DB][8];
-  const bool valid = i < n;
+  const bool valid = i < taken(a, n);
   if (valid) seen_by(a, len, n, i, w.lo, w.hi);
   const S* q = (const S*)a.q + (row0 + (valid ? i : 0)) * a.qs[0] + (h * G + (valid ? rr % G : 0)) * a.qs[1];
   uint32_t top = 0;
@@ -411,8 +413,7 @@ __global__ __launch_bounds__(NW * 64, DB <= 6 ? 2 : 1) void attention_kernel(Att
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
-  n = n < a.max_new ? n : a.max_new;
-  const int G = a.Hq / c.Hkv, base = rt * 16 * QT, rows = n * G;
+  const int G = a.Hq / c.Hkv, base = rt * 16 * QT, rows = taken(a, n) * G;
   if (base >= rows) return;
   const int len = a.lens[b];
   int lo, hi, unused;
@@ -564,8 +565,7 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
-  n = n < a.max_new ? n : a.max_new;
-  const int G = a.Hq / c.Hkv, base = rt * 32 * NW, rows = n * G;
+  const int G = a.Hq / c.Hkv, base = rt * 32 * NW, rows = taken(a, n) * G;
   if (base >= rows) return;
   const int len = a.lens[b];
   int lo, hi, unused;
@@ -734,10 +734,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
-  n = n < a.max_new ? n : a.max_new;
-  if (i >= n) return;
+  if (i >= n) return;   // and below max_new by the grid
   if (sp.chosen) sp.tiles = *sp.chosen;
-  const int G = a.Hq / c.Hkv, len = a.lens[b], rows = n * G;
+  const int G = a.Hq / c.Hkv, len = a.lens[b], rows = taken(a, n) * G;
   const int base = (i * G + hq % G) / rows_per_tile * rows_per_tile;
   int lo, hi, unused;
   seen_by(a, len, n, base / G, lo, unused);

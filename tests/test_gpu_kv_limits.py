@@ -1,0 +1,63 @@
+"""Calls at the edges of their own limits: fewer rows allowed than a sequence has, lengths cut short,
+windows and bounds as large as they may be, and grids of more workgroups than one launch holds."""
+
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_act_amd as awq
+from oracle import kv_ref
+from test_gpu_kv import (TYPES, assert_same_cache, attention_bound, check_attention, f32, ints, new_cache,
+                         page_table, wide)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    awq.library()
+    yield
+    torch.cuda.synchronize()
+
+
+def starts_of(rows):
+    return np.concatenate(([0], np.cumsum(rows))).tolist()
+
+
+# ---------------------------------------------------------------------------------------------
+# fewer rows allowed than a sequence has
+# ---------------------------------------------------------------------------------------------
+LIMITED = [   # rows of each sequence, max_new, lengths, q heads, kv heads, D, page
+    ([10], 4, [10], 2, 1, 32, 16), ([10, 3, 1], 4, [40, 3, 7], 8, 2, 64, 16), ([9, 20], 5, [300, 200], 16, 1, 64, 32),
+    ([6, 2, 9], 3, [1500, 700, 90], 8, 2, 64, 64), ([12], 2, [3001], 4, 1, 128, 64), ([40], 17, [900], 8, 2, 96, 32),
+    ([5], 1, [4], 4, 4, 256, 64),
+]
+
+
+def first_rows(rows, most):
+    """Which rows of a call are among the first `most` of their sequence."""
+    return np.concatenate([np.arange(n) < most for n in rows])
+
+
+@pytest.mark.parametrize("window,causal", [(0, True), (7, True), (0, False), (9, False)])
+@pytest.mark.parametrize("shape", LIMITED)
+def test_attention_of_the_first_rows(shape, window, causal):
+    """Rows beyond max_new are left out; those before it keep their tokens."""
+    rows, most, lens, hq, heads, dim, page = shape
+    rng = np.random.default_rng(sum(lens) + dim)
+    per_seq = -(-max(lens) // page)
+    dev, ref = new_cache(rng, len(rows) * per_seq, heads, page, dim)
+    table = page_table(rng, len(rows), dev.n_pages, per_seq)
+    starts, T = starts_of(rows), sum(rows)
+    q = torch.from_numpy(rng.standard_normal((T, hq, dim)).astype(f32)).half().cuda()
+    out = torch.full_like(q, 7.0)
+    awq.awq_kv_attention(dev, q, ints(lens), ints(table.tolist()), starts=ints(starts), max_new=most,
+                         max_len=max(lens), window=window, causal=causal, out=out)
+    scale = dim ** -0.5
+    want, _, spread, top = ref.attention(wide(q), lens, table, starts, scale, window, causal)
+    _, bound = attention_bound(ref, wide(q), scale, spread, top, want, "f16", dim)
+    taken = first_rows(rows, most)
+    assert (np.abs(wide(out) - want) <= bound)[taken].all()
+    assert (wide(out)[~taken] == 7).all()
