@@ -82,7 +82,8 @@ __device__ __forceinline__ uint32_t moved(uint32_t w, float by) {
   return r;
 }
 
-// Where a workgroup of an append works: the new tokens [lo, hi) of a page of a sequence.
+// Where a workgroup of an append works: the new tokens [lo, hi) of a page of a sequence, of
+// its first max_new rows (what the launch's registers are sized for).
 struct Place {
   int64_t row_lo, row0, first;   // rows of token lo and of the sequence; number of its first new token
   int64_t page;                  // the sequence's page
@@ -96,10 +97,10 @@ __device__ __forceinline__ bool find_place(const AppendArgs& a, int b, int j, Pl
   const int64_t len = a.lens[b];
   p.first = len - n;
   p.page = ((p.first < 0 ? 0 : p.first) >> c.p_shift) + j;
-  const int64_t base = p.page << c.p_shift;
-  if (n == 0 || base >= len) return false;
+  const int64_t base = p.page << c.p_shift, end = n < a.max_new ? len : p.first + a.max_new;
+  if (n == 0 || base >= end) return false;
   p.lo = (int)((p.first > base ? p.first : base) - base);
-  p.hi = (int)((len < base + c.P ? len : base + c.P) - base);
+  p.hi = (int)((end < base + c.P ? end : base + c.P) - base);
   p.row_lo = p.row0 + (base + p.lo - p.first);
   return true;
 }

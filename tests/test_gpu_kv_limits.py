@@ -61,3 +61,42 @@ def test_attention_of_the_first_rows(shape, window, causal):
     taken = first_rows(rows, most)
     assert (np.abs(wide(out) - want) <= bound)[taken].all()
     assert (wide(out)[~taken] == 7).all()
+
+
+APPEND_LIMITED = [   # rows of each sequence, max_new, tokens before, kv heads, q heads, D, rot, page
+    ([20], 1, [0], 1, 2, 128, 128, 64), ([20, 3], 2, [5, 30], 2, 4, 128, 64, 64), ([90, 7], 33, [10, 60], 2, 2, 64, 24, 32),
+    ([50], 40, [15], 1, 1, 80, 20, 16), ([300], 5, [250], 2, 2, 96, 72, 256), ([9], 4, [-6], 1, 2, 64, 0, 16),
+]
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+@pytest.mark.parametrize("shape", APPEND_LIMITED)
+def test_append_of_the_first_rows(shape, kind):
+    rows, most, before, heads, hq, dim, rot, page = shape
+    rng = np.random.default_rng(sum(rows) + dim)
+    B, T = len(rows), sum(rows)
+    lens = [n + m for n, m in zip(rows, before)]
+    per_seq = -(-max(lens) // page)
+    dev, ref = new_cache(rng, B * per_seq, heads, page, dim)
+    table = page_table(rng, B, dev.n_pages, per_seq)
+    qkv = torch.from_numpy(rng.standard_normal((T, hq + 2 * heads, dim)).astype(f32)).to(TYPES[kind]).cuda()
+    q, k, v = qkv[:, :hq], qkv[:, hq: hq + heads], qkv[:, hq + heads:]
+    rope = awq.awq_rope_table(max(lens), rot) if rot else None
+    at = np.concatenate([np.arange(m, n) for m, n in zip(before, lens)])
+    turn = (lambda x: kv_ref.rope(wide(x), wide(rope), at)) if rot else wide
+    q_out = torch.full_like(q, 7.0, dtype=torch.float32, memory_format=torch.contiguous_format)
+    awq.awq_kv_append(dev, k, v, ints(lens), ints(table.tolist()), starts=ints(starts_of(rows)), max_new=most,
+                      table=rope, q=q, q_out=q_out)
+    taken = np.concatenate([np.arange(n) < most for n in rows])
+    kept = [min(n, most) for n in rows]
+    ref.append(turn(k)[taken], wide(v)[taken], [m + n for m, n in zip(before, kept)], table, starts_of(kept))
+    # places past the tokens that were appended are nobody's
+    for b, n in enumerate(kept):
+        p, t = (before[b] + n) // page, (before[b] + n) % page
+        if t > 0:
+            ref.k_codes[table[b, p], :, t:] = dev.k_codes[table[b, p], :, t:].cpu().numpy()
+            ref.v_codes[table[b, p], :, :, t:] = dev.v_codes[table[b, p], :, :, t:].cpu().numpy()
+    assert_same_cache(dev, ref)
+    turned = taken & (at >= 0)       # tokens before a sequence's start are dropped, their queries with them
+    np.testing.assert_array_equal(wide(q_out)[turned], turn(q)[turned])
+    assert (wide(q_out)[~turned] == 7).all()
