@@ -976,6 +976,7 @@ awq_status_t awq_kv_read(const awq_kv_cache_t* cache, int64_t T, const int32_t* 
   a.first = first;
   a.k_out = k_out;
   a.v_out = v_out;
+  a.max_new = (int)max_new;
   a.pages_per_seq = (int)((max_new + a.c.P - 2) / a.c.P + 1);
   hipError_t e = awq::launch_kv_read(a, out_dtype, stream);
   if (e != hipSuccess) return hip_fail(e, "kv_read launch");

@@ -221,7 +221,7 @@ struct ReadArgs {
   KvArgs c;
   const int32_t* first;
   void *k_out, *v_out;           // [T][Hkv][D]
-  int pages_per_seq;
+  int pages_per_seq, max_new;
 };
 
 struct AttArgs {

@@ -447,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) 
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
-  const int64_t first = a.first[b], end = first + n;
+  const int64_t first = a.first[b], end = first + (n < a.max_new ? n : a.max_new);
   const int64_t p = (first >> c.p_shift) + j, base = p << c.p_shift;
   if (n == 0 || base >= end) return;
   const int lo = (int)((first > base ? first : base) - base);

@@ -100,3 +100,23 @@ def test_append_of_the_first_rows(shape, kind):
     turned = taken & (at >= 0)       # tokens before a sequence's start are dropped, their queries with them
     np.testing.assert_array_equal(wide(q_out)[turned], turn(q)[turned])
     assert (wide(q_out)[~turned] == 7).all()
+
+
+@pytest.mark.parametrize("most", [1, 3, 16, 19])
+def test_read_of_the_first_tokens(most):
+    rng = np.random.default_rng(most)
+    dev, ref = new_cache(rng, 8, 2, 16, 24)
+    table = page_table(rng, 2, 8, 4)
+    first, count = [5, 30], [40, 20]
+    k = torch.full((60, 2, 24), 7.0, device="cuda")
+    v = k.clone()
+    lib, struct = awq.library(), dev._ref
+    starts, at, pages = ints(starts_of(count)), ints(first), ints(table.tolist())
+    assert lib.awq_kv_read(struct, 60, starts.data_ptr(), at.data_ptr(), 2, pages.data_ptr(), 4, most,
+                           k.data_ptr(), v.data_ptr(), awq.AWQ_F32,
+                           torch.cuda.current_stream().cuda_stream) == 0
+    taken = np.concatenate([np.arange(n) < most for n in count])
+    want = [ref.tokens(b, first[b], first[b] + count[b], table) for b in range(2)]
+    for got, i in ((k, 0), (v, 1)):
+        np.testing.assert_array_equal(wide(got)[taken], np.concatenate([w[i] for w in want])[taken])
+        assert (wide(got)[~taken] == 7).all()
