@@ -198,6 +198,7 @@ __device__ __forceinline__ void load_rows(const AttArgs& a, Rows<DB>& w, int64_t
   float x[DB][8];
   const bool valid = i < taken(a, n);
   if (valid) seen_by(a, len, n, i, w.lo, w.hi);
+  if (w.lo == w.hi) w.lo = w.hi = 0;   // before every token, so that no block's steps count
   const S* q = (const S*)a.q + (row0 + (valid ? i : 0)) * a.qs[0] + (h * G + (valid ? rr % G : 0)) * a.qs[1];
   uint32_t top = 0;
 #pragma unroll

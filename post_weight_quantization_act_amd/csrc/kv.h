@@ -235,7 +235,8 @@ struct AttArgs {
   int Hq, causal, window, max_new, max_len;
 };
 
-// Tokens [lo, hi) of the cache that row i of n of a sequence of `len` tokens sees.
+// Tokens [lo, hi) of the cache that row i of n of a sequence of `len` tokens sees; lo = hi:
+// none.  Neither falls from a row to the next.
 __device__ __forceinline__ void seen_by(const AttArgs& a, int len, int n, int i, int& lo, int& hi) {
   const int at = len - n + i;
   hi = a.causal ? at + 1 : len;
@@ -244,7 +245,9 @@ __device__ __forceinline__ void seen_by(const AttArgs& a, int len, int n, int i,
   hi = hi > len ? len : hi;
   hi = hi > table ? (int)table : hi;
   hi = hi > a.max_len ? a.max_len : hi;
+  hi = hi < 0 ? 0 : hi;
   lo = lo < 0 ? 0 : lo;
+  lo = lo > hi ? hi : lo;   // a window that begins where no token is attended to any more
 }
 
 hipError_t launch_rope_table(int64_t n_pos, int rot, const RopeFreqs& fr, float* table,

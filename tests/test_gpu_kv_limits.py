@@ -120,3 +120,41 @@ def test_read_of_the_first_tokens(most):
     for got, i in ((k, 0), (v, 1)):
         np.testing.assert_array_equal(wide(got)[taken], np.concatenate([w[i] for w in want])[taken])
         assert (wide(got)[~taken] == 7).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# windows and lengths
+# ---------------------------------------------------------------------------------------------
+class Cut(kv_ref.Cache):
+    """The oracle's cache of which only the first max_len tokens of a sequence are attended to."""
+
+    def __init__(self, ref, max_len):
+        self.__dict__.update(ref.__dict__)
+        self.max_len = max_len
+
+    def tokens(self, b, lo, hi, pages):
+        k, v, there = super().tokens(b, lo, hi, pages)
+        return k, v, there & (np.arange(lo, hi) < self.max_len)
+
+
+CUT = [   # rows of each sequence, lengths, max_len, window, q heads, kv heads, D, page
+    ([4], [21], 18, 1, 2, 1, 32, 16), ([4, 6], [21, 30], 18, 3, 4, 2, 64, 32), ([70], [100], 50, 5, 2, 1, 64, 32),
+    ([60, 8], [700, 40], 661, 20, 4, 1, 128, 64), ([5, 5, 5], [1300, 1299, 1297], 1297, 2, 2, 2, 96, 64),
+    ([6], [21], 18, 0, 2, 1, 32, 16), ([3], [40], 17, 4, 2, 2, 256, 16),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("shape", CUT)
+def test_attention_windows_that_begin_past_max_len(shape, causal):
+    """Such a row sees nothing, and nothing of what lies past max_len, numbers or not."""
+    rows, lens, max_len, window, hq, heads, dim, page = shape
+    rng = np.random.default_rng(sum(lens) + dim)
+    per_seq = -(-max(lens) // page)
+    dev, ref = new_cache(rng, len(rows) * per_seq, heads, page, dim)
+    table = page_table(rng, len(rows), dev.n_pages, per_seq)
+    past = table[:, -(-max_len // page):].reshape(-1).tolist()
+    dev.k_steps[past], dev.v_steps[past] = float("nan"), float("nan")
+    q = torch.from_numpy(rng.standard_normal((sum(rows), hq, dim)).astype(f32)).half().cuda()
+    check_attention(dev, Cut(ref, max_len), q, lens, table, starts_of(rows), "f16", window, causal,
+                    max_new=max(rows), max_len=max_len)
