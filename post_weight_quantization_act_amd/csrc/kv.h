@@ -240,13 +240,12 @@ struct AttArgs {
 __device__ __forceinline__ void seen_by(const AttArgs& a, int len, int n, int i, int& lo, int& hi) {
   const int at = len - n + i;
   hi = a.causal ? at + 1 : len;
-  lo = a.window > 0 ? at - a.window + 1 : 0;
+  lo = a.window > 0 && at >= a.window ? at - a.window + 1 : 0;   // at may be below 0: no overflow
   const int64_t table = (int64_t)a.c.max_pages << a.c.p_shift;   // past it there are no pages
   hi = hi > len ? len : hi;
   hi = hi > table ? (int)table : hi;
   hi = hi > a.max_len ? a.max_len : hi;
   hi = hi < 0 ? 0 : hi;
-  lo = lo < 0 ? 0 : lo;
   lo = lo > hi ? hi : lo;   // a window that begins where no token is attended to any more
 }
 

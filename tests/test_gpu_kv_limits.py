@@ -158,3 +158,14 @@ def test_attention_windows_that_begin_past_max_len(shape, causal):
     q = torch.from_numpy(rng.standard_normal((sum(rows), hq, dim)).astype(f32)).half().cuda()
     check_attention(dev, Cut(ref, max_len), q, lens, table, starts_of(rows), "f16", window, causal,
                     max_new=max(rows), max_len=max_len)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 40])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_windows_longer_than_any_sequence(window, causal):
+    """More rows than tokens, so that the first rows' windows begin before the sequence."""
+    rng = np.random.default_rng(21)
+    dev, ref = new_cache(rng, 8, 1, 16, 32)
+    table = page_table(rng, 2, 8, 4)
+    q = torch.from_numpy(rng.standard_normal((11, 2, 32)).astype(f32)).half().cuda()
+    check_attention(dev, ref, q, [2, 60], table, [0, 5, 11], "f16", window, causal, max_new=6, max_len=64)
