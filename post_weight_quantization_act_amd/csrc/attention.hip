@@ -112,8 +112,8 @@ __device__ __forceinline__ Part choose(const AttArgs& a, const Split& sp, int wa
   }
   if (tid == 0) found[0] = -1;
   __syncthreads();
-  all = 0;
-  for (int w = 0; w < W; ++w) all += sums[w][kChoices];
+  int64_t total = 0;    // a wave's 64 sequences have at most 2^30 tiles
+  for (int w = 0; w < W; ++w) total += sums[w][kChoices];
   const int64_t groups = (int64_t)a.c.Hkv * sp.row_tiles;
   int take = log;
 #pragma unroll
@@ -121,7 +121,7 @@ __device__ __forceinline__ Part choose(const AttArgs& a, const Split& sp, int wa
     int units = 0;
     for (int w = 0; w < W; ++w) units += sums[w][k];
     take = log + k;
-    if (units * groups <= sp.slots || ((int64_t)sp.slots << take) >= 2 * all * groups) break;
+    if (units * groups <= sp.slots || ((int64_t)sp.slots << take) >= 2 * total * groups) break;
   }
   const int mine = splits_of(nt, take);
   int upto = mine;

@@ -169,3 +169,20 @@ def test_attention_windows_longer_than_any_sequence(window, causal):
     table = page_table(rng, 2, 8, 4)
     q = torch.from_numpy(rng.standard_normal((11, 2, 32)).astype(f32)).half().cuda()
     check_attention(dev, ref, q, [2, 60], table, [0, 5, 11], "f16", window, causal, max_new=6, max_len=64)
+
+
+def test_attention_over_more_tiles_than_half_a_32_bit_sum():
+    """256 sequences of 2^28 tokens, all of them the same page of equal values: every sequence's sum has to
+    come whole from its splits.  A wave adds 2^19 or 2^20 equal addends, each sum rounded to 2^-24 of itself:
+    up to 2^-4 of an addend, so of the result, in the sum of the probabilities; twice (two products a tile)
+    in the values'."""
+    cache = awq.KvCache(torch.full((1, 1, 256, 8), 128, dtype=torch.uint8, device="cuda"),
+                        torch.full((1, 1, 8, 256), 129, dtype=torch.uint8, device="cuda"),
+                        torch.ones(1, 1, device="cuda"), torch.ones(1, 1, device="cuda"))
+    B, tokens = 256, 1 << 28
+    pages = torch.zeros((B, tokens // 256), dtype=torch.int32, device="cuda")
+    q = torch.ones((B, 1, 8), dtype=torch.float16, device="cuda")
+    ws = torch.zeros(awq.awq_kv_attention_workspace_size(B, B, 1, 1, 8, 1, tokens), dtype=torch.uint8, device="cuda")
+    out, lse = awq.awq_kv_attention(cache, q, ints([tokens] * B), pages, max_len=tokens, return_lse=True, workspace=ws)
+    assert (np.abs(wide(out) - 1) <= 3 * 2.0 ** -4).all()
+    assert (np.abs(wide(lse) - 28 * np.log(2)) <= 2 * 2.0 ** -4).all()
