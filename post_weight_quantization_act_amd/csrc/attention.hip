@@ -35,6 +35,8 @@
 // over 3000 and 4096 tokens 462 us, 733 TFLOP/s (a large fp16 matrix product reaches 1140 to
 // 1180 here); the matrix units are busy 29% and the vector units 50% of the time, 1.5 waves
 // a SIMD on average.
+#include <algorithm>
+
 #include "kv.h"
 
 namespace awq {
@@ -394,22 +396,23 @@ __global__ __launch_bounds__(NW * 64, DB <= 6 ? 2 : 1) void attention_kernel(Att
   // heads first, splits last: workgroups are dealt to the eight XCDs in turn, so a
   // sequence's splits, of which only the first few may hold tokens, never fall on one
   // XCD, and with 8 heads the row tiles of a head read its keys through one L2
-  int bid = blockIdx.x, b, rt, split;
-  const int h = bid % c.Hkv;
-  bid /= c.Hkv;
+  uint32_t bid = a.first_block + blockIdx.x;
+  int b, rt, split;
+  const int h = (int)(bid % (uint32_t)c.Hkv);
+  bid /= (uint32_t)c.Hkv;
   if (sp.chosen) {
-    rt = bid % sp.row_tiles;
-    const Part u = choose<NW * 64>(a, sp, bid / sp.row_tiles);
-    if (blockIdx.x == 0 && tid == 0) *sp.chosen = u.tiles;
+    rt = (int)(bid % (uint32_t)sp.row_tiles);
+    const Part u = choose<NW * 64>(a, sp, (int)(bid / (uint32_t)sp.row_tiles));
+    if (a.first_block + blockIdx.x == 0 && tid == 0) *sp.chosen = u.tiles;
     if (u.b < 0) return;
     sp.tiles = u.tiles;
     b = u.b;
     split = u.split;
   } else {
-    b = bid % c.B;
-    bid /= c.B;
-    rt = bid % sp.row_tiles;
-    split = bid / sp.row_tiles;
+    b = (int)(bid % (uint32_t)c.B);
+    bid /= (uint32_t)c.B;
+    rt = (int)(bid % (uint32_t)sp.row_tiles);
+    split = (int)(bid / (uint32_t)sp.row_tiles);
   }
   int64_t row0;
   int n;
@@ -557,12 +560,13 @@ __global__ __launch_bounds__(NW * 64, DB > 4 ? 1 : 2) void attention_rows_kernel
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
 
-  int bid = blockIdx.x;
-  const int h = bid % c.Hkv;
-  bid /= c.Hkv;
-  const int b = bid % c.B;
-  bid /= c.B;
-  const int split = bid / sp.row_tiles, rt = sp.row_tiles - 1 - bid % sp.row_tiles;   // the longest first
+  uint32_t bid = a.first_block + blockIdx.x;
+  const int h = (int)(bid % (uint32_t)c.Hkv);
+  bid /= (uint32_t)c.Hkv;
+  const int b = (int)(bid % (uint32_t)c.B);
+  bid /= (uint32_t)c.B;
+  const int split = (int)(bid / (uint32_t)sp.row_tiles);
+  const int rt = sp.row_tiles - 1 - (int)(bid % (uint32_t)sp.row_tiles);   // the longest first
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
@@ -727,11 +731,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs a, Split sp, int rows
   __shared__ float sl[128], stop[4];
   const KvArgs& c = a.c;
   const int tid = threadIdx.x;
-  int64_t e = blockIdx.x;   // (b, i, hq)
-  const int hq = (int)(e % a.Hq);
-  e /= a.Hq;
-  const int i = (int)(e % a.max_new);
-  const int b = (int)(e / a.max_new);
+  uint32_t e = a.first_block + blockIdx.x;   // (b, i, hq)
+  const int hq = (int)(e % (uint32_t)a.Hq);
+  e /= (uint32_t)a.Hq;
+  const int i = (int)(e % (uint32_t)a.max_new);
+  const int b = (int)(e / (uint32_t)a.max_new);
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
@@ -870,10 +874,10 @@ void go_q(const AttArgs& a, const Plan& p, const Split& sp, unsigned grid, hipSt
 }
 
 template <class T>
-hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) {
-  const unsigned grid = (unsigned)p.blocks;
-  {
-    ProfScope prof("awq_kv_attention", st);
+hipError_t go(AttArgs a, const Plan& p, const Split& sp, hipStream_t st) {
+  ProfScope prof("awq_kv_attention", st);
+  in_parts(p.blocks, 64 * p.NW, [&](uint32_t first, unsigned grid) {
+    a.first_block = first;
     switch ((a.c.D + 31) / 32) {
       case 1: go_q<T, 1>(a, p, sp, grid, st); break;
       case 2: go_q<T, 2>(a, p, sp, grid, st); break;
@@ -884,12 +888,18 @@ hipError_t go(const AttArgs& a, const Plan& p, const Split& sp, hipStream_t st) 
       case 7: go_q<T, 7>(a, p, sp, grid, st); break;
       default: go_q<T, 8>(a, p, sp, grid, st); break;
     }
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
+  });
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t go_join(AttArgs a, const Plan& p, const Split& sp, hipStream_t st) {
   ProfScope prof("awq_kv_attention_join", st);
-  const int64_t rows = (int64_t)a.c.B * a.max_new * a.Hq;
-  join_kernel<T><<<(unsigned)rows, p.chosen ? 64 : 256, 0, st>>>(a, sp, p.tile_rows);
+  const int threads = p.chosen ? 64 : 256;
+  in_parts((int64_t)a.c.B * a.max_new * a.Hq, threads, [&](uint32_t first, unsigned grid) {
+    a.first_block = first;
+    join_kernel<T><<<grid, threads, 0, st>>>(a, sp, p.tile_rows);
+  });
   return hipGetLastError();
 }
 
@@ -901,12 +911,10 @@ size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int m
   return p.splits == 1 ? 0 : (size_t)p.splits * T * Hq * (D + 2) * 4 + 4;
 }
 
-int64_t kv_attention_blocks(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
-                            int max_len) {
+int64_t kv_attention_blocks(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
   if (max_new > (int64_t)INT32_MAX / Hq) return INT64_MAX;
-  const int64_t rows = (int64_t)max_new * Hq;
-  if (B > INT32_MAX / rows) return INT64_MAX;
-  return plan(B, Hq, Hkv, D, max_new, max_len).blocks;
+  const Plan p = plan(B, Hq, Hkv, D, max_new, max_len);
+  return p.splits == 1 ? p.blocks : std::max(p.blocks, B * max_new * Hq);
 }
 
 hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipStream_t st) {
@@ -917,7 +925,9 @@ hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipSt
     sp.rl = (float2*)(sp.o + (size_t)p.splits * a.c.T * a.Hq * a.c.D);
     if (p.chosen) sp.chosen = (int*)(sp.rl + (size_t)p.splits * a.c.T * a.Hq);
   }
-  return dt == AWQ_F16 ? go<F16T>(a, p, sp, st) : go<BF16T>(a, p, sp, st);
+  const hipError_t e = dt == AWQ_F16 ? go<F16T>(a, p, sp, st) : go<BF16T>(a, p, sp, st);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return dt == AWQ_F16 ? go_join<F16T>(a, p, sp, st) : go_join<BF16T>(a, p, sp, st);
 }
 
 }  // namespace awq

@@ -40,7 +40,7 @@ constexpr int kLaunchRounds = 4;      // candidate-GEMM rounds of the persistent
 constexpr int64_t kGptqMaxK = 32768;   // the fp64 factor matrix is K^2 * 8 bytes
 constexpr int64_t kLowbitGemmMaxM = 65535ll * 128;  // activation-row tiles on grid y
 constexpr int64_t kLowbitGemmMaxK = 1ll << 22;       // a 256-row activation tile in 32-bit offsets
-constexpr int64_t kMaxGrid = INT32_MAX;               // workgroups of a launch
+constexpr int64_t kMaxGrid = INT32_MAX;               // workgroups of a grid (launched in parts)
 constexpr int kMaxHeads = 16384;
 
 int esize(awq_dtype_t dt) { return dt == AWQ_F32 ? 4 : 2; }
@@ -196,9 +196,9 @@ awq_status_t kv_args(const awq_kv_cache_t* cache, int64_t T, const int32_t* star
     if (!pages) return fail(AWQ_ERR_INVALID_ARG, "null pages");
     if (!aligned(pages, 4) || !aligned(starts, 4))
       return fail(AWQ_ERR_UNSUPPORTED, "pages and starts must be 4-byte aligned");
-    const int64_t pps = (max_new + cache->page - 2) / cache->page + 1;
+    const int64_t pps = (std::min(max_new, T) + cache->page - 2) / cache->page + 1;
     if (B > kMaxGrid / 4 / (pps * cache->kv_heads))   // queries double it, and eights round it up
-      return fail(AWQ_ERR_UNSUPPORTED, "too many sequences, heads and pages for one launch");
+      return fail(AWQ_ERR_UNSUPPORTED, "too many sequences, heads and pages for one call");
   }
   a->k_codes = cache->k_codes;
   a->v_codes = cache->v_codes;
@@ -880,6 +880,7 @@ awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, 
   if (!aligned(x, esize(x_dtype)) || !aligned(out, esize(out_dtype)) || !aligned(table, 8) ||
       !aligned(positions, 4))
     return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned to its elements");
+  if (H * D > (1ll << 34)) return fail(AWQ_ERR_UNSUPPORTED, "more than 2^34 elements in a row");
   if (B * S > kMaxGrid * 256 / (H * D))
     return fail(AWQ_ERR_UNSUPPORTED, "more than %lld elements", (long long)(kMaxGrid * 256));
   awq::RopeArgs a = {};
@@ -930,6 +931,7 @@ awq_status_t awq_kv_append(const awq_kv_cache_t* cache, const void* k, const voi
     return fail(AWQ_ERR_INVALID_ARG, "Hq=%lld must be a multiple of kv_heads=%d (0 without q)",
                 (long long)Hq, a.c.Hkv);
   if (T == 0 || B == 0) return AWQ_OK;
+  max_new = std::min(max_new, T);
   if (!k || !v || !kv_strides || !lens || (q && (!q_out || !q_strides)))
     return fail(AWQ_ERR_INVALID_ARG, "null pointer");
   if (!aligned(k, esize(dtype)) || !aligned(v, esize(dtype)) || !aligned(q, esize(dtype)) ||
@@ -970,6 +972,7 @@ awq_status_t awq_kv_read(const awq_kv_cache_t* cache, int64_t T, const int32_t* 
   if (st != AWQ_OK) return st;
   if (!valid_dtype(out_dtype)) return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d", (int)out_dtype);
   if (T == 0 || B == 0) return AWQ_OK;
+  max_new = std::min(max_new, T);
   if (!first || !k_out || !v_out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
   if (!aligned(first, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
     return fail(AWQ_ERR_UNSUPPORTED, "k_out and v_out must be 16-byte aligned");
@@ -990,6 +993,7 @@ size_t awq_kv_attention_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t
       max_len < 1 || T > INT32_MAX || B > INT32_MAX || Hq > kMaxHeads || D > 256 ||
       max_new > INT32_MAX / 2 || max_len > (1 << 30))
     return 0;
+  max_new = std::min(max_new, T);
   return align_up(awq::kv_attention_ws_bytes(T, B, (int)Hq, (int)kv_heads, (int)D, (int)max_new,
                                              (int)max_len));
 }
@@ -1018,14 +1022,15 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
                 (long long)max_len);
   if (flags & ~AWQ_ATT_FULL) return fail(AWQ_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
   if (T == 0 || B == 0) return AWQ_OK;
+  max_new = std::min(max_new, T);
   if (!q || !q_strides || !lens || !out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
   if (!aligned(q, 2) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4))
     return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned (out: to 16 bytes)");
   const int64_t reach = std::max<int64_t>(1, std::min<int64_t>(max_len, max_pages * a.c.P));
   if (reach > (1 << 30))
     return fail(AWQ_ERR_UNSUPPORTED, "%lld tokens of a sequence exceed 2^30", (long long)reach);
-  if (awq::kv_attention_blocks(T, B, (int)Hq, a.c.Hkv, a.c.D, (int)max_new, (int)reach) > kMaxGrid)
-    return fail(AWQ_ERR_UNSUPPORTED, "too many rows for one launch");
+  if (awq::kv_attention_blocks(B, (int)Hq, a.c.Hkv, a.c.D, (int)max_new, (int)reach) > kMaxGrid)
+    return fail(AWQ_ERR_UNSUPPORTED, "too many rows for one call");
   const size_t need = awq_kv_attention_workspace_size(T, B, Hq, a.c.Hkv, a.c.D, max_new, reach);
   if (need > 0) {
     if (!workspace || workspace_bytes < need)

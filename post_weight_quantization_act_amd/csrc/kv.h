@@ -6,6 +6,15 @@
 
 namespace awq {
 
+// A launch holds fewer than 2^32 threads: more make an error or, where the product wraps, a
+// smaller grid.  `launch` gets the first workgroup and the number of each part of a grid.
+template <class F>
+void in_parts(int64_t blocks, int threads, F launch) {
+  const int64_t most = ((1ll << 32) - 1) / threads / 64 * 64;   // the dealing over XCDs goes on as it was
+  for (int64_t first = 0; first < blocks; first += most)
+    launch((uint32_t)first, (unsigned)(blocks - first < most ? blocks - first : most));
+}
+
 // ---- rotary positions ---------------------------------------------------------
 struct RopeFreqs {
   double base, factor, magnitude;
@@ -35,6 +44,7 @@ struct RopeArgs {
   int64_t xs[3], os[3];       // strides over B, S, H in elements
   int64_t pos_stride, n_pos;
   int D, rot, interleaved, transpose;
+  uint32_t first_block;       // of the launch in its grid
 };
 
 // cos and sin of a position, NaN outside the table: a wrong position shows.
@@ -215,6 +225,7 @@ struct AppendArgs {
   int rot, interleaved, Hq, pages_per_seq, max_new;
   int kv_blocks, q_parts;        // the launch's own
   awq_dtype_t q_type;            // of q_out
+  uint32_t first_block;
 };
 
 struct ReadArgs {
@@ -222,6 +233,7 @@ struct ReadArgs {
   const int32_t* first;
   void *k_out, *v_out;           // [T][Hkv][D]
   int pages_per_seq, max_new;
+  uint32_t first_block;
 };
 
 struct AttArgs {
@@ -233,6 +245,7 @@ struct AttArgs {
   int64_t qs[2];
   float scale;
   int Hq, causal, window, max_new, max_len;
+  uint32_t first_block;
 };
 
 // Tokens [lo, hi) of the cache that row i of n of a sequence of `len` tokens sees; lo = hi:
@@ -253,11 +266,11 @@ hipError_t launch_rope_table(int64_t n_pos, int rot, const RopeFreqs& fr, float*
                              hipStream_t st);
 hipError_t launch_rope(const RopeArgs& a, awq_dtype_t in, awq_dtype_t out, hipStream_t st);
 hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, hipStream_t st);
-hipError_t launch_kv_read(const ReadArgs& a, awq_dtype_t out, hipStream_t st);
+hipError_t launch_kv_read(ReadArgs a, awq_dtype_t out, hipStream_t st);
 size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
                              int max_len);
-int64_t kv_attention_blocks(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
-                            int max_len);   // workgroups of its largest launch
+int64_t kv_attention_blocks(int64_t B, int Hq, int Hkv, int D, int max_new,
+                            int max_len);   // workgroups of its largest grid
 hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipStream_t st);
 
 }  // namespace awq

@@ -161,8 +161,9 @@ __global__ __launch_bounds__(1024) void append_units_kernel(AppendArgs a) {
   __shared__ uint2 red[16];
   const KvArgs& c = a.c;
   constexpr bool kWave = HOLD == 1;   // one token: a wave takes a head, a workgroup four
-  const bool queries = (int)blockIdx.x >= a.kv_blocks;
-  uint32_t g = queries ? blockIdx.x - a.kv_blocks : blockIdx.x;
+  const uint32_t block = a.first_block + blockIdx.x;
+  const bool queries = block >= (uint32_t)a.kv_blocks;
+  uint32_t g = queries ? block - a.kv_blocks : block;
   const uint32_t fan = queries ? a.q_parts : kWave ? (c.Hkv + 3) / 4 : c.Hkv, low = g & 7;
   g >>= 3;
   const int part = (int)(g % fan);
@@ -328,7 +329,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   typedef typename TI::storage SI;
   __shared__ uint2 red[kThreads / 64];
   const KvArgs& c = a.c;
-  int g = blockIdx.x;
+  int g = (int)(a.first_block + blockIdx.x);
   const int j = g % a.pages_per_seq;
   g /= a.pages_per_seq;
   const int h = g % c.Hkv, b = g / c.Hkv;
@@ -440,10 +441,10 @@ template <class TO>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int blocks) {
   typedef typename TO::storage SO;
   const KvArgs& c = a.c;
-  int g = blockIdx.x;
-  const int part = g % blocks;
-  g /= blocks;
-  const int j = g % a.pages_per_seq, b = g / a.pages_per_seq;
+  uint32_t g = a.first_block + blockIdx.x;
+  const int part = (int)(g % (uint32_t)blocks);
+  g /= (uint32_t)blocks;
+  const int j = (int)(g % (uint32_t)a.pages_per_seq), b = (int)(g / (uint32_t)a.pages_per_seq);
   int64_t row0;
   int n;
   rows_of(c, b, row0, n);
@@ -504,21 +505,26 @@ bool go_units(AppendArgs a, hipStream_t st) {
   a.kv_blocks = (int)(eights * (wave ? (a.c.Hkv + 3) / 4 : a.c.Hkv) * 8);
   a.q_parts = (int)((tokens * a.Hq * units + 4 * threads - 1) / (4 * threads));   // four units a thread
   if (a.q_parts > a.c.Hkv) a.q_parts = a.c.Hkv;
-  const unsigned blocks = (unsigned)(a.kv_blocks + eights * a.q_parts * 8);
-  if (wave) append_units_kernel<TI, W, 1><<<blocks, threads, 0, st>>>(a);
-  else if (W == 8 || items <= 2048) append_units_kernel<TI, W, 2><<<blocks, threads, 0, st>>>(a);
-  else append_units_kernel<TI, 4, 4><<<blocks, threads, 0, st>>>(a);
+  in_parts(a.kv_blocks + eights * a.q_parts * 8, threads, [&](uint32_t first, unsigned grid) {
+    a.first_block = first;
+    if (wave) append_units_kernel<TI, W, 1><<<grid, threads, 0, st>>>(a);
+    else if (W == 8 || items <= 2048) append_units_kernel<TI, W, 2><<<grid, threads, 0, st>>>(a);
+    else append_units_kernel<TI, 4, 4><<<grid, threads, 0, st>>>(a);
+  });
   return true;
 }
 
 template <class TI>
-hipError_t go_append(const AppendArgs& a, hipStream_t st) {
+hipError_t go_append(AppendArgs a, hipStream_t st) {
   ProfScope prof("awq_kv_append", st);
   const bool done = a.rot % 16 == 0  ? go_units<TI, 8>(a, st)
                     : a.rot % 8 == 0 ? go_units<TI, 4>(a, st)
                                      : false;
   if (!done)
-    append_kernel<TI><<<(unsigned)((int64_t)a.pages_per_seq * a.c.Hkv * a.c.B), kThreads, 0, st>>>(a);
+    in_parts((int64_t)a.pages_per_seq * a.c.Hkv * a.c.B, kThreads, [&](uint32_t first, unsigned grid) {
+      a.first_block = first;
+      append_kernel<TI><<<grid, kThreads, 0, st>>>(a);
+    });
   return hipGetLastError();
 }
 
@@ -530,13 +536,15 @@ hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, hipStream_t st)
   return go_append<BF16T>(a, st);
 }
 
-hipError_t launch_kv_read(const ReadArgs& a, awq_dtype_t out, hipStream_t st) {
+hipError_t launch_kv_read(ReadArgs a, awq_dtype_t out, hipStream_t st) {
   const int blocks = (int)(((int64_t)a.c.Hkv * (a.c.P / 4) * (a.c.D / 8) + kThreads - 1) / kThreads);
-  const unsigned grid = (unsigned)((int64_t)a.pages_per_seq * blocks * a.c.B);
   ProfScope prof("awq_kv_read", st);
-  if (out == AWQ_F32) read_kernel<F32T><<<grid, kThreads, 0, st>>>(a, blocks);
-  else if (out == AWQ_F16) read_kernel<F16T><<<grid, kThreads, 0, st>>>(a, blocks);
-  else read_kernel<BF16T><<<grid, kThreads, 0, st>>>(a, blocks);
+  in_parts((int64_t)a.pages_per_seq * blocks * a.c.B, kThreads, [&](uint32_t first, unsigned grid) {
+    a.first_block = first;
+    if (out == AWQ_F32) read_kernel<F32T><<<grid, kThreads, 0, st>>>(a, blocks);
+    else if (out == AWQ_F16) read_kernel<F16T><<<grid, kThreads, 0, st>>>(a, blocks);
+    else read_kernel<BF16T><<<grid, kThreads, 0, st>>>(a, blocks);
+  });
   return hipGetLastError();
 }
 

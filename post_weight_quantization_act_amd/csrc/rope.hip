@@ -13,8 +13,9 @@ namespace awq {
 namespace {
 
 __global__ __launch_bounds__(256) void rope_table_kernel(int64_t n_pos, int half,
-                                                         RopeFreqs fr, float2* table) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                         RopeFreqs fr, float2* table,
+                                                         uint32_t first) {
+  const int64_t e = ((int64_t)first + blockIdx.x) * 256 + threadIdx.x;
   if (e >= n_pos * half) return;
   const int64_t p = e / half;
   const int i = (int)(e % half);
@@ -40,7 +41,7 @@ __global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int rows_pe
   const uint32_t work = (uint32_t)units * (uint32_t)blocks;     // threads' items of a row
   const uint32_t per_row = work < 256 ? work : 256;
   const uint32_t r = threadIdx.x / per_row;
-  const int64_t row = (int64_t)blockIdx.x * rows_per_block + r;
+  const int64_t row = ((int64_t)a.first_block + blockIdx.x) * rows_per_block + r;
   if ((int)r >= rows_per_block || row >= a.B * a.S) return;
   int64_t b, s;
   if ((uint64_t)(a.B * a.S) >> 32) {
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   typedef typename TO::storage SO;
   const int half = a.rot >> 1;
   const int units = half + (a.D - a.rot);   // pairs, then the columns left as they are
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t e = ((int64_t)a.first_block + blockIdx.x) * 256 + threadIdx.x;
   if (e >= a.B * a.S * a.H * units) return;
   const int u = (int)(e % units);
   int64_t r = e / units;
@@ -112,15 +113,18 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
 }
 
 template <class TI, class TO, int W, int HB>
-void go_units(const RopeArgs& a, hipStream_t st) {
+void go_units(RopeArgs a, hipStream_t st) {
   const int64_t work = (int64_t)units_of<W>(a.D, a.rot) * ((a.H + HB - 1) / HB);
   const int rows = work < 256 ? (int)(256 / work) : 1;
   const int64_t blocks = (a.B * a.S + rows - 1) / rows;
-  rope_units_kernel<TI, TO, W, HB><<<(unsigned)blocks, 256, 0, st>>>(a, rows);
+  in_parts(blocks, 256, [&](uint32_t first, unsigned grid) {
+    a.first_block = first;
+    rope_units_kernel<TI, TO, W, HB><<<grid, 256, 0, st>>>(a, rows);
+  });
 }
 
 template <class TI, class TO>
-hipError_t go(const RopeArgs& a, hipStream_t st) {
+hipError_t go(RopeArgs a, hipStream_t st) {
   ProfScope prof("awq_rope", st);
   if (a.rot % 16 == 0 && a.D % 8 == 0) {
     // four heads a thread for 2M units and more (4M units 74.9 against 79.0 us); one for fewer,
@@ -132,7 +136,10 @@ hipError_t go(const RopeArgs& a, hipStream_t st) {
     go_units<TI, TO, 4, 1>(a, st);
   } else {
     const int64_t n = a.B * a.S * a.H * (a.rot / 2 + a.D - a.rot);
-    rope_kernel<TI, TO><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+    in_parts((n + 255) / 256, 256, [&](uint32_t first, unsigned grid) {
+      a.first_block = first;
+      rope_kernel<TI, TO><<<grid, 256, 0, st>>>(a);
+    });
   }
   return hipGetLastError();
 }
@@ -150,8 +157,9 @@ hipError_t launch_rope_table(int64_t n_pos, int rot, const RopeFreqs& fr, float*
                              hipStream_t st) {
   const int64_t n = n_pos * (rot / 2);
   ProfScope prof("awq_rope_table", st);
-  rope_table_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(n_pos, rot / 2, fr,
-                                                                 (float2*)table);
+  in_parts((n + 255) / 256, 256, [&](uint32_t first, unsigned grid) {
+    rope_table_kernel<<<grid, 256, 0, st>>>(n_pos, rot / 2, fr, (float2*)table, first);
+  });
   return hipGetLastError();
 }
 

@@ -186,3 +186,109 @@ def test_attention_over_more_tiles_than_half_a_32_bit_sum():
     out, lse = awq.awq_kv_attention(cache, q, ints([tokens] * B), pages, max_len=tokens, return_lse=True, workspace=ws)
     assert (np.abs(wide(out) - 1) <= 3 * 2.0 ** -4).all()
     assert (np.abs(wide(lse) - 28 * np.log(2)) <= 2 * 2.0 ** -4).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# more workgroups than one launch holds (2^32 threads): bounds far above what a call has
+# ---------------------------------------------------------------------------------------------
+FAR = 1 << 28    # rows of a sequence: 2^24 pages of 16 tokens
+
+
+def test_append_and_read_with_a_far_bound():
+    rng = np.random.default_rng(22)
+    dev, ref = new_cache(rng, 6, 1, 16, 8)
+    table = page_table(rng, 2, 6, 3)
+    k = torch.from_numpy(rng.standard_normal((40, 1, 8)).astype(f32)).cuda()
+    starts, lens = [0, 30, 40], [40, 10]
+    for rope in (None, awq.awq_rope_table(64, 6)):       # vectors, pair by pair
+        turned = wide(k) if rope is None else kv_ref.rope(wide(k), wide(rope), list(range(10, 40)) + list(range(10)))
+        q = awq.awq_kv_append(dev, k, k, ints(lens), ints(table.tolist()), starts=ints(starts), max_new=FAR,
+                              table=rope, q=k)
+        np.testing.assert_array_equal(wide(q), turned)
+        ref.append(turned, wide(k), lens, table, starts)
+        for b, n in enumerate(lens):
+            p, t = table[b, n // 16], n % 16
+            ref.k_codes[p, :, t:] = dev.k_codes[p, :, t:].cpu().numpy()
+            ref.v_codes[p, :, :, t:] = dev.v_codes[p, :, :, t:].cpu().numpy()
+        assert_same_cache(dev, ref)
+    got = awq.awq_kv_read(dev, ints([10, 0]), ints(table.tolist()), starts=ints(starts), total=40, max_count=FAR)
+    want = [ref.tokens(0, 10, 40, table), ref.tokens(1, 0, 10, table)]
+    for i in (0, 1):
+        np.testing.assert_array_equal(wide(got[i]), np.concatenate([w[i] for w in want]))
+
+
+def test_attention_with_a_far_bound():
+    rng = np.random.default_rng(23)
+    dev, ref = new_cache(rng, 8, 1, 16, 32)
+    table = page_table(rng, 1, 8, 8)
+    q = torch.from_numpy(rng.standard_normal((90, 2, 32)).astype(f32)).half().cuda()
+    check_attention(dev, ref, q, [120], table, [0, 90], "f16", max_new=2 ** 30 - 1, max_len=128)
+
+
+@pytest.mark.parametrize("rot", [0, 6])
+def test_append_and_read_of_many_sequences_with_the_default_bounds(rot):
+    """2^12 sequences of 64 of 2^18 rows, any of which might have them all: 2^26 pages, one by one."""
+    B, n = 1 << 12, 64
+    gen = torch.Generator(device="cuda").manual_seed(26)
+    k = torch.randn((B * n, 1, 8), generator=gen, device="cuda")
+    pages = torch.randperm(4 * B, generator=gen, device="cuda").int().view(B, 4)
+    lens, starts = ints([n] * B), torch.arange(0, B * n + 1, n, device="cuda", dtype=torch.int32)
+    table = awq.awq_rope_table(n, rot) if rot else None
+    got = []
+    for bound in (None, n):
+        cache = awq.KvCache.empty(4 * B, 1, 16, 8)
+        q = awq.awq_kv_append(cache, k, -k, lens, pages, starts=starts, max_new=bound, table=table, q=k)
+        back = awq.awq_kv_read(cache, lens - n, pages, starts=starts, total=B * n, max_count=bound)
+        got.append((q, cache.k_codes, cache.v_codes, cache.k_steps, cache.v_steps, *back))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(got[0][0], k) if not rot else torch.equal(got[0][0][..., 6:], k[..., 6:])
+    assert (got[0][6] + k).abs().max() <= k.abs().max() / 254 * 1.001       # half a step
+
+
+def test_attention_of_many_sequences_with_the_default_bounds():
+    B, n = 1 << 12, 64
+    gen = torch.Generator(device="cuda").manual_seed(27)
+    cache = awq.KvCache.empty(4 * B, 1, 16, 8)
+    q = torch.randn((B * n, 8, 8), generator=gen, device="cuda").half()
+    pages = torch.randperm(4 * B, generator=gen, device="cuda").int().view(B, 4)
+    lens, starts = ints([n] * B), torch.arange(0, B * n + 1, n, device="cuda", dtype=torch.int32)
+    awq.awq_kv_append(cache, q[:, :1], q[:, 1:2], lens, pages, starts=starts, max_new=n)
+    want = awq.awq_kv_attention(cache, q, lens, pages, starts=starts, max_new=n)
+    assert torch.equal(awq.awq_kv_attention(cache, q, lens, pages, starts=starts), want)
+
+
+def test_attention_of_more_sequences_than_a_launch_has_workgroups():
+    """2^24 sequences of one token, which might have 4112: two splits each, and their join."""
+    B = 1 << 24
+    cache = awq.KvCache(*(torch.full(s, 130, dtype=torch.uint8, device="cuda") for s in ((1, 1, 16, 8), (1, 1, 8, 16))),
+                        torch.ones(1, 1, device="cuda"), torch.ones(1, 1, device="cuda"))
+    q = torch.randn((B, 1, 8), device="cuda").half()
+    out, lse = awq.awq_kv_attention(cache, q, torch.ones(B, dtype=torch.int32, device="cuda"),
+                                    torch.zeros((B, 257), dtype=torch.int32, device="cuda"), scale=0.5, return_lse=True)
+    assert (out == 2).all()
+    # one score of eight products, a few roundings of 2^-24 of at most 8 x 2 x 6
+    assert (lse.double() - q.double().sum(-1)).abs().max() <= 16 * 2.0 ** -24 * 96
+
+
+def test_rope_table_of_more_pairs_than_a_launch_has_threads():
+    n = 1 << 32
+    table = awq.awq_rope_table(n, 2)
+    at = [0, 1, 12345, (1 << 32) - 257, (1 << 32) - 256, (1 << 32) - 1]
+    got = table[at, 0].cpu().numpy()
+    want = np.stack([np.cos(np.array(at, float)), np.sin(np.array(at, float))], -1)
+    assert (np.abs(got - want) <= 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dim,rot", [(2, 2), (8, 8)])
+def test_rope_of_more_items_than_a_launch_has_threads(dim, rot):
+    """2^32 pairs one by one; and 2^24 rows of 129 vectors, a workgroup each."""
+    S, H = (1 << 22, (1 << 10) + 1) if dim == 2 else (1 << 24, 129)
+    x = torch.randn((1, H, dim), device="cuda").bfloat16().expand(S, H, dim)
+    table = awq.awq_rope_table(2, rot)
+    at = torch.zeros(S, dtype=torch.int32, device="cuda")
+    at[-1] = 1
+    out = awq.awq_rope(x, table, at)
+    want = awq.awq_rope(x[:1], table, at[:1])
+    for part, x0 in ((out[:-1].split(1 << 20), want), (out[-1:].split(1), awq.awq_rope(x[-1:], table, at[-1:]))):
+        for p in part:
+            assert torch.equal(p, x0.expand_as(p))
