@@ -927,10 +927,10 @@ awq_status_t awq_kv_append(const awq_kv_cache_t* cache, const void* k, const voi
     return fail(AWQ_ERR_INVALID_ARG, "rot=%d must be even, in [2, head_dim=%d], n_pos >= 1", rot,
                 a.c.D);
   if (!table && rot != 0) return fail(AWQ_ERR_INVALID_ARG, "rot=%d without a table", rot);
+  if (T == 0 || B == 0) return AWQ_OK;   // an empty q may be a null pointer
   if (q ? (Hq < 1 || Hq % a.c.Hkv != 0 || Hq > kMaxHeads) : Hq != 0)
     return fail(AWQ_ERR_INVALID_ARG, "Hq=%lld must be a multiple of kv_heads=%d (0 without q)",
                 (long long)Hq, a.c.Hkv);
-  if (T == 0 || B == 0) return AWQ_OK;
   max_new = std::min(max_new, T);
   if (!k || !v || !kv_strides || !lens || (q && (!q_out || !q_strides)))
     return fail(AWQ_ERR_INVALID_ARG, "null pointer");

@@ -122,6 +122,14 @@ def test_read_of_the_first_tokens(most):
         assert (wide(got)[~taken] == 7).all()
 
 
+def test_append_of_no_rows():
+    cache = awq.KvCache.empty(2, 2, 16, 16)
+    k = torch.zeros((3, 6, 16), device="cuda")
+    q = awq.awq_kv_append(cache, k[:0, :2], k[:0, 2:4], ints([5]), ints([[0, 1]]), starts=ints([0, 0]), q=k[:0],
+                          q_dtype=torch.float16)
+    assert q.shape == (0, 6, 16) and q.dtype == torch.float16
+
+
 # ---------------------------------------------------------------------------------------------
 # windows and lengths
 # ---------------------------------------------------------------------------------------------
