@@ -546,8 +546,12 @@ awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, 
  *   sums and outputs are held in fp32; probabilities are rounded to fp16
  *   before they weigh the values; a value step below 2^-100 counts as 0.  scale
  *   finite and >= 0.  Rows that belong to no sequence are not written.  Results
- *   are reproducible.  workspace: awq_kv_attention_workspace_size(T, B, Hq,
- *   kv_heads, D, max_new, max_len) bytes, 256-byte aligned, may be NULL when that is 0.
+ *   are reproducible.  workspace, 256-byte aligned:
+ *   awq_kv_attention_workspace_size(T, B, Hq, kv_heads, D, max_new, max_len) bytes are
+ *   enough for this call and every other one of these heads with at most these T <= B
+ *   max_new, B, max_new and max_len (a program keeps one for its largest);
+ *   awq_kv_attention_workspace_needed says what the call with these alone needs, where
+ *   max_len is not above max_pages page.  It may be NULL when that is 0.
  * ------------------------------------------------------------------------ */
 typedef struct {
   uint8_t* k_codes;
@@ -572,6 +576,8 @@ awq_status_t awq_kv_read(const awq_kv_cache_t* cache, int64_t T, const int32_t* 
                          hipStream_t stream);
 size_t awq_kv_attention_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t kv_heads,
                                        int64_t D, int64_t max_new, int64_t max_len);
+size_t awq_kv_attention_workspace_needed(int64_t T, int64_t B, int64_t Hq, int64_t kv_heads,
+                                         int64_t D, int64_t max_new, int64_t max_len);
 awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dtype_t dtype,
                               int64_t T, int64_t Hq, const int64_t* q_strides,
                               const int32_t* starts, const int32_t* lens, int64_t B,

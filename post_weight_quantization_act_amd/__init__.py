@@ -30,7 +30,7 @@ __all__ = [
     "awq_w8a8_workspace_size", "awq_w8a8_loss",
     "AWQ_ROPE_INTERLEAVED", "AWQ_ROPE_TRANSPOSE", "AWQ_ATT_FULL", "KvCache",
     "awq_rope_table", "awq_rope", "awq_kv_append", "awq_kv_read",
-    "awq_kv_attention_workspace_size", "awq_kv_attention",
+    "awq_kv_attention_workspace_size", "awq_kv_attention_workspace_needed", "awq_kv_attention",
     "awq_profile_enable", "awq_profile_select", "awq_profile_read", "awq_profile_reset",
     "packed_words_per_row",
 ]
@@ -146,6 +146,7 @@ _SIGS = {
                        _U32, _P, _P, _I64, _P, _P, _I32, _P], _I32),
     "awq_kv_read": ([_P, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
     "awq_kv_attention_workspace_size": ([_I64] * 7, _SZ),
+    "awq_kv_attention_workspace_needed": ([_I64] * 7, _SZ),
     "awq_kv_attention": ([_P, _P, _I32, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _D,
                           _I64, _U32, _P, _P, _P, _SZ, _P], _I32),
     "awq_profile_enable": ([_I32], _I32),
@@ -742,7 +743,14 @@ def awq_kv_read(cache: KvCache, first: torch.Tensor, pages: torch.Tensor,
 
 def awq_kv_attention_workspace_size(T: int, B: int, Hq: int, kv_heads: int, D: int, max_new: int,
                                     max_len: int) -> int:
+    """Bytes that are enough for every call with at most these T (<= B max_new), B, max_new and max_len."""
     return int(library().awq_kv_attention_workspace_size(T, B, Hq, kv_heads, D, max_new, max_len))
+
+
+def awq_kv_attention_workspace_needed(T: int, B: int, Hq: int, kv_heads: int, D: int, max_new: int,
+                                      max_len: int) -> int:
+    """Bytes that the call with these sizes needs (max_len not above what the page table holds)."""
+    return int(library().awq_kv_attention_workspace_needed(T, B, Hq, kv_heads, D, max_new, max_len))
 
 
 def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor,
@@ -773,7 +781,7 @@ def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages:
         ws = _dense(workspace, "workspace", gpu, workspace.shape, workspace.dtype)
         size = workspace.nbytes
     else:
-        ws, size = None, (_LIB or library()).awq_kv_attention_workspace_size(
+        ws, size = None, (_LIB or library()).awq_kv_attention_workspace_needed(
             T, B, Hq, cache.kv_heads, D, max_new, max_len)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)

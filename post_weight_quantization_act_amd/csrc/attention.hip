@@ -911,6 +911,37 @@ size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int m
   return p.splits == 1 ? 0 : (size_t)p.splits * T * Hq * (D + 2) * 4 + 4;
 }
 
+// Covers every call of these heads with at most these T, B, max_new and max_len whose rows
+// are at most its own B max_new, and this one whatever its page table holds.  In rows of
+// partial results, splits times rows of a call are, by plan():
+//   any: a split takes at least eight tiles, so at most `most` times its rows;
+//   as many workgroups as run at once: splits times groups are at most 512, and rows at most
+//     groups times a row tile;
+//   chosen by the kernel (up to 64 rows a group, 2 to 256 sequences): whole splits times groups
+//     at most 8192, and one more;
+//   more sequences: at most eight splits.
+size_t kv_attention_ws_bound(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
+                             int max_len) {
+  const int64_t most = ((max_len + kTile - 1) / kTile + 7) / 8, G = Hq / Hkv;
+  if (most <= 1) return 0;
+  const auto upto = [&](int64_t rows, int64_t cap) { return rows > cap / most ? cap : rows * most; };
+  const int64_t tile = D <= 192 ? 32 : 16;
+  int64_t n = upto(T * Hq, 512 * (max_new * G > 64 ? 128 : tile));
+  if (G <= 64) {
+    const int64_t few = 64 / G;     // rows of a sequence that make 64 of a group
+    if (B > 1) {
+      const int64_t rows = std::min(T, std::min<int64_t>(B, 256) * few) * Hq;
+      n = std::max(n, upto(rows, 8192 * tile + rows));
+    }
+    if (B > 256) n = std::max(n, std::min(T, B * few) * Hq * std::min<int64_t>(most, 8));
+  }
+  if (T > B * max_new) {            // rows that no sequence may have are counted all the same
+    const int64_t groups = B * Hkv * plan(B, Hq, Hkv, D, max_new, max_len).row_tiles;
+    n = std::max(n, std::min(most, 8192 / groups + 9) * T * Hq);
+  }
+  return (size_t)n * (D + 2) * 4 + 4;
+}
+
 int64_t kv_attention_blocks(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
   if (max_new > (int64_t)INT32_MAX / Hq) return INT64_MAX;
   const Plan p = plan(B, Hq, Hkv, D, max_new, max_len);

@@ -42,6 +42,8 @@ constexpr int64_t kLowbitGemmMaxM = 65535ll * 128;  // activation-row tiles on g
 constexpr int64_t kLowbitGemmMaxK = 1ll << 22;       // a 256-row activation tile in 32-bit offsets
 constexpr int64_t kMaxGrid = INT32_MAX;               // workgroups of a grid (launched in parts)
 constexpr int kMaxHeads = 16384;
+constexpr int64_t kMaxTokens = 1ll << 30;             // of a sequence
+constexpr int64_t kMaxRows = 1ll << 36;               // queries of one attention call, all heads
 
 int esize(awq_dtype_t dt) { return dt == AWQ_F32 ? 4 : 2; }
 
@@ -216,6 +218,18 @@ awq_status_t kv_args(const awq_kv_cache_t* cache, int64_t T, const int32_t* star
   a->p_shift = 0;
   while ((1 << a->p_shift) < a->P) ++a->p_shift;
   return AWQ_OK;
+}
+
+// A size of the cache attention's workspace; 0 for what the call refuses.
+template <class F>
+size_t kv_workspace(F bytes, int64_t T, int64_t B, int64_t Hq, int64_t kv_heads, int64_t D,
+                    int64_t max_new, int64_t max_len) {
+  if (T < 1 || B < 1 || kv_heads < 1 || Hq < 1 || Hq % kv_heads != 0 || D < 1 || max_new < 1 ||
+      max_len < 1 || T > INT32_MAX || B > INT32_MAX || Hq > kMaxHeads || D > 256 ||
+      max_new > INT32_MAX / 2 || T > kMaxRows / Hq)
+    return 0;
+  return align_up(bytes(T, B, (int)Hq, (int)kv_heads, (int)D, (int)std::min(max_new, T),
+                        (int)std::min(max_len, kMaxTokens)));
 }
 
 }  // namespace
@@ -989,13 +1003,12 @@ awq_status_t awq_kv_read(const awq_kv_cache_t* cache, int64_t T, const int32_t* 
 
 size_t awq_kv_attention_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t kv_heads,
                                        int64_t D, int64_t max_new, int64_t max_len) {
-  if (T < 1 || B < 1 || kv_heads < 1 || Hq < 1 || Hq % kv_heads != 0 || D < 1 || max_new < 1 ||
-      max_len < 1 || T > INT32_MAX || B > INT32_MAX || Hq > kMaxHeads || D > 256 ||
-      max_new > INT32_MAX / 2 || max_len > (1 << 30))
-    return 0;
-  max_new = std::min(max_new, T);
-  return align_up(awq::kv_attention_ws_bytes(T, B, (int)Hq, (int)kv_heads, (int)D, (int)max_new,
-                                             (int)max_len));
+  return kv_workspace(awq::kv_attention_ws_bound, T, B, Hq, kv_heads, D, max_new, max_len);
+}
+
+size_t awq_kv_attention_workspace_needed(int64_t T, int64_t B, int64_t Hq, int64_t kv_heads,
+                                         int64_t D, int64_t max_new, int64_t max_len) {
+  return kv_workspace(awq::kv_attention_ws_bytes, T, B, Hq, kv_heads, D, max_new, max_len);
 }
 
 awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dtype_t dtype,
@@ -1026,12 +1039,14 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
   if (!q || !q_strides || !lens || !out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
   if (!aligned(q, 2) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4))
     return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned (out: to 16 bytes)");
+  if (T > kMaxRows / Hq)
+    return fail(AWQ_ERR_UNSUPPORTED, "more than %lld rows of a head", (long long)kMaxRows);
   const int64_t reach = std::max<int64_t>(1, std::min<int64_t>(max_len, max_pages * a.c.P));
-  if (reach > (1 << 30))
+  if (reach > kMaxTokens)
     return fail(AWQ_ERR_UNSUPPORTED, "%lld tokens of a sequence exceed 2^30", (long long)reach);
   if (awq::kv_attention_blocks(B, (int)Hq, a.c.Hkv, a.c.D, (int)max_new, (int)reach) > kMaxGrid)
     return fail(AWQ_ERR_UNSUPPORTED, "too many rows for one call");
-  const size_t need = awq_kv_attention_workspace_size(T, B, Hq, a.c.Hkv, a.c.D, max_new, reach);
+  const size_t need = awq_kv_attention_workspace_needed(T, B, Hq, a.c.Hkv, a.c.D, max_new, reach);
   if (need > 0) {
     if (!workspace || workspace_bytes < need)
       return fail(AWQ_ERR_WORKSPACE, "kv_attention needs %zu workspace bytes, got %zu", need,

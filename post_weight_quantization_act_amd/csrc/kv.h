@@ -268,7 +268,9 @@ hipError_t launch_rope(const RopeArgs& a, awq_dtype_t in, awq_dtype_t out, hipSt
 hipError_t launch_kv_append(const AppendArgs& a, awq_dtype_t in, hipStream_t st);
 hipError_t launch_kv_read(ReadArgs a, awq_dtype_t out, hipStream_t st);
 size_t kv_attention_ws_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
-                             int max_len);
+                             int max_len);   // of this call
+size_t kv_attention_ws_bound(int64_t T, int64_t B, int Hq, int Hkv, int D, int max_new,
+                             int max_len);   // of it and every smaller one
 int64_t kv_attention_blocks(int64_t B, int Hq, int Hkv, int D, int max_new,
                             int max_len);   // workgroups of its largest grid
 hipError_t launch_kv_attention(const AttArgs& a, awq_dtype_t dt, void* ws, hipStream_t st);
