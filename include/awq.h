@@ -62,13 +62,14 @@
 extern "C" {
 #endif
 
-/* AWQ_DTYPE_MAX_ENUM is no dtype: it gives the enumeration the range of a
- * 32-bit int, so that whatever value a caller passes is a valid value for the
- * library to check (and refuse), in C and in C++ alike. */
+/* AWQ_DTYPE_MIN_ENUM and AWQ_DTYPE_MAX_ENUM are no dtypes: they give the
+ * enumeration the range of a 32-bit int, so that whatever value a caller passes
+ * is a valid value for the library to check (and refuse), in C and in C++ alike. */
 typedef enum {
   AWQ_F32 = 0,
   AWQ_F16 = 1,
   AWQ_BF16 = 2,
+  AWQ_DTYPE_MIN_ENUM = -0x7fffffff - 1,
   AWQ_DTYPE_MAX_ENUM = 0x7fffffff
 } awq_dtype_t;
 
@@ -479,6 +480,7 @@ typedef enum {
   AWQ_ROPE_SCALING_LINEAR = 1,
   AWQ_ROPE_SCALING_TURNS = 2,
   AWQ_ROPE_SCALING_LOG_TURNS = 3,
+  AWQ_ROPE_SCALING_MIN_ENUM = -0x7fffffff - 1,   /* the range of an int, as above */
   AWQ_ROPE_SCALING_MAX_ENUM = 0x7fffffff
 } awq_rope_scaling_kind_t;
 typedef struct {

@@ -1,14 +1,15 @@
 """What the rotary and cache entry points decide on the host, at the edges of their sizes (CPU): the
 C calls get pointers that are never followed, and return before anything is enqueued."""
 
+import ctypes
 import random
 import re
 
 import pytest
 
 import post_weight_quantization_act_amd as awq
-from test_kv_abi import (INVALID, UNSUPPORTED, WORKSPACE, append_args, attention_args, cache, rope_args, status,
-                         strides)
+from test_kv_abi import (INVALID, UNSUPPORTED, WORKSPACE, append_args, attention_args, cache, read_args, rope_args,
+                         status, strides, table_args)
 
 
 def test_rope_refuses_rows_past_its_items():
@@ -79,3 +80,15 @@ def test_the_workspace_stays_in_bounds():
     assert size(64, 64, 64, 8, 128, 1, 512) == 0 and needed(64, 64, 64, 8, 128, 1, 512) == 0
     assert status("awq_kv_attention", attention_args(T=(1 << 31) - 1, Hq=64, cache=cache(kv_heads=64))) == UNSUPPORTED
     assert size((1 << 31) - 1, 2, 64, 64, 64, 1, 4096) == 0
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 9, 2 ** 31 - 1])
+def test_enumerations_of_any_value_are_refused(bad):
+    for name in ("x_dtype", "out_dtype"):
+        assert status("awq_rope", rope_args(**{name: bad})) == INVALID
+    for name in ("dtype", "q_dtype"):
+        assert status("awq_kv_append", append_args(**{name: bad})) == INVALID
+    assert status("awq_kv_attention", attention_args(dtype=bad)) == INVALID
+    assert status("awq_kv_read", read_args(dtype=bad)) == INVALID
+    scaling = ctypes.byref(awq.RopeScaling(bad, 1, 1, 1, 2, 1))
+    assert status("awq_rope_table", table_args(scaling=scaling)) == INVALID
