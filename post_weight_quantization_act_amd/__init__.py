@@ -603,9 +603,12 @@ def awq_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor | Non
     """x [T, H, D] or [B, S, H, D] (any strides, the last dimension contiguous) with each
     head's first 2 * table.shape[1] columns turned by the row's position; transpose=True gives the
     gradient with respect to x.  positions int32 [T], [S] or [B, S]; None: the row's index.
-    out may be x."""
+    out may be x.  Where x requires a gradient the rotation is recorded; into a given out
+    it is not."""
     if not isinstance(x, _Tensor) or not x.is_cuda:
         _refuse(x, "x", -1, "on a GPU")
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        return _RopeGrad.apply(x, table, positions, interleaved, transpose, out_dtype)
     gpu, shape, xs, dtype = x.get_device(), x.shape, x.stride(), x.dtype
     if len(shape) == 4:
         B, S, H, D = shape
@@ -636,10 +639,28 @@ def awq_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor | Non
     return out
 
 
+class _RopeGrad(torch.autograd.Function):
+    """The rotation and, as its gradient, the one the other way."""
+
+    @staticmethod
+    def forward(ctx, x, table, positions, interleaved, transpose, out_dtype):
+        ctx.save_for_backward(table, positions)
+        ctx.rest = interleaved, transpose, x.dtype
+        return awq_rope(x, table, positions, interleaved, transpose, out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, g):
+        table, positions = ctx.saved_tensors
+        interleaved, transpose, dtype = ctx.rest
+        g = g if g.stride(-1) == 1 else g.contiguous()
+        return awq_rope(g, table, positions, interleaved, not transpose, out_dtype=dtype), *[None] * 5
+
+
 class KvCache:
     """A paged key/value cache in 8 bits: k_codes uint8 [n_pages, kv_heads, page, D],
     v_codes uint8 [n_pages, kv_heads, D, page], k_steps and v_steps fp32 [n_pages, kv_heads].
-    Holds the tensors; which page is whose is the caller's (page tables)."""
+    Holds the tensors; which page is whose is the caller's (page tables).  Appending, reading and
+    attention record nothing for gradients."""
 
     def __init__(self, k_codes, v_codes, k_steps, v_steps):
         if not isinstance(k_codes, _Tensor) or not k_codes.is_cuda or k_codes.dim() != 4:

@@ -300,3 +300,40 @@ def test_rope_of_more_items_than_a_launch_has_threads(dim, rot):
     for part, x0 in ((out[:-1].split(1 << 20), want), (out[-1:].split(1), awq.awq_rope(x[-1:], table, at[-1:]))):
         for p in part:
             assert torch.equal(p, x0.expand_as(p))
+
+
+# ---------------------------------------------------------------------------------------------
+# the rotation's gradient is recorded
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("into,out", [("f32", "f32"), ("f32", "bf16"), ("f16", "f16"), ("bf16", "f32")])
+def test_rope_records_its_gradient(into, out, interleaved):
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    table = awq.awq_rope_table(50, 24)
+    base = torch.randn((2, 7, 5, 32), generator=gen, device="cuda").to(TYPES[into])
+    leaf = base.clone().requires_grad_()
+    at = torch.randint(0, 50, (2, 7), generator=gen, device="cuda", dtype=torch.int32)
+    x = leaf[:, :, 1:4].transpose(1, 2).transpose(1, 2)          # a view with strides of its own
+    y = awq.awq_rope(x, table, at, interleaved=interleaved, out_dtype=TYPES[out])
+    assert torch.equal(y, awq.awq_rope(base[:, :, 1:4], table, at, interleaved=interleaved, out_dtype=TYPES[out]))
+    g = torch.randn(y.shape, generator=gen, device="cuda").to(y.dtype)
+    y.backward(g)
+    want = torch.zeros_like(base)
+    want[:, :, 1:4] = awq.awq_rope(g, table, at, interleaved=interleaved, transpose=True, out_dtype=TYPES[into])
+    assert leaf.grad.dtype == leaf.dtype and torch.equal(leaf.grad, want)
+
+
+def test_rope_gradients_of_a_broadcast_sum_and_of_the_gradient():
+    table = awq.awq_rope_table(9, 8)
+    x = torch.randn(1, 2, 8, device="cuda", requires_grad=True)
+    y = awq.awq_rope(x.expand(9, 2, 8), table)
+    (gx,) = torch.autograd.grad(y.sum(), x)                      # the sum's gradient has no strides
+    rows = awq.awq_rope(torch.ones(9, 2, 8, device="cuda"), table, transpose=True)
+    assert torch.equal(gx, rows.sum(0, keepdim=True))
+    g = torch.randn(9, 2, 8, device="cuda", requires_grad=True)
+    (gx,) = torch.autograd.grad(awq.awq_rope(x.expand(9, 2, 8), table), x, g, create_graph=True)
+    h = torch.randn_like(gx)
+    (gg,) = torch.autograd.grad(gx, g, h)
+    assert torch.equal(gg, awq.awq_rope(h.expand(9, 2, 8), table))
+    with torch.no_grad():
+        assert not awq.awq_rope(x, table).requires_grad
