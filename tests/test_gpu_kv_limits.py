@@ -337,3 +337,80 @@ def test_rope_gradients_of_a_broadcast_sum_and_of_the_gradient():
     assert torch.equal(gg, awq.awq_rope(h.expand(9, 2, 8), table))
     with torch.no_grad():
         assert not awq.awq_rope(x, table).requires_grad
+
+
+# ---------------------------------------------------------------------------------------------
+# instances that the other shapes do not reach
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -70, 2.0 ** -61 * 127, 2.0 ** 60 * 127, 2.0 ** 64, 2.0 ** 110])
+def test_append_of_values_whose_steps_are_scaled(size, kind):
+    """Steps below 2^-60 and above 2^60, where codes come from scaled quotients, and next to them."""
+    rng = np.random.default_rng(25)
+    dev, ref = new_cache(rng, 4, 2, 16, 32, steps=(0.0, 0.0))
+    table = page_table(rng, 1, 4, 3)
+    at = 0
+    for n, factor in ((5, 0.5), (20, 1.0), (1, 4.0), (9, 2.0 ** -8)):
+        k, v = (torch.from_numpy((rng.standard_normal((n, 2, 32)) * size * factor).astype(f32)).to(TYPES[kind]).cuda()
+                for _ in range(2))
+        at += n
+        awq.awq_kv_append(dev, k, v, ints([at]), ints(table.tolist()), starts=ints([0, n]), max_new=n)
+        ref.append(wide(k), wide(v), [at], table, [0, n])
+    k, v = awq.awq_kv_read(dev, ints([0]), ints(table.tolist()), starts=ints([0, at]), total=at)
+    want = ref.tokens(0, 0, at, table)
+    np.testing.assert_array_equal(wide(k), want[0])
+    np.testing.assert_array_equal(wide(v), want[1])
+
+
+FULL_PAGES = [   # new tokens, tokens before, D, rot, page: four units of four pairs a thread
+    (600, 3, 72, 72, 256), (259, 250, 120, 8, 256), (300, 0, 128, 120, 256), (500, 9, 104, 24, 256), (257, 127, 256, 248, 128),
+    (130, 100, 200, 104, 128),
+]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", FULL_PAGES)
+def test_append_of_full_pages_by_runs_of_four(shape, kind, interleaved):
+    new, before, dim, rot, page = shape
+    rng = np.random.default_rng(new + dim)
+    length = new + before
+    per_seq = -(-length // page)
+    dev, ref = new_cache(rng, per_seq + 1, 2, page, dim)
+    table = page_table(rng, 1, dev.n_pages, per_seq)
+    qkv = torch.from_numpy(rng.standard_normal((new, 6, dim)).astype(f32)
+                           * rng.choice([0.3, 30.0], (new, 1, 1)).astype(f32)).to(TYPES[kind]).cuda()
+    rope = awq.awq_rope_table(length, rot)
+    at = np.arange(before, length)
+    q = awq.awq_kv_append(dev, qkv[:, 2:4], qkv[:, 4:], ints([length]), ints(table.tolist()), starts=ints([0, new]),
+                          max_new=new, table=rope, interleaved=interleaved, q=qkv[:, :2], q_dtype=torch.float32)
+    turn = lambda x: kv_ref.rope(wide(x), wide(rope), at, interleaved)       # noqa: E731
+    np.testing.assert_array_equal(wide(q), turn(qkv[:, :2]))
+    ref.append(turn(qkv[:, 2:4]), wide(qkv[:, 4:]), [length], table, [0, new])
+    if length % page:
+        p, t = table[0, length // page], length % page
+        ref.k_codes[p, :, t:] = dev.k_codes[p, :, t:].cpu().numpy()
+        ref.v_codes[p, :, :, t:] = dev.v_codes[p, :, :, t:].cpu().numpy()
+    assert_same_cache(dev, ref)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", ["one short", "one long", "uneven", "two tiles", "two tiles long",
+                                  "two tiles uneven", "many"])
+@pytest.mark.parametrize("dim", [104, 120, 128, 136, 160, 168, 192, 200, 224, 256])
+def test_attention_of_every_width(dim, rows, kind):
+    """The kernels' instances above 96 columns, by each of their forms: eight waves, splits that are joined, splits that
+    the lengths choose, 17 to 64 rows of a head, and more."""
+    new, lens, hq, heads, page = {
+        "one short": ([1, 1], [300, 77], 8, 2, 16), "one long": ([1], [2600], 16, 1, 64),
+        "uneven": ([1, 1, 1], [1500, 4, 700], 8, 2, 32), "two tiles": ([9, 4], [333, 90], 8, 2, 64),
+        "two tiles long": ([13], [2600], 6, 2, 64), "two tiles uneven": ([9, 2, 5], [700, 1500, 30], 8, 2, 16),
+        "many": ([50, 21], [200, 90], 4, 2, 32)}[rows]
+    rng = np.random.default_rng(dim + len(rows))
+    per_seq = -(-max(lens) // page)
+    dev, ref = new_cache(rng, len(new) * per_seq, heads, page, dim)
+    table = page_table(rng, len(new), dev.n_pages, per_seq)
+    q = torch.from_numpy(rng.standard_normal((sum(new), hq, dim)).astype(f32)).to(TYPES[kind]).cuda()
+    starts = None if max(new) == 1 else starts_of(new)
+    for window in (0, 40):
+        check_attention(dev, ref, q, lens, table, starts, kind, window, max_new=max(new), max_len=max(lens))
