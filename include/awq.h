@@ -473,7 +473,8 @@ awq_status_t awq_w8a8_loss(const void* W, const void* X, awq_dtype_t dtype, int6
  *   x_strides[3] over B, S and H, out likewise of out_dtype; out may be x (with
  *   the same dtype and strides), otherwise they must not overlap.  positions
  *   int32, row (b, s) at b * position_stride + s (stride 0: shared), or NULL: s.
- *   A position outside [0, n_pos) turns its row to NaN.  rot <= D <= 65536.
+ *   A position outside [0, n_pos) turns its row to NaN.  rot <= D <= 65536,
+ *   H D <= 2^34.
  * ------------------------------------------------------------------------ */
 typedef enum {
   AWQ_ROPE_SCALING_NONE = 0,
@@ -518,8 +519,9 @@ awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, 
  * lens [B] int32 (device): tokens of a sequence, a call's new ones among them,
  * so row r of sequence b is its token lens[b] - (starts[b + 1] - r).
  * max_new, max_len (host): at least the largest number of rows and length of a
- * sequence; grids are sized by them.  Rows beyond max_new are not processed,
- * tokens beyond max_len not attended to.
+ * sequence; grids are sized by them.  Of a sequence with more rows the first
+ * max_new are processed, as the tokens that they are, and nothing is written for
+ * the others; tokens beyond max_len are not attended to.
  *
  * awq_kv_append: puts rows k and v [T, kv_heads, D] of dtype (strides over
  *   rows and heads: kv_strides[0..1] of k, [2..3] of v) into the cache.  With a
@@ -528,13 +530,13 @@ awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, 
  *   number.  For each block that gets tokens, in fp32 and in this order:
  *     step' = max(step, max |new| / 127), step = 0 if the page held no tokens
  *     older c' = clamp(rint(c * (step / step')), -127, 127) if step' != step
- *     new c = clamp(rint(x / step'), -127, 127), 0 where x / step' is NaN
+ *     new c = clamp(rint(x / step'), -127, 127), 0 where x / step' is NaN or step' is 0
  *   (rint: ties to even).  A NaN or an infinity makes the step that, and what
  *   the block holds reads as NaN: nothing plausible comes of it.  Tokens
- *   with a negative number are dropped.  Pages that get tokens must differ
- *   between sequences.  q (may be NULL, then Hq 0) [T, Hq, D] of dtype, Hq a
- *   multiple of kv_heads, strides q_strides[2]: turned alike into q_out [T, Hq,
- *   D] dense of q_out_dtype, by the same launch.
+ *   with a negative number are dropped, and their queries are not written.  Pages
+ *   that get tokens must differ between sequences.  q (may be NULL, then Hq 0)
+ *   [T, Hq, D] of dtype, Hq a multiple of kv_heads, strides q_strides[2]: turned
+ *   alike into q_out [T, Hq, D] dense of q_out_dtype, by the same launch.
  * awq_kv_read: tokens first[b] (device int32) and on, one for each row of the
  *   sequence, back as values: k_out and v_out [T, kv_heads, D] dense of out_dtype =
  *   fp32(c * step) rounded once.

@@ -32,7 +32,7 @@
 // tile (2.3 us a wave: values, scores, exponentials, values' product) where sequences are
 // short or uneven: 64 of 1 to 8192 tokens 33 + 5 us; one of 513 tokens, 32 heads 8.5 us.
 // attention_rows_kernel: many rows, bound by neither unit alone: 2 x 2047 rows of 64 heads
-// over 3000 and 4096 tokens 462 us, 733 TFLOP/s (a large fp16 matrix product reaches 1140 to
+// over 3000 and 4096 tokens 460 to 466 us, 727 to 736 TFLOP/s (a large fp16 matrix product reaches 1140 to
 // 1180 here); the matrix units are busy 29% and the vector units 50% of the time, 1.5 waves
 // a SIMD on average.
 #include <algorithm>
@@ -86,7 +86,8 @@ __device__ __forceinline__ int splits_of(int nt, int tiles_log) {
 // of all tiles, and finds its own split by counting: no workgroup but the last few is
 // empty.  (A grid of sequences x most splits costs about a microsecond for every 512
 // empty ones: registers let only two at a time onto a compute unit.)  64 sequences of
-// 1 to 8192 tokens, 8 heads: 29 us, against 33 with a fixed 20 tiles a split.
+// 1 to 8192 tokens, 8 heads: 32 to 35 us; it was 29, against 33 with a fixed 20 tiles a
+// split, before the keys were centred.
 struct Part {
   int tiles, b, split;    // b = -1: nothing is left for this workgroup
 };
@@ -814,7 +815,8 @@ Plan plan(int64_t B, int Hq, int Hkv, int D, int max_new, int max_len) {
   // would allow splits too finely, 21.6 against 19.0 us).
   p.slots = 256 * (wide <= (p.shared || p.QT == 2 ? 4 : 6) ? 2 : 1);
   // Few short sequences: eight waves a workgroup and no second launch.
-  // not for heads wider than 192, whose registers eight waves have no room for
+  // not for heads wider than 192, whose registers eight waves have no room for (513 tokens, 32
+  // heads of 256 columns: 24 us with eight, 15 with four; 8 x 1000 tokens, 8 heads: 34 and 19)
   if (p.QT == 1 && groups <= 256 && tiles <= 16 && D <= 192) p.NW = 8;
   p.chosen = B > 1 && B <= 64 * p.NW && !p.shared && p.NW == 4 && tiles > 8;
   if (p.chosen) {
