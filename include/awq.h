@@ -473,8 +473,7 @@ awq_status_t awq_w8a8_loss(const void* W, const void* X, awq_dtype_t dtype, int6
  *   x_strides[3] over B, S and H, out likewise of out_dtype; out may be x (with
  *   the same dtype and strides), otherwise they must not overlap.  positions
  *   int32, row (b, s) at b * position_stride + s (stride 0: shared), or NULL: s.
- *   A position outside [0, n_pos) turns its row to NaN.  rot <= D <= 65536,
- *   H D <= 2^34.
+ *   A position outside [0, n_pos) turns its row to NaN.  rot <= D <= 65536.
  * ------------------------------------------------------------------------ */
 typedef enum {
   AWQ_ROPE_SCALING_NONE = 0,

@@ -894,7 +894,6 @@ awq_status_t awq_rope(const void* x, awq_dtype_t x_dtype, int64_t B, int64_t S, 
   if (!aligned(x, esize(x_dtype)) || !aligned(out, esize(out_dtype)) || !aligned(table, 8) ||
       !aligned(positions, 4))
     return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned to its elements");
-  if (H * D > (1ll << 34)) return fail(AWQ_ERR_UNSUPPORTED, "more than 2^34 elements in a row");
   if (B * S > kMaxGrid * 256 / (H * D))
     return fail(AWQ_ERR_UNSUPPORTED, "more than %lld elements", (long long)(kMaxGrid * 256));
   awq::RopeArgs a = {};

@@ -83,8 +83,8 @@ __global__ __launch_bounds__(256) void rope_units_kernel(RopeArgs a, int rows_pe
   }
 }
 
-// Any rot: one pair, or one column that is left as it is, a thread (the pairs of a rot
-// that is no multiple of 8 do not fall into vectors).
+// Any rot and any row: one pair, or one column that is left as it is, a thread (the pairs
+// of a rot that is no multiple of 8 do not fall into vectors).
 template <class TI, class TO>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   typedef typename TI::storage SI;
@@ -128,12 +128,13 @@ void go_units(RopeArgs a, hipStream_t st) {
 template <class TI, class TO>
 hipError_t go(RopeArgs a, hipStream_t st) {
   ProfScope prof("awq_rope", st);
-  if (a.rot % 16 == 0 && a.D % 8 == 0) {
+  const bool rows = a.H * a.D <= 1ll << 34;    // a row's units are counted in 32 bits
+  if (rows && a.rot % 16 == 0 && a.D % 8 == 0) {
     // four heads a thread for 2M units and more (4M units 74.9 against 79.0 us); one for fewer,
     // which need the threads (1M units of fp32 17.6 against 19.1 us)
     if (a.B * a.S * a.H * units_of<8>(a.D, a.rot) >= 2 << 20) go_units<TI, TO, 8, 4>(a, st);
     else go_units<TI, TO, 8, 1>(a, st);
-  } else if (a.rot % 8 == 0 && a.D % 8 == 0) {
+  } else if (rows && a.rot % 8 == 0 && a.D % 8 == 0) {
     // 2 x 5066 rows x 64 heads x 80 columns of which 40 turn, bf16: 50 us (186 pair by pair)
     go_units<TI, TO, 4, 1>(a, st);
   } else {

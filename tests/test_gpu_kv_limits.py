@@ -302,6 +302,18 @@ def test_rope_of_more_items_than_a_launch_has_threads(dim, rot):
             assert torch.equal(p, x0.expand_as(p))
 
 
+def test_rope_of_a_row_of_more_units_than_32_bits_count():
+    """One row of 1.4e9 heads of three units."""
+    H = (1 << 32) // 3 + 100
+    x = torch.randn((1, 1, 24), device="cuda").bfloat16().expand(1, H, 24)
+    table = awq.awq_rope_table(2, 8)
+    out = torch.full((1, H, 24), 7.0, device="cuda", dtype=torch.bfloat16)
+    awq.awq_rope(x, table, ints([1]), out=out)
+    want = awq.awq_rope(x[:, :1], table, ints([1]))[0]
+    for p in out[0].split(1 << 24):
+        assert torch.equal(p, want.expand_as(p))
+
+
 # ---------------------------------------------------------------------------------------------
 # the rotation's gradient is recorded
 # ---------------------------------------------------------------------------------------------

@@ -12,11 +12,6 @@ from test_kv_abi import (INVALID, UNSUPPORTED, WORKSPACE, append_args, attention
                          status, strides, table_args)
 
 
-def test_rope_refuses_rows_past_its_items():
-    assert status("awq_rope", rope_args(B=1, S=1, H=1 << 20, D=65536, xs=strides(0, 0, 65536),
-                                        os=strides(0, 0, 65536))) == UNSUPPORTED
-
-
 def test_append_of_no_rows_takes_an_empty_q():
     """Torch's empty tensors have null pointers."""
     nothing = dict(T=0, k=None, v=None, q=None, q_out=None)
