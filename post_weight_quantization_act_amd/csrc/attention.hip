@@ -32,9 +32,9 @@
 // tile (2.3 us a wave: values, scores, exponentials, values' product) where sequences are
 // short or uneven: 64 of 1 to 8192 tokens 33 + 5 us; one of 513 tokens, 32 heads 8.5 us.
 // attention_rows_kernel: many rows, bound by neither unit alone: 2 x 2047 rows of 64 heads
-// over 3000 and 4096 tokens 460 to 466 us, 727 to 736 TFLOP/s (a large fp16 matrix product reaches 1140 to
-// 1180 here); the matrix units are busy 29% and the vector units 50% of the time, 1.5 waves
-// a SIMD on average.
+// over 3000 and 4096 tokens 460 to 466 us, 727 to 736 TFLOP/s (a large fp16 matrix product
+// reaches 1140 to 1180 here); the matrix units are busy 29% and the vector units 50% of the
+// time, 1.5 waves a SIMD on average.
 #include <algorithm>
 
 #include "kv.h"
