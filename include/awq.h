@@ -20,7 +20,10 @@
  * (awq_gptq_*) and SmoothQuant W8A8 (awq_smooth_scales,
  * awq_quantize_rows_int8, awq_w8a8_loss), and what stands between the low-bit
  * projections of an attention layer: rotary positions (awq_rope*) and a paged
- * key/value cache in 8 bits with the attention over it (awq_kv_*).
+ * key/value cache in 8 bits with the attention over it (awq_kv_*), and a block
+ * of experts: the router, tokens sorted by expert and back (awq_moe_*), and the
+ * packed product with an epilogue, of one projection or of each expert's
+ * (awq_lowbit_linear).
  *
  * Sources (web pages on the method):
  *   [P1] "Как работает quantization-aware scaling в AWQ для защиты важных
@@ -32,8 +35,9 @@
  *
  * Conventions shared by every entry point
  *   - Every tensor is a dense row-major buffer in device memory (but for the
- *     strided ones of awq_rope and awq_kv_*), allocated and owned by the caller; the library allocates no device memory.  Host
- *     buffers are named as such below.
+ *     strided ones of awq_rope, awq_kv_*, awq_moe_* and awq_lowbit_linear), allocated and
+ *     owned by the caller; the library allocates no device memory.  Host buffers are
+ *     named as such below.
  *   - Work is enqueued asynchronously on `stream` (NULL = the null stream);
  *     outputs are valid once the stream has been synchronised.  Calls that
  *     share a workspace must be ordered on one stream.
@@ -48,7 +52,7 @@
  *   - W and X share one dtype.  fp16/bf16 layers use the MFMA path (fp32
  *     accumulation); fp32 layers use an fp32 vector-ALU path.
  *   - Sizes: every operand buffer must be below 4 GiB (byte offsets are
- *     32-bit inside the kernels; not so in awq_rope and awq_kv_*); bits in [2, 8]; group a power of two in
+ *     32-bit inside the kernels; not so in awq_rope, awq_kv_* and awq_moe_*); bits in [2, 8]; group a power of two in
  *     [32, 512] dividing K.
  */
 #ifndef AWQ_MI355X_AWQ_H
@@ -590,6 +594,113 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
                               hipStream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * A block of experts.  Every one of T tokens goes to k of E experts; pair t k + j
+ * is token t's j-th choice.  Sorted by expert, an expert's pairs in their own
+ * order, the pairs make T k rows:
+ *   order [T k] int32: the pair of each sorted row;
+ *   place [T k] int32: the sorted row of each pair;
+ *   offsets [count + 1] int32: rows [offsets[e], offsets[e + 1]) are those of
+ *     expert first + e.  Pairs of any other expert (one that another GPU holds,
+ *     or a choice taken out by a number below 0) come last, past offsets[count]:
+ *     rows that nobody has, zero wherever rows are written, never read.
+ * All device memory.  T k < 2^31, k <= 32, count and E <= 1024.  Results are reproducible.
+ *
+ * awq_moe_route: from logits [T, E] of dtype (row stride in elements) the k experts
+ *   with the largest scores, in falling order, the lower number first of equals.
+ *   AWQ_SCORE_SOFTMAX: the score is the logit, AWQ_SCORE_SIGMOID: its sigmoid; bias
+ *   [E] fp32 (NULL: none) is added, in 64 bits, for the choice alone.  NaN ranks
+ *   last.  weights_out[t, j] fp32 = scale p_j, p the softmax over all E logits, or
+ *   the sigmoid; with AWQ_ROUTE_NORMALISE over their sum over the k chosen.  Where
+ *   that sum is 0 (a row of -inf) the weights are 0.  experts_out [T, k] int32.
+ *   Where offsets is not NULL the pairs are sorted as awq_moe_sort does.
+ * awq_moe_route_grad: dlogits [T, E] dense of dtype from dweights [T, k] and the
+ *   experts that the call chose; no gradient goes to the choice, or to the bias.
+ * awq_moe_sort: sorts n pairs by their experts [n].
+ *   workspace: awq_moe_sort_workspace_size(n, count) bytes, 4-byte aligned, may be
+ *   NULL when that is 0; for awq_moe_route too, n = T k.
+ * awq_moe_gather: out [T k, C] dense: row place[t, j] = weights[t, j] x[t], x [T, C] of
+ *   dtype (row stride in elements), weights fp32 [T, k] or NULL: 1.  Products are
+ *   rounded once.
+ * awq_moe_combine: out [T, C] dense of out_dtype = residual[t] + sum_j weights[t, j]
+ *   rows[place[t, j]], summed in fp32 in the order of j; rows [T k, C] dense of
+ *   dtype, residual [T, C] of out_dtype with a row stride, or NULL.  Each of the
+ *   two is the other's gradient with respect to x or rows.
+ * awq_moe_combine_grad: both gradients of awq_moe_combine for dy [T, C] of dy_dtype (row
+ *   stride in elements): drows [T k, C] of dtype as awq_moe_gather writes (may be NULL),
+ *   and dweights [T, k] fp32 = <dy[t], rows[place[t, j]]>, rows of dtype (may be NULL;
+ *   then rows may be).  With x for dy and the rows'
+ *   gradient for rows dweights is awq_moe_gather's.
+ * place and order outside [0, T k) are passed over; C < 2^31.
+ * ------------------------------------------------------------------------ */
+#define AWQ_SCORE_SOFTMAX 0
+#define AWQ_SCORE_SIGMOID 1
+#define AWQ_ROUTE_NORMALISE 1u
+size_t awq_moe_sort_workspace_size(int64_t n, int64_t count);
+awq_status_t awq_moe_sort(const int32_t* experts, int64_t n, int64_t first, int64_t count,
+                          int32_t* offsets, int32_t* order, int32_t* place, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+awq_status_t awq_moe_route(const void* logits, awq_dtype_t dtype, int64_t T, int64_t E,
+                           int64_t stride, int k, const float* bias, int score, uint32_t flags,
+                           double scale, int32_t* experts_out, float* weights_out, int64_t first,
+                           int64_t count, int32_t* offsets, int32_t* order, int32_t* place,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+awq_status_t awq_moe_route_grad(const void* logits, awq_dtype_t dtype, int64_t T, int64_t E,
+                                int64_t stride, int k, int score, uint32_t flags, double scale,
+                                const int32_t* experts, const float* dweights, void* dlogits,
+                                hipStream_t stream);
+awq_status_t awq_moe_gather(const void* x, awq_dtype_t dtype, int64_t T, int64_t C, int64_t stride,
+                            int k, int64_t count, const int32_t* offsets, const int32_t* place,
+                            const float* weights, void* out, hipStream_t stream);
+awq_status_t awq_moe_combine(const void* rows, awq_dtype_t dtype, int64_t T, int64_t C, int k,
+                             int64_t count, const int32_t* offsets, const int32_t* place,
+                             const float* weights, const void* residual, int64_t residual_stride,
+                             void* out, awq_dtype_t out_dtype, hipStream_t stream);
+awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t T, int64_t C,
+                                  int64_t stride, int k, int64_t count, const int32_t* offsets,
+                                  const int32_t* place, const float* weights, const void* rows,
+                                  awq_dtype_t dtype, void* drows, float* dweights,
+                                  hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * awq_lowbit_linear: the packed product with its epilogue,
+ *     v = x W'^T + bias,   y = act(v) + residual
+ *   or, with AWQ_LINEAR_GATED, of a weight whose first N / 2 rows are gates and
+ *   whose others are ups, y = act(v_gate) v_up + residual.  W' = (c - z) step in
+ *   awq_lowbit_repack's layout: one projection [N, K], or, with offsets, the rows
+ *   of `experts` projections one after another, repacked as one weight of
+ *   experts * N rows.
+ *   x [x_rows, K] of dtype (AWQ_F16 or AWQ_BF16; row stride in elements, a
+ *   multiple of 8; 16-byte aligned).  Without offsets row r of the outputs is row r of
+ *   x (x_rows = rows) and `experts` is 1.  With offsets [experts + 1] rows
+ *   [offsets[e], offsets[e + 1]) are expert e's, rows past the last are zero; they
+ *   take row r of x or, with order [rows] (awq_moe_sort's), row order[r] /
+ *   per_token of x: the tokens' rows, without sorted copies of them.
+ *   bias fp32 [experts, N] or NULL; residual [rows, outputs] of out_dtype with a row
+ *   stride, or NULL; out [rows, outputs] dense of out_dtype (any), outputs = N, or
+ *   N / 2 where gated.
+ *   Products x (c - z) are exact and summed in fp32; steps must be finite, those of
+ *   a row within a factor of 2^100 of each other.  The result is rounded once.
+ *   workspace: awq_lowbit_linear_workspace_size(...) bytes, 256-byte aligned, may be NULL
+ *   when that is 0.
+ * ------------------------------------------------------------------------ */
+#define AWQ_ACT_NONE 0
+#define AWQ_ACT_RELU 1
+#define AWQ_ACT_SILU 2
+#define AWQ_ACT_GELU 3        /* with erf */
+#define AWQ_ACT_GELU_TANH 4
+#define AWQ_LINEAR_GATED 1u
+size_t awq_lowbit_linear_workspace_size(awq_dtype_t dtype, int64_t rows, int64_t x_rows, int64_t N,
+                                        int64_t K, int64_t experts, uint32_t flags);
+awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows, int64_t K,
+                               int64_t stride, const uint32_t* codes_t, const void* meta_t,
+                               int64_t N, int64_t experts, int bits, int group, const float* bias,
+                               int act, uint32_t flags, const int32_t* offsets,
+                               const int32_t* order, int per_token, int64_t rows,
+                               const void* residual, int64_t residual_stride, void* out,
+                               awq_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Kernel timing.  While enabled, every kernel the library launches (or, after
  * awq_profile_select(prefix), every kernel whose name starts with prefix) is
  * bracketed by a pair of HIP events on its stream; each event pair adds a few
@@ -604,7 +715,9 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
  * awq_gptq_inverse, awq_gptq_columns, awq_gptq_pack.  SmoothQuant: awq_smooth_scales,
  * awq_quant_rows_int8, awq_gemm_w8a8_sse (the INT8 GEMM with the squared-error
  * epilogue), awq_gemm_w8a8_store (the INT8 GEMM writing y).  awq_rope_table, awq_rope,
- * awq_kv_append, awq_kv_read, awq_kv_attention, awq_kv_attention_join.
+ * awq_kv_append, awq_kv_read, awq_kv_attention, awq_kv_attention_join.  awq_moe_sort,
+ * awq_moe_route, awq_moe_route_grad, awq_moe_gather, awq_moe_combine, awq_moe_combine_grad,
+ * awq_lowbit_linear.
  * awq_profile_reset() drops the records.  Thread-safe.
  * ------------------------------------------------------------------------ */
 awq_status_t awq_profile_enable(int enable);

@@ -31,6 +31,8 @@ __all__ = [
     "AWQ_ROPE_INTERLEAVED", "AWQ_ROPE_TRANSPOSE", "AWQ_ATT_FULL", "KvCache",
     "awq_rope_table", "awq_rope", "awq_kv_append", "awq_kv_read",
     "awq_kv_attention_workspace_size", "awq_kv_attention_workspace_needed", "awq_kv_attention",
+    "Routing", "awq_moe_route", "awq_moe_sort", "awq_moe_sort_workspace_size", "awq_moe_gather",
+    "awq_moe_combine", "awq_moe_combine_grad", "awq_moe_route_grad", "awq_lowbit_linear", "awq_lowbit_linear_workspace_size",
     "awq_profile_enable", "awq_profile_select", "awq_profile_read", "awq_profile_reset",
     "packed_words_per_row",
 ]
@@ -46,6 +48,11 @@ AWQ_ROPE_INTERLEAVED = 1
 AWQ_ROPE_TRANSPOSE = 2
 AWQ_ATT_FULL = 1
 _ROPE_SCALING = {"none": 0, "linear": 1, "turns": 2, "log_turns": 3}
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+AWQ_ROUTE_NORMALISE = 1
+_ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+AWQ_LINEAR_GATED = 1
 
 _DTYPES = {torch.float32: AWQ_F32, torch.float16: AWQ_F16, torch.bfloat16: AWQ_BF16}
 _STATUS = {0: "AWQ_OK", -1: "AWQ_ERR_INVALID_ARG", -2: "AWQ_ERR_UNSUPPORTED",
@@ -149,6 +156,18 @@ _SIGS = {
     "awq_kv_attention_workspace_needed": ([_I64] * 7, _SZ),
     "awq_kv_attention": ([_P, _P, _I32, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _D,
                           _I64, _U32, _P, _P, _P, _SZ, _P], _I32),
+    "awq_moe_sort_workspace_size": ([_I64, _I64], _SZ),
+    "awq_moe_sort": ([_P, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P], _I32),
+    "awq_moe_route": ([_P, _I32, _I64, _I64, _I64, _I32, _P, _I32, _U32, _D, _P, _P, _I64, _I64, _P,
+                       _P, _P, _P, _SZ, _P], _I32),
+    "awq_moe_route_grad": ([_P, _I32, _I64, _I64, _I64, _I32, _I32, _U32, _D, _P, _P, _P, _P], _I32),
+    "awq_moe_gather": ([_P, _I32, _I64, _I64, _I64, _I32, _I64, _P, _P, _P, _P, _P], _I32),
+    "awq_moe_combine": ([_P, _I32, _I64, _I64, _I32, _I64, _P, _P, _P, _P, _I64, _P, _I32, _P], _I32),
+    "awq_moe_combine_grad": ([_P, _I32, _I64, _I64, _I64, _I32, _I64, _P, _P, _P, _P, _I32, _P, _P,
+                              _P], _I32),
+    "awq_lowbit_linear_workspace_size": ([_I32, _I64, _I64, _I64, _I64, _I64, _U32], _SZ),
+    "awq_lowbit_linear": ([_P, _I32, _I64, _I64, _I64, _P, _P, _I64, _I64, _I32, _I32, _P, _I32, _U32,
+                           _P, _P, _I32, _I64, _P, _I64, _P, _I32, _P, _SZ, _P], _I32),
     "awq_profile_enable": ([_I32], _I32),
     "awq_profile_select": ([ctypes.c_char_p], _I32),
     "awq_profile_read": ([ctypes.c_char_p, ctypes.POINTER(_I64), ctypes.POINTER(_D)], _I32),
@@ -812,6 +831,356 @@ def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages:
          D ** -0.5 if scale is None else scale, window, 0 if causal else AWQ_ATT_FULL, op,
          None if lse is None else lse.data_ptr(), ws, size)
     return (out, lse) if return_lse else out
+
+
+class Routing:
+    """Which tokens go to which experts: experts int32 [T, k] (their numbers), weights fp32 [T, k] or
+    None, and the pairs sorted by expert: offsets int32 [count + 1], order int32 [T k], place int32
+    [T, k].  Made by awq_moe_route or awq_moe_sort."""
+
+    __slots__ = ("experts", "weights", "offsets", "order", "place", "gpu", "tokens", "k", "count")
+
+    def __init__(self, experts, weights, offsets, order, place):
+        if not isinstance(place, _Tensor) or not place.is_cuda or place.dim() != 2:
+            _refuse(place, "place", -1, "int32 [T, k]")
+        gpu = place.get_device()
+        self.tokens, self.k = shape = place.shape
+        _ints(place, "place", gpu, shape)
+        _ints(order, "order", gpu, (self.tokens * self.k,))
+        if not isinstance(offsets, _Tensor) or offsets.dim() != 1 or not offsets.shape[0]:
+            _refuse(offsets, "offsets", gpu, "int32 [count + 1]")
+        _ints(offsets, "offsets", gpu, offsets.shape)
+        if experts is not None:
+            _ints(experts, "experts", gpu, shape)
+        if weights is not None:
+            _dense(weights, "weights", gpu, shape, torch.float32)
+        self.count = offsets.shape[0] - 1
+        self.experts, self.weights, self.offsets, self.order, self.place, self.gpu = \
+            experts, weights, offsets, order, place, gpu
+
+
+def awq_moe_sort_workspace_size(n: int, count: int) -> int:
+    return int(library().awq_moe_sort_workspace_size(n, count))
+
+
+def _lists(T: int, k: int, count: int, device):
+    """offsets, order, place and a workspace, with their pointers."""
+    n = T * k
+    offsets = torch.empty(max(count, 0) + 1, dtype=torch.int32, device=device)
+    order = torch.empty(n, dtype=torch.int32, device=device)
+    place = torch.empty((T, k), dtype=torch.int32, device=device)
+    size = (_LIB or library()).awq_moe_sort_workspace_size(n, count)
+    ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    return (offsets, order, place), (offsets.data_ptr(), order.data_ptr(), place.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), size), ws
+
+
+def awq_moe_sort(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
+                 weights: torch.Tensor | None = None) -> Routing:
+    """Sorts the pairs of experts int32 [T, k] by expert; those of experts outside [first_expert,
+    first_expert + num_experts) come last and count nowhere."""
+    if not isinstance(experts, _Tensor) or not experts.is_cuda or experts.dim() != 2:
+        _refuse(experts, "experts", -1, "int32 [T, k]")
+    gpu = experts.get_device()
+    T, k = shape = experts.shape
+    ep = _ints(experts, "experts", gpu, shape)
+    if weights is not None:
+        _dense(weights, "weights", gpu, shape, torch.float32)
+    lists, pointers, ws = _lists(T, k, num_experts, experts.device)
+    _run("awq_moe_sort", gpu, ep, T * k, first_expert, num_experts, *pointers)
+    return Routing(experts, weights, *lists)
+
+
+def _rows_of(x: torch.Tensor, name: str, gpu: int = -1) -> int:
+    """A matrix whose rows' columns lie together; its row stride."""
+    if not isinstance(x, _Tensor) or not x.is_cuda or (gpu >= 0 and x.get_device() != gpu) \
+            or x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1 and x.shape[0]):
+        _refuse(x, name, gpu, "a matrix with contiguous columns")
+    return x.stride(0)
+
+
+def awq_moe_route(logits: torch.Tensor, k: int, score: str = "softmax",
+                  bias: torch.Tensor | None = None, normalise: bool = True, scale: float = 1.0,
+                  num_experts: int | None = None, first_expert: int = 0) -> Routing:
+    """The k experts of every row of logits [T, E] with the largest scores, their weights, and the
+    pairs sorted by expert, for experts [first_expert, first_expert + num_experts) (None: all).
+    score "softmax" or "sigmoid"; bias fp32 [E] is added to the scores for the choice alone;
+    normalise: weights over their sum.  Where logits require a gradient that of the
+    weights is recorded."""
+    _rows_of(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    rest = k, score, normalise, scale
+    local = logits.shape[1] if num_experts is None else num_experts, first_expert
+    if logits.requires_grad and torch.is_grad_enabled():
+        return Routing(*_RouteGrad.apply(logits, bias, rest, local))
+    return Routing(*_route(logits, bias, rest, local))
+
+
+def _route(logits, bias, rest, local):
+    gpu, device = logits.get_device(), logits.device
+    T, E = logits.shape
+    k, score, normalise, scale = rest
+    if k < 0:
+        raise ValueError("k must be >= 1")
+    bp = None if bias is None else _dense(bias, "bias", gpu, (E,), torch.float32)
+    experts = torch.empty((T, k), dtype=torch.int32, device=device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    lists, pointers, ws = _lists(T, k, local[0], device)
+    _run("awq_moe_route", gpu, logits.data_ptr(), _dtype(logits), T, E, logits.stride(0), k, bp,
+         _SCORES[score], AWQ_ROUTE_NORMALISE if normalise else 0, scale, experts.data_ptr(), weights.data_ptr(), local[1], local[0], *pointers)
+    return experts, weights, *lists
+
+
+def awq_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor,
+                       score: str = "softmax", normalise: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """The gradient of awq_moe_route's weights with respect to the logits, [T, E] of their type,
+    from dweights fp32 [T, k] and the experts that it chose."""
+    stride = _rows_of(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    gpu, (T, E) = logits.get_device(), logits.shape
+    if not isinstance(experts, _Tensor) or experts.dim() != 2 or experts.shape[0] != T:
+        _refuse(experts, "experts", gpu, "int32 [T, k]")
+    shape = experts.shape
+    ep, gp = _ints(experts, "experts", gpu, shape), _dense(dweights, "dweights", gpu, shape, torch.float32)
+    d = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _run("awq_moe_route_grad", gpu, logits.data_ptr(), _dtype(logits), T, E, stride, shape[1],
+         _SCORES[score], AWQ_ROUTE_NORMALISE if normalise else 0, scale, ep, gp, d.data_ptr())
+    return d
+
+
+class _RouteGrad(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, rest, local):
+        out = _route(logits, bias, rest, local)
+        ctx.mark_non_differentiable(out[0], *out[2:])
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(logits, out[0])
+        ctx.rest = rest
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, g, *unused):
+        if g is None:
+            return None, None, None, None
+        logits, experts = ctx.saved_tensors
+        _, score, normalise, scale = ctx.rest
+        return awq_moe_route_grad(logits, experts, g.contiguous(), score, normalise, scale), None, None, None
+
+
+def _pair_weights(routing, weights, gpu):
+    return None if weights is None else _dense(weights, "weights", gpu, routing.place.shape, torch.float32)
+
+
+def _is_routing(routing) -> int:
+    if not isinstance(routing, Routing):
+        raise TypeError("routing must be a Routing (awq_moe_route, awq_moe_sort)")
+    return routing.gpu
+
+
+def awq_moe_gather(x: torch.Tensor, routing: Routing, weights: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """Tokens x [T, C] (any row stride) into the sorted rows [T k, C], times weights fp32 [T, k] if
+    given; rows of pairs that no expert here has are zero.  The gradients of x and weights are recorded
+    where they require one; into a given out they are not."""
+    gpu = _is_routing(routing)
+    xs = _rows_of(x, "x", gpu)
+    if out is None and torch.is_grad_enabled() and (
+            x.requires_grad or (weights is not None and weights.requires_grad)):
+        return _GatherGrad.apply(x, weights, routing)
+    wp = _pair_weights(routing, weights, gpu)
+    T, C = x.shape
+    if T != routing.tokens:
+        raise ValueError(f"x has {T} rows and the routing {routing.tokens} tokens")
+    shape = (T * routing.k, C)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", gpu, shape, x.dtype)
+    _run("awq_moe_gather", gpu, x.data_ptr(), _dtype(x), T, C, xs, routing.k, routing.count,
+         routing.offsets.data_ptr(), routing.place.data_ptr(), wp, op)
+    return out
+
+
+def awq_moe_combine(rows: torch.Tensor, routing: Routing, weights: torch.Tensor | None = None,
+                    residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Sorted rows [T k, C] back into tokens [T, C]: residual + the sum of each token's rows, times
+    weights fp32 [T, k] if given.  residual [T, C] of out_dtype (None: rows').  The gradients
+    of rows, weights and residual are recorded where they require one; into a given out they are not."""
+    gpu = _is_routing(routing)
+    if out is None and torch.is_grad_enabled() and (
+            rows.requires_grad or (weights is not None and weights.requires_grad)
+            or (residual is not None and residual.requires_grad)):
+        return _CombineGrad.apply(rows, weights, residual, routing, out_dtype)
+    T, k = routing.tokens, routing.k
+    if not isinstance(rows, _Tensor) or rows.dim() != 2:
+        _refuse(rows, "rows", gpu, "[T k, C]")
+    C = rows.shape[1]
+    rp = _dense(rows, "rows", gpu, (T * k, C), rows.dtype)
+    wp = _pair_weights(routing, weights, gpu)
+    if out is None:
+        out = torch.empty((T, C), dtype=out_dtype or rows.dtype, device=rows.device)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", gpu, (T, C), out_dtype or (out.dtype if isinstance(out, _Tensor) else rows.dtype))
+    ap, ast = None, 0
+    if residual is not None:
+        ast = _rows_of(residual, "residual", gpu)
+        if residual.shape != (T, C) or residual.dtype is not out.dtype:
+            _refuse(residual, "residual", gpu, f"{out.dtype} {[T, C]}")
+        ap = residual.data_ptr()
+    _run("awq_moe_combine", gpu, rp, _dtype(rows), T, C, k, routing.count, routing.offsets.data_ptr(),
+         routing.place.data_ptr(), wp, ap, ast, op, _dtype(out))
+    return out
+
+
+def awq_moe_combine_grad(dy: torch.Tensor, routing: Routing, weights: torch.Tensor | None = None,
+                         rows: torch.Tensor | None = None, dtype: torch.dtype | None = None,
+                         need_rows: bool = True, need_weights: bool = True):
+    """(drows, dweights) of awq_moe_combine for dy [T, C] (any row stride): drows [T k, C] of dtype
+    (None: rows' or dy's), dweights fp32 [T, k] from rows; None for what is not needed."""
+    gpu = _is_routing(routing)
+    stride = _rows_of(dy, "dy", gpu)
+    T, C = dy.shape
+    if T != routing.tokens:
+        raise ValueError(f"dy has {T} rows and the routing {routing.tokens} tokens")
+    shape = (T * routing.k, C)
+    wp = _pair_weights(routing, weights, gpu)
+    dtype = dtype or (dy.dtype if rows is None else rows.dtype)
+    if need_weights and rows is None:
+        raise ValueError("dweights without rows")
+    rp = _dense(rows, "rows", gpu, shape, dtype) if need_weights else None
+    drows = torch.empty(shape, dtype=dtype, device=dy.device) if need_rows else None
+    dw = torch.empty((T, routing.k), dtype=torch.float32, device=dy.device) if need_weights else None
+    _run("awq_moe_combine_grad", gpu, dy.data_ptr(), _dtype(dy), T, C, stride, routing.k, routing.count,
+         routing.offsets.data_ptr(), routing.place.data_ptr(), wp, rp, _DTYPES[dtype],
+         None if drows is None else drows.data_ptr(), None if dw is None else dw.data_ptr())
+    return drows, dw
+
+
+class _GatherGrad(torch.autograd.Function):
+    """Back from the sorted rows as awq_moe_combine does it."""
+
+    @staticmethod
+    def forward(ctx, x, weights, routing):
+        ctx.save_for_backward(x if weights is not None else None, weights)
+        ctx.routing = routing
+        return awq_moe_gather(x, routing, weights)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        x, weights = ctx.saved_tensors
+        g, dw = g.contiguous(), None
+        dx = awq_moe_combine(g, ctx.routing, weights) if ctx.needs_input_grad[0] else None
+        if ctx.needs_input_grad[1]:
+            dw = awq_moe_combine_grad(x, ctx.routing, None, g, need_rows=False)[1]
+        return dx, dw, None
+
+
+class _CombineGrad(torch.autograd.Function):
+    """Back into the sorted rows as awq_moe_gather does it."""
+
+    @staticmethod
+    def forward(ctx, rows, weights, residual, routing, out_dtype):
+        ctx.save_for_backward(rows if weights is not None else None, weights)
+        ctx.routing, ctx.dtype = routing, rows.dtype
+        return awq_moe_combine(rows, routing, weights, residual, out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        rows, weights = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        drows = dw = None
+        if need[0] or need[1]:
+            dy = g if g.stride(1) == 1 or g.shape[1] == 1 else g.contiguous()
+            drows, dw = awq_moe_combine_grad(dy, ctx.routing, weights, rows, ctx.dtype, need[0], need[1])
+        return drows, dw, g if need[2] else None, None, None
+
+
+def awq_lowbit_linear_workspace_size(dtype: torch.dtype, rows: int, x_rows: int, N: int, K: int,
+                                     experts: int = 1, gated: bool = False) -> int:
+    return int(library().awq_lowbit_linear_workspace_size(_DTYPES[dtype], rows, x_rows, N, K, experts,
+                                                          AWQ_LINEAR_GATED if gated else 0))
+
+
+def awq_lowbit_linear(x: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tensor, bits: int, group: int,
+                      bias: torch.Tensor | None = None, activation: str | None = None,
+                      gated: bool = False, residual: torch.Tensor | None = None,
+                      routing: Routing | None = None, gather: bool = False,
+                      out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """act(x W'^T + bias) + residual on packed weights (awq_lowbit_repack); gated: the first half of
+    the weight's rows are gates, the others ups, and the result is act(gate) up + residual.
+    x [M, K] fp16 or bf16 (row stride a multiple of 8).  With a routing the weight holds the rows of
+    all its experts one after another, bias is [experts, N], and each expert multiplies its
+    sorted rows: rows of x, or, gather, the tokens' that they come from.  activation "none", "relu",
+    "silu", "gelu" or "gelu_tanh".  -> [rows, N or N/2] of out_dtype (None: x's).  Packed weights
+    take no gradient and the call records none: it refuses inputs that require one."""
+    xs = _rows_of(x, "x")
+    gpu = x.get_device()
+    if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
+        raise RuntimeError("awq_lowbit_linear records no gradient: call it under torch.no_grad()")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {[a for a in _ACTIVATIONS if a]}")
+    M, K = x.shape
+    experts, rows, offsets, order, per_token = 1, M, None, None, 1
+    if routing is not None:
+        if _is_routing(routing) != gpu:
+            raise ValueError(f"the routing is on cuda:{routing.gpu}, x on cuda:{gpu}")
+        experts, rows = routing.count, routing.tokens * routing.k
+        offsets = routing.offsets.data_ptr()
+        if M != (routing.tokens if gather else rows):
+            raise ValueError(f"x has {M} rows, the routing {routing.tokens} tokens and {rows} sorted rows")
+        if gather:
+            order, per_token = routing.order.data_ptr(), routing.k
+    elif gather:
+        raise ValueError("gather without a routing")
+    if not isinstance(codes_t, _Tensor) or codes_t.dim() != 3:
+        _refuse(codes_t, "codes_t", gpu, "[K/32, experts N, bits] of 32-bit words")
+    R = codes_t.shape[1]
+    if R % experts:
+        raise ValueError(f"{R} rows of weights for {experts} experts")
+    N = R // experts
+    cp = _dense(codes_t, "codes_t", gpu, (K // 32, R, bits), codes_t.dtype)
+    if codes_t.element_size() != 4:
+        _refuse(codes_t, "codes_t", gpu, "[K/32, experts N, bits] of 32-bit words")
+    mp = _dense(meta_t, "meta_t", gpu, (K // group if group > 0 else 0, R, 2), torch.float32)
+    bp = None
+    if bias is not None:
+        bp = _dense(bias, "bias", gpu, bias.shape, torch.float32)
+        if bias.numel() != R or bias.shape[-1] != N:
+            _refuse(bias, "bias", gpu, f"fp32 {[experts, N]}")
+    outs = N // 2 if gated else N
+    if out is None:
+        out = torch.empty((rows, outs), dtype=out_dtype or x.dtype, device=x.device)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", gpu, (rows, outs), out_dtype or (out.dtype if isinstance(out, _Tensor) else x.dtype))
+    rp, rs = None, 0
+    if residual is not None:
+        rs = _rows_of(residual, "residual", gpu)
+        if residual.shape != (rows, outs) or residual.dtype is not out.dtype:
+            _refuse(residual, "residual", gpu, f"{out.dtype} {[rows, outs]}")
+        rp = residual.data_ptr()
+    flags = AWQ_LINEAR_GATED if gated else 0
+    if workspace is not None:
+        ws = _dense(workspace, "workspace", gpu, workspace.shape, workspace.dtype)
+        size = workspace.nbytes
+    else:
+        ws, size = None, (_LIB or library()).awq_lowbit_linear_workspace_size(_dtype(x), rows, M, N, K, experts, flags)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+            ws = workspace.data_ptr()
+    _run("awq_lowbit_linear", gpu, x.data_ptr(), _dtype(x), M, K, xs, cp, mp, N, experts, bits, group, bp,
+         _ACTIVATIONS[activation], flags, offsets, order, per_token, rows, rp, rs, op, _dtype(out), ws, size)
+    return out
 
 
 def awq_profile_enable(enable: bool = True) -> None:

@@ -40,7 +40,14 @@ PER_FILE = {
                  "-fno-gpu-flush-denormals-to-zero"],
 }
 SOURCES = ["act_stats.hip", "quant.hip", "gemm_sse.hip", "lowbit.hip", "gptq.hip", "w8a8.hip",
-           "rope.hip", "kvcache.hip", "attention.hip", "awq_api.cpp"]
+           "rope.hip", "kvcache.hip", "attention.hip", "moe.hip", "linear_plan.hip", "awq_api.cpp"]
+# Compiled once for each width of codes.
+EACH_WIDTH = ["linear.hip"]
+UNITS = [(src, None) for src in SOURCES] + [(src, bits) for src in EACH_WIDTH for bits in range(2, 9)]
+
+
+def obj_path(src: str, bits: int | None = None) -> Path:
+    return OBJ / (src + ("" if bits is None else f".{bits}") + ".o")
 
 
 def hipcc() -> str:
@@ -50,10 +57,12 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found; the AWQ library needs ROCm's hipcc to build")
 
 
-def _compile(src: str) -> Path:
-    obj = OBJ / (src + ".o")
+def _compile(unit: tuple) -> Path:
+    src, bits = unit
+    obj = obj_path(src, bits)
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
-    cmd = [hipcc(), *COMMON, *PER_FILE.get(src, []), *lang, "-c", str(CSRC / src), "-o", str(obj)]
+    width = [] if bits is None else [f"-DAWQ_LINEAR_BITS={bits}"]
+    cmd = [hipcc(), *COMMON, *PER_FILE.get(src, []), *width, *lang, "-c", str(CSRC / src), "-o", str(obj)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
@@ -63,7 +72,7 @@ def _compile(src: str) -> Path:
 def build(verbose: bool = False) -> Path:
     OBJ.mkdir(exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
+        objs = list(ex.map(_compile, UNITS))
     tmp = OUT.with_suffix(".so.tmp")
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *map(str, objs), "-o", str(tmp)]
     r = subprocess.run(cmd, capture_output=True, text=True)

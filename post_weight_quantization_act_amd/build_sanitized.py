@@ -32,7 +32,7 @@ def runtime() -> str:
 
 
 def build_sanitized(verbose: bool = False) -> Path:
-    objs = [_build.OBJ / (src + ".o") for src in _build.SOURCES if src != "awq_api.cpp"]
+    objs = [_build.obj_path(*unit) for unit in _build.UNITS if unit[0] != "awq_api.cpp"]
     if not all(o.exists() for o in objs):
         _build.build(verbose=verbose)
     OUT.parent.mkdir(parents=True, exist_ok=True)

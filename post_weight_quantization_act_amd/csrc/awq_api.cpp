@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "kv.h"
+#include "moe.h"
 
 namespace {
 
@@ -217,6 +218,81 @@ awq_status_t kv_args(const awq_kv_cache_t* cache, int64_t T, const int32_t* star
   a->P = cache->page;
   a->p_shift = 0;
   while ((1 << a->p_shift) < a->P) ++a->p_shift;
+  return AWQ_OK;
+}
+
+// Checks shared by the entry points around a block of experts.
+awq_status_t moe_sizes(int64_t T, int64_t k, int64_t count) {
+  if (T < 0) return fail(AWQ_ERR_INVALID_ARG, "negative number of tokens %lld", (long long)T);
+  if (k < 1 || count < 1)
+    return fail(AWQ_ERR_INVALID_ARG, "k=%lld and count=%lld must be >= 1", (long long)k, (long long)count);
+  if (k > awq::kMostChosen || count > awq::kMostExperts)
+    return fail(AWQ_ERR_UNSUPPORTED, "k=%lld above %d or count=%lld above %d", (long long)k,
+                awq::kMostChosen, (long long)count, awq::kMostExperts);
+  if (T > INT32_MAX / k)
+    return fail(AWQ_ERR_UNSUPPORTED, "T k = %lld x %lld must fit 31 bits", (long long)T, (long long)k);
+  return AWQ_OK;
+}
+
+awq_status_t moe_lists(int64_t n, int64_t first, int64_t count, int32_t* offsets, int32_t* order,
+                       int32_t* place, void* workspace, size_t workspace_bytes, awq::SortArgs* s) {
+  if (first < INT32_MIN || first > INT32_MAX)
+    return fail(AWQ_ERR_INVALID_ARG, "first=%lld is no expert's number", (long long)first);
+  if (!offsets || (n > 0 && (!order || !place))) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(offsets, 4) || !aligned(order, 4) || !aligned(place, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "offsets, order and place must be 4-byte aligned");
+  const size_t need = awq::moe_sort_ws_bytes(n, (int)count);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(AWQ_ERR_WORKSPACE, "sorting needs %zu workspace bytes, got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (need > 0 && !aligned(workspace, 4))
+    return fail(AWQ_ERR_WORKSPACE, "workspace must be 4-byte aligned");
+  s->offsets = offsets;
+  s->order = order;
+  s->place = place;
+  s->hist = (int32_t*)workspace;
+  s->n = n;
+  s->first = (int)first;
+  s->count = (int)count;
+  return AWQ_OK;
+}
+
+awq_status_t moe_scores(awq_dtype_t dtype, int64_t T, int64_t E, int64_t stride, int k, int score,
+                        uint32_t flags, double scale) {
+  if (!valid_dtype(dtype)) return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  awq_status_t st = moe_sizes(T, k, E);
+  if (st != AWQ_OK) return st;
+  if (k > E) return fail(AWQ_ERR_INVALID_ARG, "k=%d of E=%lld experts", k, (long long)E);
+  if (stride < 0) return fail(AWQ_ERR_INVALID_ARG, "negative row stride");
+  if (score != AWQ_SCORE_SOFTMAX && score != AWQ_SCORE_SIGMOID)
+    return fail(AWQ_ERR_INVALID_ARG, "unknown score %d", score);
+  if (flags & ~AWQ_ROUTE_NORMALISE) return fail(AWQ_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (!std::isfinite(scale) || !std::isfinite((float)scale))
+    return fail(AWQ_ERR_INVALID_ARG, "scale must be finite");
+  return AWQ_OK;
+}
+
+// Tokens [T][C] against sorted rows.
+awq_status_t moe_rows(awq_dtype_t dtype, int64_t T, int64_t C, int64_t stride, int k, int64_t count,
+                      const int32_t* offsets, const int32_t* place, const float* weights,
+                      awq::RowsArgs* a) {
+  if (!valid_dtype(dtype)) return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  awq_status_t st = moe_sizes(T, k, count);
+  if (st != AWQ_OK) return st;
+  if (C < 1) return fail(AWQ_ERR_INVALID_ARG, "C=%lld must be >= 1", (long long)C);
+  if (C > INT32_MAX - 64) return fail(AWQ_ERR_UNSUPPORTED, "C=%lld must fit 31 bits", (long long)C);
+  if (stride < 0) return fail(AWQ_ERR_INVALID_ARG, "negative row stride");
+  if (T > 0 && (!offsets || !place)) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(offsets, 4) || !aligned(place, 4) || !aligned(weights, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "offsets, place and weights must be 4-byte aligned");
+  a->weights = weights;
+  a->offsets = offsets;
+  a->place = place;
+  a->T = T;
+  a->C = C;
+  a->stride = stride;
+  a->k = k;
+  a->count = (int)count;
   return AWQ_OK;
 }
 
@@ -1067,6 +1143,268 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
   a.max_len = (int)reach;
   hipError_t e = awq::launch_kv_attention(a, dtype, workspace, stream);
   if (e != hipSuccess) return hip_fail(e, "kv_attention launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+// ---------------------------------------------------------------------------
+// A block of experts.
+// ---------------------------------------------------------------------------
+size_t awq_moe_sort_workspace_size(int64_t n, int64_t count) {
+  if (n < 0 || n > INT32_MAX || count < 1 || count > awq::kMostExperts) return 0;
+  return awq::moe_sort_ws_bytes(n, (int)count);
+}
+
+awq_status_t awq_moe_sort(const int32_t* experts, int64_t n, int64_t first, int64_t count,
+                          int32_t* offsets, int32_t* order, int32_t* place, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq_status_t st = moe_sizes(n, 1, count);
+  if (st != AWQ_OK) return st;
+  if (n > 0 && !experts) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(experts, 4)) return fail(AWQ_ERR_UNSUPPORTED, "experts must be 4-byte aligned");
+  awq::SortArgs a = {};
+  st = moe_lists(n, first, count, offsets, order, place, workspace, workspace_bytes, &a);
+  if (st != AWQ_OK) return st;
+  a.experts = experts;
+  hipError_t e = awq::launch_moe_sort(a, stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_sort launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_moe_route(const void* logits, awq_dtype_t dtype, int64_t T, int64_t E,
+                           int64_t stride, int k, const float* bias, int score, uint32_t flags,
+                           double scale, int32_t* experts_out, float* weights_out, int64_t first,
+                           int64_t count, int32_t* offsets, int32_t* order, int32_t* place,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq_status_t st = moe_scores(dtype, T, E, stride, k, score, flags, scale);
+  if (st != AWQ_OK) return st;
+  if (T > 0 && (!logits || !experts_out || !weights_out))
+    return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(logits, esize(dtype)) || !aligned(bias, 4) || !aligned(experts_out, 4) ||
+      !aligned(weights_out, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned to its elements");
+  awq::RouteArgs a = {};
+  if (offsets) {
+    st = moe_sizes(T, k, count);
+    if (st != AWQ_OK) return st;
+    st = moe_lists(T * k, first, count, offsets, order, place, workspace, workspace_bytes, &a.s);
+    if (st != AWQ_OK) return st;
+  } else if (T == 0) {
+    return AWQ_OK;
+  }
+  a.logits = logits;
+  a.bias = bias;
+  a.experts = experts_out;
+  a.weights = weights_out;
+  a.T = T;
+  a.stride = stride;
+  a.scale = (float)scale;
+  a.E = (int)E;
+  a.k = k;
+  a.sigmoid = score == AWQ_SCORE_SIGMOID;
+  a.normalise = (flags & AWQ_ROUTE_NORMALISE) != 0;
+  hipError_t e = awq::launch_moe_route(a, dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_route launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_moe_route_grad(const void* logits, awq_dtype_t dtype, int64_t T, int64_t E,
+                                int64_t stride, int k, int score, uint32_t flags, double scale,
+                                const int32_t* experts, const float* dweights, void* dlogits,
+                                hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq_status_t st = moe_scores(dtype, T, E, stride, k, score, flags, scale);
+  if (st != AWQ_OK) return st;
+  if (T == 0) return AWQ_OK;
+  if (!logits || !experts || !dweights || !dlogits) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(logits, esize(dtype)) || !aligned(experts, 4) || !aligned(dweights, 4) ||
+      !aligned(dlogits, esize(dtype)))
+    return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned to its elements");
+  awq::RouteGradArgs a = {};
+  a.logits = logits;
+  a.experts = experts;
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  a.T = T;
+  a.stride = stride;
+  a.scale = (float)scale;
+  a.E = (int)E;
+  a.k = k;
+  a.sigmoid = score == AWQ_SCORE_SIGMOID;
+  a.normalise = (flags & AWQ_ROUTE_NORMALISE) != 0;
+  hipError_t e = awq::launch_moe_route_grad(a, dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_route_grad launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_moe_gather(const void* x, awq_dtype_t dtype, int64_t T, int64_t C, int64_t stride,
+                            int k, int64_t count, const int32_t* offsets, const int32_t* place,
+                            const float* weights, void* out, hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq::RowsArgs a = {};
+  awq_status_t st = moe_rows(dtype, T, C, stride, k, count, offsets, place, weights, &a);
+  if (st != AWQ_OK) return st;
+  if (T == 0) return AWQ_OK;
+  if (!x || !out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, esize(dtype)) || !aligned(out, esize(dtype)))
+    return fail(AWQ_ERR_UNSUPPORTED, "x and out must be aligned to their elements");
+  a.tokens = x;
+  a.out = out;
+  hipError_t e = awq::launch_moe_gather(a, dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_gather launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_moe_combine(const void* rows, awq_dtype_t dtype, int64_t T, int64_t C, int k,
+                             int64_t count, const int32_t* offsets, const int32_t* place,
+                             const float* weights, const void* residual, int64_t residual_stride,
+                             void* out, awq_dtype_t out_dtype, hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq::RowsArgs a = {};
+  awq_status_t st = moe_rows(dtype, T, C, residual ? residual_stride : 0, k, count, offsets, place, weights, &a);
+  if (st != AWQ_OK) return st;
+  if (!valid_dtype(out_dtype)) return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d", (int)out_dtype);
+  if (T == 0) return AWQ_OK;
+  if (!rows || !out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(rows, esize(dtype)) || !aligned(out, esize(out_dtype)) ||
+      !aligned(residual, esize(out_dtype)))
+    return fail(AWQ_ERR_UNSUPPORTED, "rows, residual and out must be aligned to their elements");
+  a.rows = rows;
+  a.tokens = residual;
+  a.out = out;
+  hipError_t e = awq::launch_moe_combine(a, dtype, out_dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_combine launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t T, int64_t C,
+                                  int64_t stride, int k, int64_t count, const int32_t* offsets,
+                                  const int32_t* place, const float* weights, const void* rows,
+                                  awq_dtype_t dtype, void* drows, float* dweights,
+                                  hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  awq::RowsArgs a = {};
+  awq_status_t st = moe_rows(dtype, T, C, stride, k, count, offsets, place, weights, &a);
+  if (st != AWQ_OK) return st;
+  if (!valid_dtype(dy_dtype)) return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dy_dtype);
+  if (T == 0 || (!drows && !dweights)) return AWQ_OK;
+  if (!dy || (dweights && !rows)) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(dy, esize(dy_dtype)) || !aligned(rows, esize(dtype)) || !aligned(drows, esize(dtype)) ||
+      !aligned(dweights, 4))
+    return fail(AWQ_ERR_UNSUPPORTED, "a pointer is not aligned to its elements");
+  a.tokens = dy;
+  a.rows = rows;
+  a.out = drows;
+  a.dots = dweights;
+  hipError_t e = awq::launch_moe_combine_grad(a, dy_dtype, dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_combine_grad launch");
+  return AWQ_OK;
+  AWQ_GUARD_END
+}
+
+size_t awq_lowbit_linear_workspace_size(awq_dtype_t dtype, int64_t rows, int64_t x_rows, int64_t N,
+                                        int64_t K, int64_t experts, uint32_t flags) {
+  if (!valid_dtype(dtype) || rows < 1 || x_rows < 1 || N < 1 || K < 32 || experts < 1 ||
+      rows > INT32_MAX || x_rows > INT32_MAX || N > INT32_MAX || experts > awq::kMostExperts)
+    return 0;
+  awq::LinearArgs a = {};
+  a.rows = rows;
+  a.x_rows = x_rows;
+  a.N = (int)N;
+  a.K = K;
+  a.experts = (int)experts;
+  a.gated = (flags & AWQ_LINEAR_GATED) != 0;
+  return align_up(awq::linear_ws_bytes(a, dtype));
+}
+
+awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows, int64_t K,
+                               int64_t stride, const uint32_t* codes_t, const void* meta_t,
+                               int64_t N, int64_t experts, int bits, int group, const float* bias,
+                               int act, uint32_t flags, const int32_t* offsets,
+                               const int32_t* order, int per_token, int64_t rows,
+                               const void* residual, int64_t residual_stride, void* out,
+                               awq_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream) {
+  AWQ_GUARD_BEGIN
+  if (!valid_dtype(dtype) || !valid_dtype(out_dtype))
+    return fail(AWQ_ERR_INVALID_ARG, "unknown dtype %d or %d", (int)dtype, (int)out_dtype);
+  if (dtype == AWQ_F32) return fail(AWQ_ERR_UNSUPPORTED, "lowbit linear takes fp16 or bf16 activations");
+  if (N < 1 || K < 1 || experts < 1 || x_rows < 0 || rows < 0)
+    return fail(AWQ_ERR_INVALID_ARG, "N=%lld, K=%lld, experts=%lld must be >= 1, rows not negative",
+                (long long)N, (long long)K, (long long)experts);
+  if (bits < 2 || bits > 8) return fail(AWQ_ERR_UNSUPPORTED, "bits=%d outside [2, 8]", bits);
+  if (group < 32 || group > 512 || (group & (group - 1)) != 0)
+    return fail(AWQ_ERR_UNSUPPORTED, "group=%d must be a power of two in [32, 512]", group);
+  if (K % group != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "K=%lld is not a multiple of group=%d", (long long)K, group);
+  if (act < AWQ_ACT_NONE || act > AWQ_ACT_GELU_TANH)
+    return fail(AWQ_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (flags & ~AWQ_LINEAR_GATED) return fail(AWQ_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  const bool gated = (flags & AWQ_LINEAR_GATED) != 0;
+  if (gated && N % 2 != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "N=%lld gates and ups are not as many of each", (long long)N);
+  if (stride < 0 || stride % 8 != 0)
+    return fail(AWQ_ERR_UNSUPPORTED, "x's row stride %lld must be a multiple of 8", (long long)stride);
+  if (residual && residual_stride < 0) return fail(AWQ_ERR_INVALID_ARG, "negative row stride");
+  if (!offsets && (experts != 1 || order || x_rows != rows))
+    return fail(AWQ_ERR_INVALID_ARG, "without offsets there is one expert, no order, and x has the rows");
+  if (order && per_token < 1) return fail(AWQ_ERR_INVALID_ARG, "per_token=%d must be >= 1", per_token);
+  if (offsets && !order && x_rows != rows)
+    return fail(AWQ_ERR_INVALID_ARG, "without order x has the sorted rows");
+  if (experts > awq::kMostExperts || N > INT32_MAX / experts || rows > INT32_MAX / 2 ||
+      x_rows > INT32_MAX || K > INT32_MAX / 2)
+    return fail(AWQ_ERR_UNSUPPORTED, "experts=%lld above %d, or experts N, rows or K too large",
+                (long long)experts, awq::kMostExperts);
+  if (rows == 0) return AWQ_OK;
+  if (x_rows < 1) return fail(AWQ_ERR_INVALID_ARG, "rows of an empty x");
+  if (x_rows > 1 && stride > (int64_t)(kMaxBufferBytes / 2) / (x_rows - 1))
+    return fail(AWQ_ERR_UNSUPPORTED, "x exceeds the 4 GiB operand limit");
+  if ((uint64_t)((x_rows - 1) * stride + K) * 2 > kMaxBufferBytes)
+    return fail(AWQ_ERR_UNSUPPORTED, "x exceeds the 4 GiB operand limit");
+  if (!x || !codes_t || !meta_t || !out) return fail(AWQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, 16) || !aligned(codes_t, 4) || !aligned(meta_t, 8) || !aligned(bias, 4) ||
+      !aligned(offsets, 4) || !aligned(order, 4) || !aligned(out, esize(out_dtype)) ||
+      !aligned(residual, esize(out_dtype)))
+    return fail(AWQ_ERR_UNSUPPORTED, "x 16-byte, meta_t 8-byte aligned, the others to their elements");
+  awq::LinearArgs a = {};
+  a.x = x;
+  a.codes = codes_t;
+  a.meta = (const float2*)meta_t;
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.offsets = offsets;
+  a.order = order;
+  a.K = K;
+  a.stride = stride;
+  a.residual_stride = residual_stride;
+  a.x_rows = x_rows;
+  a.R = experts * N;
+  a.rows = rows;
+  a.N = (int)N;
+  a.experts = (int)experts;
+  a.per_token = per_token;
+  while ((32 << a.lg_cpg) < group) ++a.lg_cpg;
+  a.act = act;
+  a.gated = gated;
+  a.out_type = (int)out_dtype;
+  if (awq::linear_threads(a) > (int64_t)UINT32_MAX)
+    return fail(AWQ_ERR_UNSUPPORTED, "too many rows and columns for one call");
+  const size_t need = awq_lowbit_linear_workspace_size(dtype, rows, x_rows, N, K, experts, flags);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(AWQ_ERR_WORKSPACE, "lowbit_linear needs %zu workspace bytes, got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (need > 0 && !aligned(workspace, 256))
+    return fail(AWQ_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  hipError_t e = awq::launch_linear(a, dtype, bits, workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "lowbit_linear launch");
   return AWQ_OK;
   AWQ_GUARD_END
 }

@@ -30,7 +30,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "common.h"
+#include "lowbit.h"
 
 namespace awq {
 namespace {
@@ -90,9 +90,6 @@ __global__ __launch_bounds__(256) void repack_meta_kernel(const float* __restric
 // fp32 accumulation).  The group sum is scaled by delta once per group:
 //   y = sum_g delta_g * sum_{k in g} x_k (c_k - z_g).
 // Code pairs are (c_2t, c_2t+1), matching the activation pair in dword t.
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef __bf16 bf162v __attribute__((ext_vector_type(2)));
-
 template <int BITS>
 __device__ __forceinline__ uint32_t code_at(const uint32_t (&w)[BITS], int i) {
   const int p = BITS * i;                    // compile-time after unrolling
@@ -131,35 +128,6 @@ struct MagicWindows {
     return (w_end < 32 ? w_end : 32) * BITS - 1;
   }
 };
-
-// The AND-OR of the unpacking as one v_and_or_b32, mask in an SGPR and
-// exponent in a VGPR.  Written out because the compiler splits (w & mask) |
-// expo into a v_and_b32 and a v_or_b32 with literal operands, which measured
-// slower (the 70B decode call took 36.5 us that way, 30.3 us with the single
-// instruction).
-// The constants come from magic_ops(), built once per kernel.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t smask, uint32_t vexpo) {
-  uint32_t r;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(smask), "v"(vexpo));
-  return r;
-}
-
-// Masks (SGPRs) and exponents (VGPRs) of the window offsets sh = BITS t.
-template <int BITS, int N>
-struct MagicOps {
-  uint32_t mask[N];
-  uint32_t expo[N];
-};
-template <int BITS, int N>
-__device__ __forceinline__ MagicOps<BITS, N> magic_ops() {
-  MagicOps<BITS, N> o;
-#pragma unroll
-  for (int t = 0; t < N; ++t) {
-    asm("s_mov_b32 %0, %1" : "=s"(o.mask[t]) : "i"(((1u << BITS) - 1u) << (BITS * t)));
-    asm("v_mov_b32 %0, %1" : "=v"(o.expo[t]) : "i"((uint32_t)(150 - BITS * t) << 23));
-  }
-  return o;
-}
 
 template <int BITS>
 __device__ __forceinline__ uint32_t magic_window(const uint32_t (&w)[BITS], int i) {
@@ -459,8 +427,6 @@ hipError_t gemv_bits(int bits, const void* X, int64_t M, int64_t K, const uint32
 // Rows of 64 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3) (no
 // bank conflicts for the fragment reads).  The LDS traffic of a stage (about
 // 100 KB: fragment reads, transfers, unpacking) is what bounds this kernel.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 constexpr int kGM = 256;                         // activation rows per tile
 constexpr int kGN = 128;                         // output rows per tile
 constexpr int kGWaves = 8;
@@ -473,36 +439,6 @@ constexpr int kBSlot = kGN * 64;                 // 8 KB
 constexpr int kPerStage = 3;                     // transfers per stage of a wave with a third one
 
 __device__ __forceinline__ int g_off(int r, int c) { return r * 64 + 16 * (c ^ ((r >> 1) & 3)); }
-
-// Buffer resource of a raw byte range: loads at offsets >= num_bytes return 0.
-__device__ __forceinline__ i32x4 byte_range(const void* base, uint32_t num_bytes) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), (int)num_bytes, 0x00020000};
-}
-
-// 16 bytes per lane from rsrc + voff into LDS at lds_addr + 16 * lane.  Inline
-// asm, so that the compiler does not wait for every transfer before each LDS
-// read; the kernel waits with explicit counts.  m0 is declared clobbered (the
-// compiler keeps nothing of its own in it across the transfer and pads its own
-// next use), and the SALU write of m0 gets the one wait state an LDS-DMA load
-// needs before it reads m0.  clang warns about any reserved register in a
-// clobber list; the clobber is honoured all the same.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void to_lds16(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(lds_addr), "v"(voff), "s"(rsrc)
-               : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// Wait until at most n transfers of this lane are outstanding.
-template <int n>
-__device__ __forceinline__ void vm_wait() {
-  static_assert(n >= 0 && n < 64, "vmcnt is 6 bits");
-  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
-}
 
 // Wait until at most the transfers of the last n stages this wave issued are
 // in flight (three per stage for a wave with a third transfer, else two).
@@ -534,31 +470,11 @@ struct GemmLds {
   static_assert(kBytes <= 160 * 1024, "LDS of one CU");
 };
 
-template <typename S>
-__device__ __forceinline__ f32x16 mfma32(i32x4 a, i32x4 b, f32x16 c);
-template <>
-__device__ __forceinline__ f32x16 mfma32<_Float16>(i32x4 a, i32x4 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a),
-                                                __builtin_bit_cast(half8, b), c, 0, 0, 0);
-}
-template <>
-__device__ __forceinline__ f32x16 mfma32<__bf16>(i32x4 a, i32x4 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
 // Code T of 8 consecutive ones (bits [T BITS, T BITS + BITS) of hi:lo) as
 // the fp32 value c - z without integer conversions: the code is masked in
 // place inside a window dword that starts at a code boundary and holds it
 // below bit 23 - BITS, OR-ed under the exponent of 2^(23 - sh), so the float
 // reads 2^(23 - sh) + c exactly; sub[sh / BITS] = 2^(23 - sh) + z.
-template <int BITS>
-struct QuarterWindows {
-  static constexpr int kPer = (23 - BITS) / BITS + 1;   // codes per window
-};
-template <int BITS>
-using QuarterOps = MagicOps<BITS, QuarterWindows<BITS>::kPer>;
-
 template <int BITS, int T>
 __device__ __forceinline__ float quarter_cz(uint32_t lo, uint32_t hi, const float* sub,
                                             const QuarterOps<BITS>& ops) {
@@ -916,19 +832,6 @@ struct TileLds {
   static_assert(kAux <= 2 * kTWaves, "at most two aux transfers per wave");
 };
 
-template <typename S>
-__device__ __forceinline__ f32x4 mfma16x32(i32x4 a, i32x4 b, f32x4 c);
-template <>
-__device__ __forceinline__ f32x4 mfma16x32<_Float16>(i32x4 a, i32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
-                                                __builtin_bit_cast(half8, b), c, 0, 0, 0);
-}
-template <>
-__device__ __forceinline__ f32x4 mfma16x32<__bf16>(i32x4 a, i32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
 // Wait until at most the last U issue units of this wave (2 + n_aux
 // transfers each) are in flight.
 template <int U>
@@ -1238,47 +1141,6 @@ constexpr int kSmMinM = 5;                   // below this the vector kernel is 
 constexpr int64_t kGemmMaxK = 1ll << 22;     // the large-tile kernel's limits (32-bit tile offsets,
 constexpr int64_t kGemmMaxM = 65535ll * 128; // activation-row tiles on grid y)
 constexpr int kSmMaxM = 1024;
-
-// Code T of 16 consecutive ones held in bits [T BITS, T BITS + BITS) of sw.
-template <int BITS, int NW, int T>
-__device__ __forceinline__ uint32_t code_in(const uint32_t (&sw)[NW]) {
-  constexpr int b = T * BITS, w = b >> 5, o = b & 31;
-  constexpr uint32_t mask = (1u << BITS) - 1u;
-  if constexpr (o + BITS <= 32) return (sw[w] >> o) & mask;
-  else return __builtin_amdgcn_alignbit(sw[w + 1], sw[w], o) & mask;
-}
-
-// Code T of the run as fp32 (c - z) in the magic-exponent form of the
-// quarter unpacking: windows of QuarterWindows<BITS>::kPer codes start at code
-// boundaries, sub[sh / BITS] = 2^(23 - sh) + z.
-template <int BITS, int NW, int T>
-__device__ __forceinline__ float small_cz(const uint32_t (&sw)[NW], const float* sub,
-                                          const QuarterOps<BITS>& ops) {
-  constexpr int kPer = QuarterWindows<BITS>::kPer;
-  constexpr int w0 = (T / kPer) * kPer * BITS, wi = w0 >> 5, o = w0 & 31;
-  constexpr int sh = T * BITS - w0;
-  uint32_t win;
-  if constexpr (o == 0) win = sw[wi];
-  else if constexpr (wi + 1 >= NW || o + sh + BITS <= 32) win = sw[wi] >> o;
-  else win = __builtin_amdgcn_alignbit(sw[wi + 1], sw[wi], o);
-  return __uint_as_float(and_or(win, ops.mask[sh / BITS], ops.expo[sh / BITS])) - sub[sh / BITS];
-}
-
-// Codes 2P and 2P + 1 of the run as two S values (c - z), exact.
-template <typename S, int BITS, int NW, int P>
-__device__ __forceinline__ int small_pair(const uint32_t (&sw)[NW], half2v negz, const float* sub,
-                                          const QuarterOps<BITS>& ops) {
-  if constexpr (std::is_same<S, _Float16>::value) {
-    const uint32_t c0 = code_in<BITS, NW, 2 * P>(sw), c1 = code_in<BITS, NW, 2 * P + 1>(sw);
-    const uint32_t v = c0 | (c1 << 16) | 0x64006400u;
-    return (int)__builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, v) + negz);
-  } else {
-    // small integers are exact in fp32 and their upper halves are exact bf16
-    const float f0 = small_cz<BITS, NW, 2 * P>(sw, sub, ops);
-    const float f1 = small_cz<BITS, NW, 2 * P + 1>(sw, sub, ops);
-    return (int)__builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
-  }
-}
 
 // MB blocks of 32 activation rows per workgroup (grid z walks the row tiles),
 // FS 32-column stages per activation fill.

@@ -1,0 +1,700 @@
+// Around a block of experts: the router, tokens sorted by expert, rows there and back.
+//
+// Pair t k + j is token t's j-th choice.  Sorted rows are the pairs by expert, an expert's
+// in their own order, and last, past offsets[count], pairs of experts elsewhere.
+#include <algorithm>
+
+#include "kv.h"
+#include "moe.h"
+
+namespace awq {
+namespace {
+
+// ---- over the 16 lanes of a row -----------------------------------------------------
+template <int N>
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  return __builtin_amdgcn_update_dpp(0, x, 0x120 + N, 0xf, 0xf, false);
+}
+template <class F>
+__device__ __forceinline__ uint32_t row_all(uint32_t x, F f) {
+  x = f(x, turned<8>(x));
+  x = f(x, turned<4>(x));
+  x = f(x, turned<2>(x));
+  return f(x, turned<1>(x));
+}
+__device__ __forceinline__ uint32_t row_umax(uint32_t x) {
+  return row_all(x, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ uint32_t row_umin(uint32_t x) {
+  return row_all(x, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+__device__ __forceinline__ uint32_t row_or(uint32_t x) {
+  return row_all(x, [](uint32_t a, uint32_t b) { return a | b; });
+}
+__device__ __forceinline__ float row_max(float x) {
+  return __uint_as_float(row_all(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float row_sum(float x) {
+  return __uint_as_float(row_all(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+__device__ __forceinline__ uint64_t row_umax(uint64_t x) {
+  const uint32_t hi = row_umax((uint32_t)(x >> 32));
+  const uint32_t lo = row_umax((uint32_t)(x >> 32) == hi ? (uint32_t)x : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// ---- the router -------------------------------------------------------------------------
+// Keys that order as the scores do: 0 for what is taken or not there, 1 for NaN, which ranks last.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  if (x != x) return 1u;
+  const uint32_t u = __float_as_uint(x + 0.0f);    // -0 and 0 are equal
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t key_of(double x) {
+  if (x != x) return 1ull;
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
+// One token by 16 lanes, lane l holding the logits l, l + 16, ..  Choice j ends in lane j % 16.
+// Without a bias the scores order as the logits; with one they are formed in 64 bits, where
+// two experts' sums may lie close.
+template <class S, int VPL, class Key>
+__device__ __forceinline__ void route_token(const RouteArgs& a, const S* row, int l, int (&index)[2],
+                                            float (&weight)[2]) {
+  float x[VPL];
+  Key key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int c = l + 16 * i;
+    const bool in = c < a.E;
+    x[i] = in ? to_f32(row[in ? c : 0]) : -INFINITY;
+    if constexpr (sizeof(Key) == 8) {
+      const double v = x[i];
+      const double score = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : v;
+      key[i] = in ? key_of(score + (double)a.bias[in ? c : 0]) : 0;
+    } else {
+      key[i] = in ? key_of(x[i]) : 0;
+    }
+  }
+  float v[2] = {-INFINITY, -INFINITY};
+  index[0] = index[1] = 0;
+  for (int j = 0; j < a.k; ++j) {
+    Key best = 0;
+    uint32_t at = 0xffffffffu;
+    float mine = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool more = key[i] > best;             // the lowest of equals
+      best = more ? key[i] : best;
+      at = more ? (uint32_t)(l + 16 * i) : at;
+      mine = more ? x[i] : mine;
+    }
+    const Key top = row_umax(best);
+    const uint32_t won = row_umin(best == top ? at : 0xffffffffu);
+    const float value = __uint_as_float(row_or(at == won ? __float_as_uint(mine) : 0u));
+    if (l == (j & 15)) {
+      v[j >> 4] = value;
+      index[j >> 4] = (int)won;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = won == (uint32_t)(l + 16 * i) ? (Key)0 : key[i];
+  }
+  const bool there[2] = {l < a.k, 16 + l < a.k};
+  float p[2], sum;
+  if (a.sigmoid) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) p[s] = there[s] ? 1.0f / (1.0f + expf(-v[s])) : 0.0f;
+    sum = a.normalise ? row_sum(p[0] + p[1]) : 1.0f;
+  } else {
+    // the weights of the chosen alone need their own largest; a row of -inf has no weight
+    float top = there[0] ? v[0] : -INFINITY;
+    top = there[1] ? fmaxf(top, v[1]) : top;
+    if (!a.normalise) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) top = fmaxf(top, x[i]);
+    }
+    top = row_max(top);
+    const float least = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) p[s] = there[s] ? expf(v[s] - least) : 0.0f;
+    sum = p[0] + p[1];
+    if (!a.normalise) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum += expf(x[i] - least);   // exp(-inf) past the last
+    }
+    sum = row_sum(sum);
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) weight[s] = sum == 0.0f ? 0.0f : p[s] / sum * a.scale;
+}
+
+__device__ __forceinline__ int bucket_of(const SortArgs& a, int expert) {
+  const uint32_t e = (uint32_t)expert - (uint32_t)a.first;
+  return e < (uint32_t)a.count ? (int)e : a.count;
+}
+
+constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
+constexpr int kBuckets = kMostExperts + 1;
+constexpr int kSmallPairs = 1024;          // sorted by one workgroup, by the router's own
+
+struct SortLds {
+  int cur[kSortWaves][kBuckets];           // next place of a wave's pairs in a bucket
+  int start[kBuckets];
+  int sums[kSortWaves];
+};
+
+// Exclusive sums of start[0 .. buckets) over the workgroup, in place; -> the last but one's end.
+__device__ __forceinline__ void scan_starts(SortLds& s, int buckets) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kPer = (kBuckets + kSortThreads - 1) / kSortThreads;
+  int v[kPer], own = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    v[i] = e < buckets ? s.start[e] : 0;
+    own += v[i];
+  }
+  int upto = own;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int x = __shfl_up(upto, m);
+    upto += lane >= m ? x : 0;
+  }
+  if (lane == 63) s.sums[wave] = upto;
+  __syncthreads();
+  int run = upto - own;
+  for (int w = 0; w < wave; ++w) run += s.sums[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    if (e < buckets) s.start[e] = run;
+    run += v[i];
+  }
+  __syncthreads();
+}
+
+// Counts of the workgroup's pairs [lo, hi) by wave and bucket; bucket(p) tells a pair's.
+template <class F>
+__device__ __forceinline__ void count_pairs(SortLds& s, int64_t lo, int64_t hi, int64_t step, int buckets,
+                                            F bucket) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < kSortWaves * buckets; e += kSortThreads) s.cur[e / buckets][e % buckets] = 0;
+  __syncthreads();
+  const int64_t from = lo + wave * step, to = from + step < hi ? from + step : hi;
+  for (int64_t p = from + lane; p < to; p += 64) atomicAdd(&s.cur[wave][bucket(p)], 1);
+  __syncthreads();
+}
+
+// Places of the pairs: start[] holds where the workgroup's pairs of a bucket begin, cur[] its
+// waves' counts.  A wave takes 64 pairs at a time; those of a bucket find each other by the bits
+// of its number.
+template <class F>
+__device__ __forceinline__ void place_pairs(const SortArgs& a, SortLds& s, int64_t lo, int64_t hi, int64_t step,
+                                            int buckets, F bucket) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < buckets; e += kSortThreads) {
+    int run = s.start[e];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = s.cur[w][e];
+      s.cur[w][e] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz(buckets);
+  const int64_t from = lo + wave * step, to = from + step < hi ? from + step : hi;
+  volatile int* cur = s.cur[wave];
+  for (int64_t p0 = from; p0 < to; p0 += 64) {
+    const int64_t p = p0 + lane;
+    const bool in = p < to;
+    const int b = in ? bucket(p) : 0;
+    uint64_t same = __ballot(in);
+    for (int i = 0; i < bits; ++i) {
+      const uint64_t set = __ballot((b >> i) & 1);
+      same &= (b >> i) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const int at = in ? cur[b] + rank : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (in && rank == 0) cur[b] = at + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (in) {
+      a.order[at] = (int32_t)p;
+      a.place[p] = at;
+    }
+  }
+}
+
+// All pairs in one workgroup.
+template <class F>
+__device__ __forceinline__ void sort_alone(const SortArgs& a, SortLds& s, F bucket) {
+  const int buckets = a.count + 1;
+  const int64_t step = ((a.n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
+  count_pairs(s, 0, a.n, step, buckets, bucket);
+  for (int e = threadIdx.x; e < buckets; e += kSortThreads) {
+    int all = 0;
+    for (int w = 0; w < kSortWaves; ++w) all += s.cur[w][e];
+    s.start[e] = all;
+  }
+  __syncthreads();
+  scan_starts(s, buckets);
+  for (int e = threadIdx.x; e < buckets; e += kSortThreads) a.offsets[e] = s.start[e];
+  place_pairs(a, s, 0, a.n, step, buckets, bucket);
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_alone_kernel(SortArgs a) {
+  __shared__ SortLds s;
+  sort_alone(a, s, [&](int64_t p) { return bucket_of(a, a.experts[p]); });
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+  __shared__ int hist[kBuckets];
+  const int buckets = a.count + 1;
+  for (int e = threadIdx.x; e < buckets; e += kSortThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * a.per, hi = lo + a.per < a.n ? lo + a.per : a.n;
+  for (int64_t p = lo + threadIdx.x; p < hi; p += kSortThreads) atomicAdd(&hist[bucket_of(a, a.experts[p])], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < buckets; e += kSortThreads) a.hist[(int64_t)blockIdx.x * buckets + e] = hist[e];
+}
+
+// Every workgroup sums the counts of all of them, and of those before it.
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
+  __shared__ SortLds s;
+  __shared__ int before[kBuckets];
+  const int buckets = a.count + 1;
+  const int64_t lo = blockIdx.x * a.per, hi = lo + a.per < a.n ? lo + a.per : a.n;
+  const int64_t step = ((a.per + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
+  auto bucket = [&](int64_t p) { return bucket_of(a, a.experts[p]); };
+  for (int e = threadIdx.x; e < buckets; e += kSortThreads) {
+    int all = 0, less = 0;
+#pragma unroll 8
+    for (int b = 0; b < a.blocks; ++b) {
+      const int c = a.hist[(int64_t)b * buckets + e];
+      all += c;
+      less += b < (int)blockIdx.x ? c : 0;
+    }
+    s.start[e] = all;
+    before[e] = less;
+  }
+  count_pairs(s, lo, hi, step, buckets, bucket);
+  scan_starts(s, buckets);
+  for (int e = threadIdx.x; e < buckets; e += kSortThreads) {
+    if (blockIdx.x == 0) a.offsets[e] = s.start[e];
+    s.start[e] += before[e];
+  }
+  __syncthreads();
+  place_pairs(a, s, lo, hi, step, buckets, bucket);
+}
+
+template <class T, int VPL, class Key>
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, int64_t lo, int64_t hi, int* hist, int* buckets) {
+  typedef typename T::storage S;
+  const int l = threadIdx.x & 15, row = threadIdx.x >> 4, rows = blockDim.x >> 4;
+  for (int64_t t0 = lo; t0 < hi; t0 += rows) {
+    const int64_t t = t0 + row;
+    const bool in = t < hi;
+    int index[2];
+    float weight[2];
+    route_token<S, VPL, Key>(a, (const S*)a.logits + (in ? t : lo) * a.stride, l, index, weight);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int j = 16 * s + l;
+      if (!in || j >= a.k) continue;
+      const int64_t p = t * a.k + j;
+      a.experts[p] = index[s];
+      a.weights[p] = weight[s];
+      if (hist) atomicAdd(&hist[bucket_of(a.s, index[s])], 1);
+      if (buckets) buckets[p] = bucket_of(a.s, index[s]);
+    }
+  }
+}
+
+// A workgroup's tokens, and how many pairs of them a bucket has.
+template <class T, int VPL, class Key>
+__global__ __launch_bounds__(kSortThreads) void route_kernel(RouteArgs a, int64_t per) {
+  __shared__ int hist[kBuckets];
+  const int buckets = a.s.count + 1;
+  const bool sorted = a.s.offsets != nullptr;
+  if (sorted) {
+    for (int e = threadIdx.x; e < buckets; e += kSortThreads) hist[e] = 0;
+    __syncthreads();
+  }
+  const int64_t lo = blockIdx.x * per, hi = lo + per < a.T ? lo + per : a.T;
+  route_tokens<T, VPL, Key>(a, lo, hi, sorted ? hist : nullptr, nullptr);
+  if (!sorted) return;
+  __syncthreads();
+  for (int e = threadIdx.x; e < buckets; e += kSortThreads) a.s.hist[(int64_t)blockIdx.x * buckets + e] = hist[e];
+}
+
+// Few tokens: routed and sorted by one workgroup.
+template <class T, int VPL, class Key>
+__global__ __launch_bounds__(kSortThreads) void route_alone_kernel(RouteArgs a) {
+  __shared__ SortLds s;
+  __shared__ int pairs[kSmallPairs];
+  route_tokens<T, VPL, Key>(a, 0, a.T, nullptr, pairs);
+  __syncthreads();
+  sort_alone(a.s, s, [&](int64_t p) { return pairs[p]; });
+}
+
+// dlogits of one token by 16 lanes.
+template <class T>
+__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
+  typedef typename T::storage S;
+  const int l = threadIdx.x & 15;
+  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const bool in = t < a.T;
+  const S* row = (const S*)a.logits + (in ? t : 0) * a.stride;
+  const int64_t p0 = (in ? t : 0) * a.k;
+  float top = -INFINITY, all = 0.0f;
+  if (!a.sigmoid) {
+    if (a.normalise) {
+      for (int j = l; j < a.k; j += 16) {
+        const int e = a.experts[p0 + j];
+        top = fmaxf(top, (uint32_t)e < (uint32_t)a.E ? to_f32(row[e]) : -INFINITY);
+      }
+    } else {
+      for (int c = l; c < a.E; c += 16) top = fmaxf(top, to_f32(row[c]));
+    }
+    top = row_max(top);
+    top = top == -INFINITY ? 0.0f : top;
+    if (!a.normalise) {
+      for (int c = l; c < a.E; c += 16) all += expf(to_f32(row[c]) - top);
+      all = row_sum(all);
+    }
+  }
+  // choice j in lane j % 16: probability, gradient, and how it goes on to the logit
+  float p[2], g[2], sum = 0.0f, dot = 0.0f;
+  int index[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int j = 16 * s + l;
+    index[s] = j < a.k ? a.experts[p0 + j] : -1;
+    const bool ok = (uint32_t)index[s] < (uint32_t)a.E;
+    index[s] = ok ? index[s] : -1;
+    const float v = ok ? to_f32(row[index[s]]) : -INFINITY;
+    p[s] = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top);
+    p[s] = ok ? p[s] : 0.0f;
+    g[s] = ok ? a.dweights[p0 + j] * a.scale : 0.0f;
+    sum += p[s];
+  }
+  sum = a.normalise ? row_sum(sum) : a.sigmoid ? 1.0f : all;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    p[s] = sum == 0.0f ? 0.0f : p[s] / sum;
+    dot += index[s] >= 0 ? g[s] * p[s] : 0.0f;
+  }
+  dot = row_sum(dot);
+  float d[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    // normalised, both: q (g - sum g q), times 1 - p where q are shares of sigmoids; softmax over
+    // all: p g here and - p sum g p for every expert below
+    d[s] = p[s] * (a.normalise ? g[s] - dot : g[s]);
+    if (a.sigmoid) d[s] *= index[s] >= 0 ? 1.0f / (1.0f + expf(to_f32(row[index[s]]))) : 0.0f;
+  }
+  const bool spread = !a.sigmoid && !a.normalise;
+  S* out = (S*)a.dlogits + t * a.E;
+  for (int c0 = 0; c0 < a.E; c0 += 16) {
+    const int c = c0 + l;
+    float v = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+      const int at = __shfl(j < 16 ? index[0] : index[1], j & 15, 16);
+      const float dj = __shfl(j < 16 ? d[0] : d[1], j & 15, 16);
+      v += at == c ? dj : 0.0f;
+    }
+    if (!in || c >= a.E) continue;
+    if (spread) v -= all == 0.0f ? 0.0f : expf(to_f32(row[c]) - top) / all * dot;
+    out[c] = from_f32<S>(v);
+  }
+}
+
+// ---- rows there and back ------------------------------------------------------------------
+constexpr int kRun = 8;                    // columns that a thread takes at a time
+constexpr int kTogether = 8;               // choices whose rows are in flight together
+
+template <class S>
+__device__ __forceinline__ Run<kRun, S> load_part(const S* p, int left) {
+  if (left >= kRun) return load_run<kRun>(p);
+  Run<kRun, S> r;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) r.v[i] = i < left ? p[i] : (S)0.0f;
+  return r;
+}
+template <class S>
+__device__ __forceinline__ void store_part(S* p, const float* x, int left) {
+  if (left >= kRun) return store_run<kRun>(p, x);
+#pragma unroll
+  for (int i = 0; i < kRun; ++i)
+    if (i < left) p[i] = from_f32<S>(x[i]);
+}
+
+// The token and the run of columns of a thread: several tokens to a workgroup where rows are short.
+struct Part {
+  int64_t t;
+  int v, step, runs;
+  __device__ __forceinline__ Part(const RowsArgs& a) {
+    runs = (int)((a.C + kRun - 1) / kRun);
+    step = runs < 256 ? runs : 256;
+    const int tokens = 256 / step, r = (int)threadIdx.x / step;
+    t = ((int64_t)a.first_block + blockIdx.x) * tokens + r;
+    v = (int)threadIdx.x % step;
+    if (r >= tokens) t = INT64_MAX;
+  }
+};
+int64_t part_blocks(int64_t T, int64_t C) {
+  const int64_t runs = (C + kRun - 1) / kRun, tokens = 256 / std::min<int64_t>(runs, 256);
+  return (T + tokens - 1) / tokens;
+}
+
+// rows[place] = weight tokens[t], 0 where the expert is elsewhere.
+template <class T>
+__global__ __launch_bounds__(256) void gather_kernel(RowsArgs a) {
+  typedef typename T::storage S;
+  const Part u(a);
+  if (u.t >= a.T) return;
+  const int64_t n = a.T * a.k;
+  const int kept = a.offsets[a.count];
+  for (int v = u.v; v < u.runs; v += u.step) {
+    const int64_t c = (int64_t)v * kRun;
+    const int left = (int)(a.C - c < kRun ? a.C - c : kRun);
+    const Run<kRun, S> r = load_part((const S*)a.tokens + u.t * a.stride + c, left);
+    float x[kRun], y[kRun];
+    widen(r, x);
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t p = u.t * a.k + j;
+      const int at = a.place[p];
+      if ((uint64_t)(int64_t)at >= (uint64_t)n) continue;
+      const bool here = at < kept;
+      const float w = a.weights ? a.weights[p] : 1.0f;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) y[i] = here ? x[i] * w : 0.0f;
+      store_part((S*)a.out + at * a.C + c, y, left);
+    }
+  }
+}
+
+// out[t] = tokens[t] + sum_j weight rows[place], in the order of the choices.
+template <class T, class TO>
+__global__ __launch_bounds__(256) void combine_kernel(RowsArgs a) {
+  typedef typename T::storage S;
+  typedef typename TO::storage SO;
+  const Part u(a);
+  if (u.t >= a.T) return;
+  const int kept = a.offsets[a.count];
+  const int64_t n = a.T * a.k, most = kept < n ? kept : n;
+  for (int v = u.v; v < u.runs; v += u.step) {
+    const int64_t c = (int64_t)v * kRun;
+    const int left = (int)(a.C - c < kRun ? a.C - c : kRun);
+    float y[kRun] = {};
+    if (a.tokens) widen(load_part((const SO*)a.tokens + u.t * a.stride + c, left), y);
+    for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+      Run<kRun, S> r[kTogether];
+      float w[kTogether];
+      bool here[kTogether];
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        const bool in = j0 + j < a.k;
+        const int64_t p = u.t * a.k + (in ? j0 + j : 0);
+        const int at = a.place[p];
+        here[j] = in && at >= 0 && at < most;
+        w[j] = a.weights ? a.weights[p] : 1.0f;
+        if (here[j]) r[j] = load_part((const S*)a.rows + at * a.C + c, left);
+      }
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        if (!here[j]) continue;
+        float x[kRun];
+        widen(r[j], x);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) y[i] = fmaf(w[j], x[i], y[i]);
+      }
+    }
+    store_part((SO*)a.out + u.t * a.C + c, y, left);
+  }
+}
+
+// Sorted rows of tokens as gather_kernel, and the product of every pair's token and row; a
+// workgroup a token.
+template <class TT, class T>
+__global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
+  typedef typename TT::storage ST;
+  typedef typename T::storage S;
+  __shared__ float sums[4][kTogether];
+  const int64_t t = (int64_t)a.first_block + blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t n = a.T * a.k;
+  const int kept = a.offsets[a.count];
+  const int runs = (int)((a.C + kRun - 1) / kRun);
+  for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+    float dot[kTogether] = {};
+    int at[kTogether];
+    float w[kTogether];
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const bool in = j0 + j < a.k;
+      const int64_t p = t * a.k + (in ? j0 + j : 0);
+      at[j] = in ? a.place[p] : -1;
+      at[j] = (uint64_t)(int64_t)at[j] < (uint64_t)n ? at[j] : -1;
+      w[j] = a.weights ? a.weights[p] : 1.0f;
+    }
+    for (int v = tid; v < runs; v += 256) {
+      const int64_t c = (int64_t)v * kRun;
+      const int left = (int)(a.C - c < kRun ? a.C - c : kRun);
+      Run<kRun, S> r[kTogether];
+      if (a.dots) {
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j)
+          if (at[j] >= 0 && at[j] < kept) r[j] = load_part((const S*)a.rows + at[j] * a.C + c, left);
+      }
+      float d[kRun], x[kRun];
+      widen(load_part((const ST*)a.tokens + t * a.stride + c, left), d);
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        if (at[j] < 0) continue;
+        const bool here = at[j] < kept;
+        if (a.dots && here) {
+          widen(r[j], x);
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) dot[j] = fmaf(d[i], x[i], dot[j]);
+        }
+        if (a.out) {
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) x[i] = here ? d[i] * w[j] : 0.0f;
+          store_part((S*)a.out + at[j] * a.C + c, x, left);
+        }
+      }
+    }
+    if (!a.dots) continue;
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+#pragma unroll
+      for (int m = 32; m >= 1; m >>= 1) dot[j] += __shfl_xor(dot[j], m);
+      if (lane == 0) sums[wave][j] = dot[j];
+    }
+    __syncthreads();
+    if (tid < kTogether && j0 + tid < a.k)
+      a.dots[t * a.k + j0 + tid] = (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
+    __syncthreads();
+  }
+}
+
+template <class F>
+hipError_t by_type(awq_dtype_t dt, F f) {
+  if (dt == AWQ_F32) f(F32T{});
+  else if (dt == AWQ_F16) f(F16T{});
+  else f(BF16T{});
+  return hipGetLastError();
+}
+
+// Workgroups that share the pairs; each sums all their counts, so not more than the chip takes at once.
+int sort_blocks(int64_t n) { return (int)std::min<int64_t>(256, (n + 511) / 512); }
+
+template <class T, int VPL>
+void go_route(const RouteArgs& a, bool alone, int64_t per, int blocks, hipStream_t st) {
+  if (a.bias) {
+    if (alone) route_alone_kernel<T, VPL, uint64_t><<<1, kSortThreads, 0, st>>>(a);
+    else route_kernel<T, VPL, uint64_t><<<blocks, kSortThreads, 0, st>>>(a, per);
+  } else {
+    if (alone) route_alone_kernel<T, VPL, uint32_t><<<1, kSortThreads, 0, st>>>(a);
+    else route_kernel<T, VPL, uint32_t><<<blocks, kSortThreads, 0, st>>>(a, per);
+  }
+}
+
+}  // namespace
+
+size_t moe_sort_ws_bytes(int64_t n, int count) {
+  return n <= kSmallPairs ? 0 : (size_t)sort_blocks(n) * (count + 1) * 4;
+}
+
+hipError_t launch_moe_sort(SortArgs a, hipStream_t st) {
+  ProfScope prof("awq_moe_sort", st);
+  if (a.n <= kSmallPairs) {
+    sort_alone_kernel<<<1, kSortThreads, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  a.blocks = sort_blocks(a.n);
+  a.per = (a.n + a.blocks - 1) / a.blocks;
+  sort_count_kernel<<<a.blocks, kSortThreads, 0, st>>>(a);
+  sort_place_kernel<<<a.blocks, kSortThreads, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route(RouteArgs a, awq_dtype_t dt, hipStream_t st) {
+  ProfScope prof("awq_moe_route", st);
+  const bool sorted = a.s.offsets != nullptr;
+  a.s.n = a.T * a.k;
+  a.s.experts = a.experts;
+  const bool alone = sorted && a.s.n <= kSmallPairs;
+  // a workgroup's pairs are whole tokens
+  int64_t blocks = sorted ? sort_blocks(a.s.n) : (a.T + 31) / 32;
+  blocks = std::min<int64_t>(std::max<int64_t>(blocks, 1), 1 << 20);
+  const int64_t per = std::max<int64_t>(1, (a.T + blocks - 1) / blocks);
+  blocks = (a.T + per - 1) / per;
+  a.s.blocks = (int)blocks;
+  a.s.per = per * a.k;
+  const hipError_t e = by_type(dt, [&](auto t) {
+    typedef decltype(t) T;
+    if (a.E <= 64) go_route<T, 4>(a, alone, per, (int)blocks, st);
+    else if (a.E <= 128) go_route<T, 8>(a, alone, per, (int)blocks, st);
+    else if (a.E <= 256) go_route<T, 16>(a, alone, per, (int)blocks, st);
+    else if (a.E <= 512) go_route<T, 32>(a, alone, per, (int)blocks, st);
+    else go_route<T, 64>(a, alone, per, (int)blocks, st);
+  });
+  if (e != hipSuccess || !sorted || alone) return e;
+  sort_place_kernel<<<a.s.blocks, kSortThreads, 0, st>>>(a.s);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route_grad(const RouteGradArgs& a, awq_dtype_t dt, hipStream_t st) {
+  ProfScope prof("awq_moe_route_grad", st);
+  return by_type(dt, [&](auto t) {
+    route_grad_kernel<decltype(t)><<<(unsigned)((a.T + 15) / 16), 256, 0, st>>>(a);
+  });
+}
+
+hipError_t launch_moe_gather(RowsArgs a, awq_dtype_t dt, hipStream_t st) {
+  ProfScope prof("awq_moe_gather", st);
+  return by_type(dt, [&](auto t) {
+    in_parts(part_blocks(a.T, a.C), 256, [&](uint32_t first, unsigned grid) {
+      a.first_block = first;
+      gather_kernel<decltype(t)><<<grid, 256, 0, st>>>(a);
+    });
+  });
+}
+
+hipError_t launch_moe_combine(RowsArgs a, awq_dtype_t dt, awq_dtype_t out_dt, hipStream_t st) {
+  ProfScope prof("awq_moe_combine", st);
+  hipError_t e = hipSuccess;
+  const hipError_t f = by_type(dt, [&](auto t) {
+    e = by_type(out_dt, [&](auto o) {
+      in_parts(part_blocks(a.T, a.C), 256, [&](uint32_t first, unsigned grid) {
+        a.first_block = first;
+        combine_kernel<decltype(t), decltype(o)><<<grid, 256, 0, st>>>(a);
+      });
+    });
+  });
+  return e != hipSuccess ? e : f;
+}
+
+hipError_t launch_moe_combine_grad(RowsArgs a, awq_dtype_t token_dt, awq_dtype_t dt, hipStream_t st) {
+  ProfScope prof("awq_moe_combine_grad", st);
+  hipError_t e = hipSuccess;
+  const hipError_t f = by_type(token_dt, [&](auto t) {
+    e = by_type(dt, [&](auto r) {
+      in_parts(a.T, 256, [&](uint32_t first, unsigned grid) {
+        a.first_block = first;
+        combine_grad_kernel<decltype(t), decltype(r)><<<grid, 256, 0, st>>>(a);
+      });
+    });
+  });
+  return e != hipSuccess ? e : f;
+}
+
+}  // namespace awq

@@ -1,0 +1,326 @@
+"""The packed product with its epilogue on the GPU, of one projection and of each expert's, against the
+64-bit oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_act_amd as awq
+from oracle import moe_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF_ULP = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+TINY = {"f32": 2.0 ** -149, "f16": 2.0 ** -24, "bf16": 2.0 ** -133}
+# an activation's steepest slope
+SLOPE = {"none": 1.0, "relu": 1.0, "silu": 1.1, "gelu": 1.13, "gelu_tanh": 1.13}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    awq.library()
+    yield
+    torch.cuda.synchronize()
+
+
+def wide(t):
+    return t.detach().double().cpu().numpy()
+
+
+def normal(rng, shape, kind):
+    return torch.from_numpy(rng.normal(size=shape).astype(np.float32)).to(TYPES[kind]).cuda()
+
+
+class Packed:
+    """Random packed weights of `experts` projections [n, K]."""
+
+    def __init__(self, rng, experts, n, K, bits, group, dead=False):
+        top = 2 ** bits - 1
+        codes = np.clip(np.rint(rng.normal(size=(experts * n, K)) * (top + 1) / 5 + top / 2), 0, top).astype(np.uint8)
+        steps = (np.exp(rng.normal(size=(experts * n, K // group)) * 0.3) * 5 / (top + 1) * K ** -0.5).astype(np.float32)
+        if dead:      # groups whose step is 0 among the others, first and last ones too
+            steps[rng.random(steps.shape) < 0.3] = 0
+        zeros = rng.integers(0, top + 1, size=steps.shape)
+        words, meta = ref.repack(codes, steps, zeros, bits)
+        self.codes, self.meta = torch.from_numpy(words.view(np.int32)).cuda(), torch.from_numpy(meta).cuda()
+        self.W = ref.weights_of(codes, steps, zeros, group).reshape(experts, n, K)
+        self.bits, self.group, self.K = bits, group, K
+
+
+def bound(x, W, offsets, source, group, bias, act, gated, want, residual, kind):
+    """How far a result may be off.  v: K products that are exact, K / 2 additions or fewer in a chain, two
+    roundings for every group, eight waves' sums, the bias: |dv| <= (K + 2 K / group + 12) 2^-24 sum |x w| +
+    2^-24 |bias| (all first order; 2% for the rest).  The activation: its slope times that, and
+    24 2^-24 max(|v|, 1) for exp, erf or tanh and what is done with it (|v| below 16: its argument's
+    rounding times |v|).  Gated: both factors'.  One rounding to the output's type, one to fp32 before."""
+    K = x.shape[1]
+    size = ref.experts_product(np.abs(x), np.abs(W), offsets, source)
+    v = ref.experts_product(x, W, offsets, source)
+    if bias is not None:
+        rows = np.zeros_like(size)
+        for e in range(W.shape[0]):
+            rows[offsets[e]:offsets[e + 1]] = bias[e]
+        size, v = size + np.abs(rows), v + rows
+    dv = 1.02 * (K + 2 * K / group + 14) * 2.0 ** -24 * size
+
+    def acted(v, dv):
+        return SLOPE[act] * dv + (0 if act in ("none", "relu") else 24 * 2.0 ** -24 * np.maximum(np.abs(v), 1) * np.minimum(16, np.maximum(1, np.abs(v))))
+
+    if gated:
+        half = v.shape[1] // 2
+        g, u, dg, du = v[:, :half], v[:, half:], dv[:, :half], dv[:, half:]
+        a, da = np.abs(ref.activate(g, act)), acted(g, dg)
+        off = a * du + np.abs(u) * da + da * du + 2.0 ** -24 * a * np.abs(u)
+    else:
+        off = acted(v, dv)
+    more = 0 if residual is None else 2.0 ** -24 * np.abs(residual)
+    return off + more + (HALF_ULP[kind] + 2.0 ** -23) * (np.abs(want) + off) + TINY[kind]
+
+
+def run(rng, rows, n, K, bits, group, kind, out, act, gated, biased, residual, pad=0, routing=None, gather=False, experts=1,
+        dead=False):
+    p = Packed(rng, experts, n, K, bits, group, dead)
+    outs = n // 2 if gated else n
+    total = rows if routing is None else routing.tokens * routing.k
+    x = normal(rng, ((routing.tokens if gather else total) if routing else rows, K + pad), kind)[:, :K]
+    bias = normal(rng, (experts, n), "f32") if biased else None
+    res = normal(rng, (total, outs + pad), out)[:, :outs] if residual else None
+    y = awq.awq_lowbit_linear(x, p.codes, p.meta, bits, group, bias=bias, activation=act, gated=gated, residual=res,
+                              routing=routing, gather=gather, out_dtype=TYPES[out])
+    assert y.shape == (total, outs) and y.dtype is TYPES[out]
+    offsets = [0, rows] if routing is None else routing.offsets.cpu().numpy()
+    source = routing.order.cpu().numpy() // routing.k if gather else None
+    xn = wide(x)
+    v = ref.experts_product(xn, p.W, offsets, source)
+    b = None if bias is None else wide(bias)
+    if b is not None:
+        for e in range(experts):
+            v[offsets[e]:offsets[e + 1]] += b[e]
+    rn = None if res is None else wide(res)
+    want = ref.finish(v, act, gated, rn)
+    want[offsets[-1]:] = 0                                   # rows that no expert has: nothing is added either
+    off = np.abs(wide(y) - want)
+    assert (off <= bound(xn, p.W, offsets, source, group, b, act, gated, want, rn, out)).all(), \
+        (off.max(), np.unravel_index(off.argmax(), off.shape))
+    assert (wide(y)[offsets[-1]:] == 0).all()
+    return y
+
+
+DENSE = [   # rows, n, K, bits, group, kind, out, act, gated, bias, residual, pad
+    (1, 16, 32, 4, 32, "f16", "f16", "none", False, False, False, 0),
+    (1, 1, 128, 4, 128, "bf16", "f32", "none", False, True, False, 0),
+    (1, 2, 64, 3, 64, "bf16", "bf16", "silu", True, True, True, 0),
+    (2, 29, 96, 2, 32, "f16", "f32", "relu", False, False, True, 8),
+    (3, 130, 1024, 3, 512, "bf16", "bf16", "gelu", False, True, False, 0),
+    (15, 64, 160, 5, 32, "f16", "bf16", "gelu_tanh", False, False, False, 16),
+    (16, 65, 256, 6, 64, "bf16", "f16", "none", False, False, True, 0),
+    (17, 34, 384, 7, 128, "f16", "f16", "silu", True, False, False, 0),
+    (31, 257, 320, 8, 64, "bf16", "f32", "none", False, True, True, 8),
+    (33, 96, 512, 4, 256, "f16", "f32", "gelu_tanh", True, True, True, 0),
+    (64, 513, 256, 4, 128, "bf16", "bf16", "none", False, False, False, 0),
+    (65, 100, 288, 4, 32, "bf16", "f32", "silu", True, True, False, 0),
+    (100, 255, 1184, 3, 32, "f16", "f16", "relu", False, False, True, 8),
+    (127, 30, 448, 2, 64, "bf16", "f32", "gelu", False, True, False, 0),
+    (129, 516, 640, 4, 128, "f16", "f16", "none", False, False, True, 0),
+    (200, 300, 96, 5, 32, "bf16", "bf16", "gelu_tanh", True, False, False, 0),
+    (256, 256, 2048, 4, 128, "bf16", "f32", "none", False, False, False, 0),
+    (300, 333, 736, 6, 32, "f16", "bf16", "silu", False, True, False, 24),
+    (513, 66, 512, 7, 512, "bf16", "f32", "none", True, True, True, 0),
+    (700, 600, 256, 8, 256, "f16", "f32", "none", False, False, False, 0),
+    (1000, 1100, 160, 4, 32, "bf16", "bf16", "silu", True, False, True, 0),
+    (260, 2100, 1152, 3, 128, "f16", "f16", "gelu_tanh", False, True, True, 0),
+    (400, 1200, 1088, 4, 64, "bf16", "bf16", "none", False, False, False, 0),
+]
+
+
+@pytest.mark.parametrize("case", DENSE, ids=lambda c: "-".join(map(str, c)))
+def test_one_projection(case):
+    run(np.random.default_rng(case[0] * 31 + case[1]), *case)
+
+
+@pytest.mark.parametrize("bits", range(2, 9))
+@pytest.mark.parametrize("rows", [1, 20, 40, 90, 150])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_every_width(bits, rows, kind):
+    for group in (32, 64, 128):
+        run(np.random.default_rng(bits * 100 + rows), rows, 80, 256 + group, bits, group, kind, "f32", "none", False, False, False)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 150])
+def test_groups_whose_step_is_zero(rows):
+    for bits, group, kind in ((4, 32, "f16"), (3, 64, "bf16"), (8, 128, "f16")):
+        run(np.random.default_rng(rows), rows, 70, 640, bits, group, kind, "f32", "none", False, False, False, dead=True)
+
+
+def routed(rng, T, k, of, count, lean=0.0, first=0):
+    """A routing; lean: this share of the tokens takes the first experts alone."""
+    e = np.stack([np.arange(k) if rng.random() < lean else rng.permutation(of)[:k] for _ in range(T)]) if T else np.zeros((0, k))
+    return awq.awq_moe_sort(torch.from_numpy(e.astype(np.int32)).cuda(), count, first_expert=first)
+
+
+EXPERTS = [   # T, k, of, count, lean, then as above without rows and pad
+    (1, 8, 64, 64, 0, 48, 256, 4, 128, "bf16", "bf16", "silu", True, False, False),
+    (1, 1, 1, 1, 0, 16, 32, 4, 32, "f16", "f32", "none", False, True, False),
+    (5, 2, 8, 3, 0, 33, 128, 3, 64, "f16", "f16", "gelu", False, True, True),
+    (40, 6, 200, 200, 0, 20, 96, 4, 32, "bf16", "f32", "none", False, False, False),
+    (61, 4, 16, 16, 0.5, 64, 288, 5, 32, "bf16", "bf16", "silu", True, True, False),
+    (130, 2, 4, 4, 0, 130, 384, 4, 128, "f16", "f16", "none", False, False, True),
+    (300, 3, 7, 5, 0.7, 70, 512, 3, 256, "bf16", "f32", "gelu_tanh", True, False, True),
+    (700, 2, 3, 3, 1.0, 96, 160, 4, 32, "f16", "bf16", "relu", False, True, False),
+    (257, 4, 70, 65, 0, 40, 128, 2, 128, "bf16", "bf16", "none", False, False, False),
+    (64, 1, 2, 2, 1.0, 258, 320, 8, 64, "f16", "f32", "silu", True, False, False),
+    (900, 1, 130, 129, 0.3, 36, 64, 6, 32, "f16", "f32", "none", False, False, False),
+]
+
+
+@pytest.mark.parametrize("case", EXPERTS, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("gather", [False, True])
+def test_experts(case, gather):
+    T, k, of, count, lean, n, K, bits, group, kind, out, act, gated, bias, residual = case
+    rng = np.random.default_rng(T * 7 + n)
+    r = routed(rng, T, k, of, count, lean)
+    run(rng, None, n, K, bits, group, kind, out, act, gated, bias, residual, routing=r, gather=gather, experts=count, pad=8)
+
+
+def test_no_pair_or_no_row():
+    rng = np.random.default_rng(1)
+    e = torch.full((4, 2), 9, dtype=torch.int32, device="cuda")       # experts elsewhere
+    r = awq.awq_moe_sort(e, 3)
+    run(rng, None, 24, 64, 4, 32, "f16", "f16", "none", False, False, False, routing=r, gather=True, experts=3)
+    r = awq.awq_moe_sort(e[:0], 3)
+    p = Packed(rng, 3, 24, 64, 4, 32)
+    for gather in (False, True):
+        y = awq.awq_lowbit_linear(torch.empty(0, 64, dtype=torch.float16, device="cuda"), p.codes, p.meta, 4, 32, routing=r,
+                                  gather=gather)
+        assert y.shape == (0, 24)
+
+
+@pytest.mark.parametrize("rows", [3, 50, 140])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_a_row_that_is_not_finite_stays_alone(rows, kind):
+    rng = np.random.default_rng(rows)
+    p = Packed(rng, 1, 72, 224, 4, 32)
+    x = normal(rng, (rows, 224), kind)
+    good = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32)
+    for value in (float("nan"), float("inf"), float("-inf")):
+        bad = x.clone()
+        bad[1, 100] = value
+        y = awq.awq_lowbit_linear(bad, p.codes, p.meta, 4, 32)
+        assert not torch.isfinite(y[1]).any()
+        keep = torch.arange(rows, device="cuda") != 1
+        assert torch.equal(y[keep], good[keep])
+
+
+@pytest.mark.parametrize("rows", [2, 150])
+def test_large_and_small_activations(rows):
+    """Rows far apart in size, and elements of a row: each row as exact as alone."""
+    rng = np.random.default_rng(rows)
+    p = Packed(rng, 1, 40, 512, 4, 128)
+    x = rng.normal(size=(rows, 512)) * 2.0 ** rng.integers(-60, 60, size=(rows, 1)) * 2.0 ** rng.integers(-12, 4, size=(1, 512))
+    x = torch.from_numpy(x.astype(np.float32)).bfloat16().cuda()
+    y = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 128, out_dtype=torch.float32)
+    want = ref.experts_product(wide(x), p.W, [0, rows])
+    off = bound(wide(x), p.W, [0, rows], None, 128, None, "none", False, want, None, "f32")
+    assert (np.abs(wide(y) - want) <= off).all()
+
+
+def test_as_the_other_packed_products():
+    """The same weights through awq_lowbit_repack, beside awq_lowbit_gemm: the results of two exact forms."""
+    rng = np.random.default_rng(4)
+    W = normal(rng, (96, 256), "bf16")
+    s = torch.ones(256, device="cuda")
+    codes, steps, zeros = awq.awq_quantize_pack(W, s, 4, 64)
+    ct, mt = awq.awq_lowbit_repack(codes, steps, zeros, 256, 4, 64)
+    x = normal(rng, (70, 256), "bf16")
+    a = awq.awq_lowbit_linear(x, ct, mt, 4, 64, out_dtype=torch.float32)
+    b = awq.awq_lowbit_gemm(x, ct, mt, 4, 64)
+    W64 = wide(awq.awq_fake_quant(W.float(), s, 4, 64)[0])
+    size = np.abs(wide(x)) @ np.abs(W64).T
+    # both within (K + 2 K / group + 14) 2^-24 of the exact sum of absolute products
+    assert (np.abs(wide(a) - wide(b)) <= 2 * 1.02 * (256 + 8 + 14) * 2.0 ** -24 * size).all()
+
+
+def test_binding_refuses():
+    rng = np.random.default_rng(3)
+    p = Packed(rng, 2, 16, 64, 4, 32)
+    r = routed(rng, 4, 2, 2, 2)
+    x = normal(rng, (4, 64), "f16")
+    ok = dict(routing=r, gather=True)
+    awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, **ok)
+    for call in (lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 3, 32, **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64, **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 0, **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, routing=r),
+                 lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, gather=True),
+                 lambda: awq.awq_lowbit_linear(x[:, :32], p.codes, p.meta, 4, 32, **ok),
+                 lambda: awq.awq_lowbit_linear(x.float(), p.codes, p.meta, 4, 32, **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, activation="tanh", **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes.cpu(), p.meta, 4, 32, **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes[:, :31].contiguous(), p.meta, 4, 32, **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, bias=x[0].float(), **ok),
+                 lambda: awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, residual=x[:, :16], **ok),
+                 lambda: awq.awq_lowbit_linear(normal(rng, (4, 68), "f16")[:, :64], p.codes, p.meta, 4, 32, **ok),
+                 lambda: awq.awq_lowbit_linear(x.T, p.codes, p.meta, 4, 32, **ok),
+                 lambda: awq.awq_lowbit_linear(normal(rng, (4, 72), "f16")[:, 4:68], p.codes, p.meta, 4, 32, **ok)):
+        with pytest.raises((ValueError, awq.AwqError)):
+            call()
+    with pytest.raises(RuntimeError, match="no gradient"):
+        awq.awq_lowbit_linear(x.requires_grad_(), p.codes, p.meta, 4, 32, **ok)
+    with torch.no_grad():
+        awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, **ok)
+
+
+@pytest.mark.parametrize("T", [3, 800])
+def test_captured_on_another_stream_and_replayed(T):
+    """A whole block, routed to down projection, in a graph; then eagerly beside it."""
+    rng = np.random.default_rng(T)
+    E, k, K, F = 8, 2, 256, 160
+    up, down = Packed(rng, E, 2 * F, K, 4, 128), Packed(rng, E, K, F, 4, 32)
+    logits, x = normal(rng, (T, E), "f32"), normal(rng, (T, K), "bf16")
+
+    def step():
+        r = awq.awq_moe_route(logits, k)
+        h = awq.awq_lowbit_linear(x, up.codes, up.meta, 4, 128, activation="silu", gated=True, routing=r, gather=True)
+        y = awq.awq_lowbit_linear(h, down.codes, down.meta, 4, 32, routing=r)
+        return awq.awq_moe_combine(y, r, r.weights, residual=x)
+
+    step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):       # two graphs, each with its own workspaces
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = step()
+        graphs.append((graph, y))
+    for i in range(3):
+        logits.copy_(normal(rng, (T, E), "f32"))
+        x.copy_(normal(rng, (T, K), "bf16"))
+        for graph, _ in graphs:
+            graph.replay()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for _, y in graphs), i
+
+
+def test_a_block_of_experts():
+    """Routed, up, down and combined, against the whole in 64 bits: four roundings to bf16 on the way."""
+    rng = np.random.default_rng(21)
+    T, E, k, K, F = 37, 6, 2, 128, 96
+    up, down = Packed(rng, E, 2 * F, K, 4, 64), Packed(rng, E, K, F, 4, 32)
+    logits, x = normal(rng, (T, E), "f32"), normal(rng, (T, K), "bf16")
+    r = awq.awq_moe_route(logits, k)
+    h = awq.awq_lowbit_linear(x, up.codes, up.meta, 4, 64, activation="silu", gated=True, routing=r, gather=True)
+    y = awq.awq_moe_combine(awq.awq_lowbit_linear(h, down.codes, down.meta, 4, 32, routing=r), r, r.weights, residual=x)
+    xn, e = wide(x), ref.choose(wide(logits), k)
+    w = ref.route_weights(wide(logits), e)
+    want, size = xn.copy(), np.abs(xn)
+    for t in range(T):
+        for j in range(k):
+            g = ref.finish((up.W[e[t, j]] @ xn[t])[None], "silu", True)[0]
+            want[t] += w[t, j] * (down.W[e[t, j]] @ g)
+            size[t] += w[t, j] * (np.abs(down.W[e[t, j]]) @ np.abs(g))
+    # h rounded (2^-8 of it at every product), y's rows rounded, the result rounded; 2^-12 for all that is fp32
+    assert (np.abs(wide(y) - want) <= (3 * 2.0 ** -8 + 2.0 ** -12) * size).all()
