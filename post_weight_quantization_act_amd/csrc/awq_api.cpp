@@ -1362,6 +1362,9 @@ awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows,
       x_rows > INT32_MAX || K > INT32_MAX / 2)
     return fail(AWQ_ERR_UNSUPPORTED, "experts=%lld above %d, or experts N, rows or K too large",
                 (long long)experts, awq::kMostExperts);
+  if ((uint64_t)(experts * N) * (uint64_t)(K / 32) > kMaxBufferBytes / 4 / bits ||
+      (uint64_t)(experts * N) * (uint64_t)(K / group) > kMaxBufferBytes / 8)
+    return fail(AWQ_ERR_UNSUPPORTED, "packed layer exceeds the 4 GiB operand limit");
   if (rows == 0) return AWQ_OK;
   if (x_rows < 1) return fail(AWQ_ERR_INVALID_ARG, "rows of an empty x");
   if (x_rows > 1 && stride > (int64_t)(kMaxBufferBytes / 2) / (x_rows - 1))

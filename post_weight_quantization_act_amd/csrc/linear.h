@@ -8,11 +8,15 @@ namespace awq {
 
 // Which kernel a call takes, and its grid; the same for all widths.
 struct LinearPlan {
-  bool tiles;        // linear_tile_kernel, else linear_few_kernel
+  bool tiles;        // linear_tile_kernel, else linear_rows_kernel or linear_few_kernel
   int blocks;        // row blocks of a tile: 16 rows each (few) or 32 (tiles)
   int waves;         // of a workgroup; few: they share the columns of K
   int64_t row_tiles;
   int col_tiles;
+  int most;          // rows of a tile
+  int team;          // > 0: linear_rows_kernel, so many of a workgroup's waves share a column tile
+  int col_groups;    // its workgroups of a row tile
+  size_t lds;        // and their LDS
 };
 
 template <int BITS>   // one for each of 2 to 8

@@ -10,6 +10,7 @@
 #error "compiled once for each width of codes"
 #endif
 
+#include "kv.h"
 #include "linear.h"
 
 namespace awq {
@@ -20,49 +21,90 @@ constexpr int BITS = AWQ_LINEAR_BITS;
 // ---- rows of a tile --------------------------------------------------------------------
 struct Tile {
   int64_t row0;      // first output row
-  int rows;          // 0: there is no such tile
+  int rows;
   int expert;        // `experts`: rows that no expert here has
 };
 
-// Tile `want` of the rows, `most` rows each, expert by expert; the wave's 64 lanes look at
-// 64 experts at a time.
-__device__ __forceinline__ Tile find_tile(const LinearArgs& a, int most, int64_t want) {
-  Tile t;
-  if (!a.offsets) {
-    t.row0 = want * most;
-    const int64_t left = a.rows - t.row0;
-    t.rows = left < 0 ? 0 : (int)(left < most ? left : most);
-    t.expert = 0;
-    return t;
-  }
-  const int lane = threadIdx.x & 63, total = (int)a.rows;
-  int before = 0;
-  for (int e0 = 0; e0 <= a.experts; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = e <= a.experts ? a.offsets[e] : total;
-    int hi = e < a.experts ? a.offsets[e + 1] : total;
+// Inclusive sums over the wave's lanes.
+__device__ __forceinline__ int wave_sums(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // from 1, 2, 4, 8 lanes below in a row of 16
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // a row's last into the next, a half's into the other
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
+}
+
+// The rows' tiles of `most` rows, expert by expert, and last those of rows that no expert has: a lane
+// counts a run of experts.
+struct Tiles {
+  const LinearArgs& a;
+  int most, each, mine, upto, all;     // all: tiles
+
+  __device__ __forceinline__ void rows_of(int e, int& lo, int& hi) const {
+    const int total = (int)a.rows;
+    lo = e <= a.experts ? a.offsets[e] : total;
+    hi = e < a.experts ? a.offsets[e + 1] : total;
     lo = lo < 0 ? 0 : lo > total ? total : lo;
     hi = hi < lo ? lo : hi > total ? total : hi;
-    const int tiles = (hi - lo + most - 1) / most;
-    int upto = tiles;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int x = __shfl_up(upto, m);
-      upto += lane >= m ? x : 0;
+  }
+  __device__ __forceinline__ Tiles(const LinearArgs& args, int most_rows) : a(args), most(most_rows) {
+    if (!a.offsets) {
+      all = (int)((a.rows + most - 1) / most);
+      return;
     }
-    const uint64_t mine = __ballot(want < before + upto);
-    if (mine) {
-      const int l = __builtin_ctzll(mine);
-      const int part = (int)want - (before + __builtin_amdgcn_readlane(upto - tiles, l));
-      const int from = __builtin_amdgcn_readlane(lo, l), to = __builtin_amdgcn_readlane(hi, l);
-      t.row0 = from + (int64_t)part * most;
-      t.rows = to - (int)t.row0 < most ? to - (int)t.row0 : most;
-      t.expert = e0 + l;
+    each = a.experts / 64 + 1;         // experts + 1 of them in all
+    mine = 0;
+    for (int i = 0; i < each; ++i) {
+      int lo, hi;
+      rows_of((int)(threadIdx.x & 63) * each + i, lo, hi);
+      mine += (hi - lo + most - 1) / most;
+    }
+    upto = wave_sums(mine);
+    all = __builtin_amdgcn_readlane(upto, 63);
+  }
+  // Tile want < all.
+  __device__ __forceinline__ Tile at(int want) const {
+    Tile t;
+    if (!a.offsets) {
+      t.row0 = (int64_t)want * most;
+      const int64_t left = a.rows - t.row0;
+      t.rows = (int)(left < most ? left : most);
+      t.expert = 0;
       return t;
     }
-    before += __builtin_amdgcn_readlane(upto, 63);
+    const int l = __builtin_ctzll(__ballot(want < upto));
+    want -= __builtin_amdgcn_readlane(upto - mine, l);
+    for (int e = l * each;; ++e) {
+      int lo, hi;
+      rows_of(e, lo, hi);
+      const int tiles = (hi - lo + most - 1) / most;
+      if (want < tiles || e >= a.experts) {
+        t.row0 = lo + (int64_t)want * most;
+        t.rows = hi - (int)t.row0 < most ? hi - (int)t.row0 : most;
+        t.expert = e;
+        return t;
+      }
+      want -= tiles;
+    }
   }
-  return Tile{0, 0, 0};
+};
+
+// Workgroups are dealt to the eight XCDs in turn.  Each XCD takes a run of tiles, eight row tiles by
+// all columns after one another, so that its L2 holds what neighbours share: the activations of
+// eight row tiles and an expert's weights.  (The grid is sized by a bound; past the tiles there are
+// none.)
+struct Place {
+  int row, col;
+};
+__device__ __forceinline__ Place place_of(uint32_t id, uint32_t col_tiles, uint32_t row_tiles) {
+  constexpr uint32_t kXcds = 8, kGroup = 8;
+  const uint32_t n = col_tiles * row_tiles, per = n / kXcds, more = n % kXcds, x = id % kXcds;
+  const uint32_t at = x * per + (x < more ? x : more) + id / kXcds;
+  const uint32_t group = at / (kGroup * col_tiles), in = at - group * (kGroup * col_tiles);
+  const uint32_t left = row_tiles - group * kGroup, rows = left < kGroup ? left : kGroup;
+  return {(int)(group * kGroup + in % rows), (int)(in / rows)};
 }
 
 // Row of x that output row r takes.
@@ -73,14 +115,19 @@ __device__ __forceinline__ int64_t source(const LinearArgs& a, int64_t r) {
 }
 
 // ---- epilogue ------------------------------------------------------------------------------
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case AWQ_ACT_RELU: return v < 0.0f ? 0.0f : v;
-    case AWQ_ACT_SILU: return v / (1.0f + expf(-v));
-    case AWQ_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case AWQ_ACT_GELU_TANH: return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
-    default: return v;
-  }
+// exp, quotients and tanh from the hardware's exp2 and reciprocal (an ulp each): relative error
+// a few 2^-24 and that of the exponent's own rounding, |v| 2^-24.  tanh's form is v / (1 + exp(-2 u)).
+__device__ __forceinline__ float over_one_plus_exp(float v, float minus) {
+  return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(minus * -1.44269504088896341f));
+}
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (ACT == AWQ_ACT_RELU) return v < 0.0f ? 0.0f : v;
+  else if constexpr (ACT == AWQ_ACT_SILU) return over_one_plus_exp(v, v);
+  else if constexpr (ACT == AWQ_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  else if constexpr (ACT == AWQ_ACT_GELU_TANH)
+    return over_one_plus_exp(v, 1.5957691216057307f * fmaf(0.044715f * v, v * v, v));
+  else return v;
 }
 
 __device__ __forceinline__ float load_as(const void* p, int64_t i, int type) {
@@ -93,18 +140,49 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, int type, float v) 
   else ((__bf16*)p)[i] = (__bf16)v;
 }
 
-// Output (row, column n) of an expert from its sums, gate and up where gated.
-__device__ __forceinline__ void finish(const LinearArgs& a, int expert, int64_t row, int n, float v, float up) {
+// N outputs of a row from column n on, from their sums, gates and ups where gated.
+template <int ACT, int N>
+__device__ __forceinline__ void finish_act(const LinearArgs& a, int expert, int64_t row, int n, float (&v)[N],
+                                           float (&up)[N]) {
   const int outputs = a.gated ? a.N / 2 : a.N;
   if (a.bias) {
-    const float* b = a.bias + (int64_t)expert * a.N;
-    v += b[n];
-    if (a.gated) up += b[outputs + n];
+    const float* b = a.bias + (int64_t)expert * a.N + n;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] += b[i];
+      if (a.gated) up[i] += b[outputs + i];
+    }
   }
-  v = activate(v, a.act);
-  if (a.gated) v *= up;
-  if (a.residual) v += load_as(a.residual, row * a.residual_stride + n, a.out_type);
-  store_as(a.out, row * outputs + n, a.out_type, v);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = activate<ACT>(v[i]);
+    if (a.gated) v[i] *= up[i];
+  }
+  if (a.residual) {
+    const int64_t at = row * a.residual_stride + n;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += load_as(a.residual, at + i, a.out_type);
+  }
+  const int64_t at = row * outputs + n;
+  if constexpr (N == 1) {
+    store_as(a.out, at, a.out_type, v[0]);
+  } else if (a.out_type == AWQ_F32) {
+    store_run<N>((float*)a.out + at, v);
+  } else if (a.out_type == AWQ_F16) {
+    store_run<N>((_Float16*)a.out + at, v);
+  } else {
+    store_run<N>((__bf16*)a.out + at, v);
+  }
+}
+template <int N>
+__device__ __forceinline__ void finish(const LinearArgs& a, int expert, int64_t row, int n, float (&v)[N], float (&up)[N]) {
+  switch (a.act) {
+    case AWQ_ACT_RELU: return finish_act<AWQ_ACT_RELU>(a, expert, row, n, v, up);
+    case AWQ_ACT_SILU: return finish_act<AWQ_ACT_SILU>(a, expert, row, n, v, up);
+    case AWQ_ACT_GELU: return finish_act<AWQ_ACT_GELU>(a, expert, row, n, v, up);
+    case AWQ_ACT_GELU_TANH: return finish_act<AWQ_ACT_GELU_TANH>(a, expert, row, n, v, up);
+    default: return finish_act<AWQ_ACT_NONE>(a, expert, row, n, v, up);
+  }
 }
 
 // ---- codes to values ------------------------------------------------------------------------
@@ -127,6 +205,134 @@ struct Zero {
   }
 };
 
+// The same in fp16 with fewer instructions, scaled: two codes in the low bits of the halves of a word
+// read as the subnormals c 2^-24, and one packed multiply-add makes (c - z) 2^-10 of them, exactly.
+// 4 bits: 11 instructions for eight codes, 8 bits: 8, others 16 to 18.
+constexpr float kHalfScale = 1024.0f;
+template <int P, int NW>
+__device__ __forceinline__ uint32_t two_codes(const uint32_t (&w)[NW]) {
+  constexpr int b = 2 * BITS * P, wi = b >> 5, o = b & 31;
+  if constexpr (BITS == 8) {
+    return __builtin_amdgcn_perm(0u, w[wi], o == 0 ? 0x0c010c00u : 0x0c030c02u);
+  } else if constexpr (BITS == 4) {
+    constexpr uint32_t k = P & 3;
+    return __builtin_amdgcn_perm((w[wi] >> 4) & 0x0f0f0f0fu, w[wi] & 0x0f0f0f0fu, 0x0c040c00u + 0x00010001u * k);
+  } else {
+    constexpr uint32_t field = (1u << 2 * BITS) - 1u, mask = (1u << BITS) - 1u;
+    uint32_t p;
+    if constexpr (o + 2 * BITS <= 32) p = (w[wi] >> o) & field;
+    else p = __builtin_amdgcn_alignbit(w[wi + 1], w[wi], o) & field;
+    return (p << (16 - BITS) | p) & (mask | mask << 16);
+  }
+}
+template <int Q, int NW>
+__device__ __forceinline__ i32x4 eight_f16(const uint32_t (&w)[NW], bool live, half2v minus) {
+  const half2v by = __builtin_bit_cast(half2v, live ? 0x74007400u : 0u);    // 2^14; 0 where a step is 0
+  auto one = [&](uint32_t v) {
+    return (int)__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2v, v), by, minus));
+  };
+  return i32x4{one(two_codes<4 * Q>(w)), one(two_codes<4 * Q + 1>(w)), one(two_codes<4 * Q + 2>(w)),
+               one(two_codes<4 * Q + 3>(w))};
+}
+// Where the activations' order is the kernel's own, a chunk's 32 codes are taken in pairs that one
+// AND finds: in a window of the chunk's bits from o on, code a lies within bits 0 .. 9, code b within
+// bits 16 .. 25, both subnormals of their halves, and each half has its own factor in the
+// multiply-add.  Two instructions a pair, and one for each window.  32 codes of 4 bits: 36, of 3 bits:
+// 39 (64 in their order), of 2 bits: 34, of 5 to 7 bits: 47.
+struct Pairs {
+  int a[16], b[16], o[16];
+  int pos[32];                  // where code i's activation goes
+};
+constexpr Pairs pairs_of(int bits) {
+  Pairs p = {};
+  int n = 0;
+  for (int a0 = 0; a0 < 32;) {
+    // a run of `apart` codes with the next as many
+    const int apart = bits == 2 ? 8 : bits == 3 ? (a0 < 24 ? 6 : 4) : bits == 4 ? 4 : bits == 5 ? (a0 < 24 ? 3 : 4) : 2;
+    const int run = 32 - a0 < 2 * apart ? (32 - a0) / 2 : apart;
+    for (int i = 0; i < run; ++i) {
+      p.a[n] = a0 + i;
+      p.b[n] = a0 + run + i;
+      ++n;
+    }
+    a0 += 2 * run;
+  }
+  for (int i = 0; i < 16; ++i) {
+    const int at = bits * p.a[i], d = bits * (p.b[i] - p.a[i]);
+    const int least = d < 16 ? 16 - d : 0, most = 10 - bits < 26 - bits - d ? 10 - bits : 26 - bits - d;
+    // the window before, if it holds both; else one that begins as late as it may
+    const int before = i > 0 ? at - p.o[i - 1] : -1;
+    p.o[i] = before >= least && before <= most ? p.o[i - 1] : at - least;
+    p.pos[p.a[i]] = 2 * i;
+    p.pos[p.b[i]] = 2 * i + 1;
+  }
+  return p;
+}
+constexpr Pairs kPairs = pairs_of(BITS);
+constexpr bool pairs_fit() {
+  for (int i = 0; i < 16; ++i) {
+    const int s = BITS * kPairs.a[i] - kPairs.o[i], t = BITS * kPairs.b[i] - kPairs.o[i];
+    if (s < 0 || s + BITS > 10 || t < 16 || t + BITS > 26) return false;
+  }
+  return true;
+}
+static_assert(pairs_fit());
+
+template <int P>
+__device__ __forceinline__ int pair_of_window(const uint32_t (&w)[BITS], half2v minus) {
+  constexpr int o = kPairs.o[P], s = BITS * kPairs.a[P] - o, t = BITS * kPairs.b[P] - o - 16;
+  constexpr int wi = o < 0 ? 0 : o >> 5, sh = o < 0 ? 0 : o & 31;
+  constexpr uint32_t mask = (1u << BITS) - 1u;
+  uint32_t v;
+  if constexpr (o < 0) v = w[0] << -o;
+  else if constexpr (sh == 0) v = w[wi];
+  else if constexpr (sh + 26 > 32 && wi + 1 < BITS) v = __builtin_amdgcn_alignbit(w[wi + 1], w[wi], sh);
+  else v = w[wi] >> sh;
+  const half2v by = {(_Float16)(float)(1 << (14 - s)), (_Float16)(float)(1 << (14 - t))};
+  return (int)__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(
+                                               __builtin_bit_cast(half2v, v & (mask << s | mask << (16 + t))), by, minus));
+}
+template <int Q>
+__device__ __forceinline__ i32x4 eight_paired(const uint32_t (&w)[BITS], half2v minus) {
+  return i32x4{pair_of_window<4 * Q>(w, minus), pair_of_window<4 * Q + 1>(w, minus), pair_of_window<4 * Q + 2>(w, minus),
+               pair_of_window<4 * Q + 3>(w, minus)};
+}
+
+__device__ __forceinline__ half2v minus_f16(float z) {
+  const _Float16 n = (_Float16)(z * (-1.0f / kHalfScale));
+  return half2v{n, n};
+}
+
+// ---- loads ---------------------------------------------------------------------------------
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+}
+
+// Words at voff + soff bytes: one load for up to four.
+template <int NW>
+__device__ __forceinline__ void load_words(Buffer b, uint32_t voff, uint32_t soff, uint32_t (&w)[NW]) {
+  if constexpr (NW > 4) {
+    uint32_t lo[4], hi[NW - 4];
+    load_words<4>(b, voff, soff, lo);
+    load_words<NW - 4>(b, voff + 16, soff, hi);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = i < 4 ? lo[i < 4 ? i : 0] : hi[i < 4 ? 0 : i - 4];
+  } else if constexpr (NW == 1) {
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, voff, soff, 0);
+  } else if constexpr (NW == 2) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(b, voff, soff, 0);
+    w[0] = v[0], w[1] = v[1];
+  } else if constexpr (NW == 3) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b96(b, voff, soff, 0);
+    w[0] = v[0], w[1] = v[1], w[2] = v[2];
+  } else {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, 0);
+    w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
+  }
+}
+
 // ---- few rows ---------------------------------------------------------------------------------
 // A workgroup takes WT tiles of 16 weight rows (gated: a tile of gates and the same of ups) and
 // 16 TT output rows; its waves share the columns of K, 128 at a time, and add up in LDS.  Lane
@@ -141,8 +347,10 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
   const int outputs = a.gated ? a.N / 2 : a.N;
   const int wide = a.gated ? 16 : 16 * WT;             // outputs of a workgroup
   const int n0 = (int)(blockIdx.x % (uint32_t)col_tiles) * wide;
-  const Tile t = find_tile(a, 16 * TT, blockIdx.x / (uint32_t)col_tiles);
-  if (t.rows == 0) return;
+  Tiles tiles(a, 16 * TT);
+  const uint32_t want = blockIdx.x / (uint32_t)col_tiles;
+  if (want >= (uint32_t)tiles.all) return;
+  const Tile t = tiles.at(want);
   if (t.expert == a.experts) {
     for (int e = tid; e < t.rows * wide; e += blockDim.x)
       if (n0 + e % wide < outputs) store_as(a.out, (t.row0 + e / wide) * outputs + n0 + e % wide, a.out_type, 0.0f);
@@ -248,127 +456,377 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
   for (int e = tid; e < t.rows * wide; e += blockDim.x) {
     const int n = e % wide, m = e / wide;
     if (n0 + n >= outputs) continue;
-    const float v = total(a.gated ? 0 : n >> 4, m, n & 15);
-    const float up = a.gated ? total(WT - 1, m, n) : 0.0f;
+    float v[1] = {total(a.gated ? 0 : n >> 4, m, n & 15)}, up[1] = {a.gated ? total(WT - 1, m, n) : 0.0f};
     finish(a, t.expert, t.row0 + m, n0 + n, v, up);
   }
 }
 
+// Few rows and K columns that fit LDS: the rows come there once, as fp16 (bf16 ones scaled by a power
+// of two for each row, as scale_rows_kernel does).  The workgroup's eight waves are teams of `team`:
+// a team takes a column tile of 32 weight rows (gated: 16 gates and 16 ups), its waves 128 columns of
+// K each in turn, and adds up in LDS; then the next tile, whose first steps are on their way by then.
+constexpr int kRowPad = 8;         // elements between rows in LDS: 16 rows' parts lie in different banks
+constexpr int kRowWaves = 8;
+
+template <int TT>
+__global__ __launch_bounds__(64 * kRowWaves, TT == 1 ? 4 : 2) void linear_rows_kernel(LinearArgs a, LinearPlan p, int bf16) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int kAhead = BITS <= 4 ? 3 : 2;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), member = wave & (p.team - 1), mate0 = wave - member;
+  const int r = lane & 15, g = lane >> 4;
+  const int outputs = a.gated ? a.N / 2 : a.N, wide = a.gated ? 16 : 32;   // outputs of a column tile
+  Tiles tiles(a, p.most);
+  const int want = (int)(blockIdx.x / (uint32_t)p.col_groups);
+  if (want >= tiles.all) return;
+  const Tile t = tiles.at(want);
+  const int teams = kRowWaves / p.team, stride = p.col_groups * teams;
+  const int col0 = (int)(blockIdx.x % (uint32_t)p.col_groups) * teams;
+  if (t.expert == a.experts) {
+    for (int c0 = col0; c0 < p.col_tiles; c0 += stride)
+      for (int e = tid; e < t.rows * wide * teams; e += 64 * kRowWaves) {
+        const int n = c0 * wide + e % (wide * teams);
+        if (n < outputs) store_as(a.out, (t.row0 + e / (wide * teams)) * outputs + n, a.out_type, 0.0f);
+      }
+    return;
+  }
+  const int chunks = (int)(a.K / 32), steps = (chunks + 3) / 4;
+  const int mine = member < steps ? (steps - 1 - member) / p.team + 1 : 0;    // of a tile's steps
+  struct Step {
+    uint32_t w[2][BITS];
+    float2 m[2];
+  };
+  const uint32_t R = (uint32_t)a.R;
+  const Buffer rc = buffer_of(a.codes, (uint32_t)chunks * R * BITS * 4);
+  const Buffer rm = buffer_of(a.meta, (uint32_t)(chunks >> a.lg_cpg) * R * 8);
+  // offsets of this lane's row and chunk; a chunk past the last reads as 0, and its activations are 0
+  const uint32_t gm = (uint32_t)g >> a.lg_cpg;
+  uint32_t woff[2], moff[2];
+  auto aim = [&](int col) __attribute__((always_inline)) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      int n = col * wide + (a.gated ? 0 : 16 * w) + r;
+      n = n < outputs ? n : outputs - 1;
+      const uint32_t row = (uint32_t)t.expert * a.N + n + (a.gated && w ? outputs : 0);
+      woff[w] = (g * R + row) * (BITS * 4);
+      moff[w] = (gm * R + row) * 8;
+    }
+  };
+  auto load = [&](int i, Step& b) __attribute__((always_inline)) {
+    const uint32_t s = member + i * p.team;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      load_words<BITS>(rc, woff[w], 4 * s * R * (BITS * 4), b.w[w]);
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(rm, moff[w], (4 * s >> a.lg_cpg) * R * 8, 0);
+      b.m[w] = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    }
+  };
+  Step ring[kAhead];
+  auto prime = [&](int col) __attribute__((always_inline)) {
+    aim(col);
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+      if (d < mine) load(d, ring[d]);
+  };
+  if (col0 + wave / p.team < p.col_tiles) prime(col0 + wave / p.team);
+
+  // the rows
+  const int pitch = (int)a.K + kRowPad;
+  _Float16* xs = (_Float16*)lds;
+  f32x4* red = (f32x4*)(lds + (size_t)p.most * pitch * 2);        // [2][waves][2][TT][64]
+  __shared__ uint32_t top[16 * TT];
+  const int parts = ((int)a.K + 511) / 512, units = t.rows * parts;   // 512 elements: a wave's
+  constexpr int kHeld = 2;                                        // units that stay in registers
+  u16x8 held[kHeld];
+  auto fetch = [&](int u) __attribute__((always_inline)) {
+    const int m = u / parts, k = (u % parts) * 512 + 8 * lane;
+    return k < a.K ? *(const u16x8*)((const uint16_t*)a.x + source(a, t.row0 + m) * a.stride + k) : u16x8{};
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (wave + i * kRowWaves < units) held[i] = fetch(wave + i * kRowWaves);
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (wave + i * kRowWaves < units) f(wave + i * kRowWaves, held[i]);
+    for (int u = wave + kHeld * kRowWaves; u < units; u += kRowWaves) f(u, fetch(u));
+  };
+  if (bf16) {
+    if (tid < 16 * TT) top[tid] = 0;
+    __syncthreads();
+    each([&](int u, u16x8 v) __attribute__((always_inline)) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = v[i] & 0x7fffu;
+        most = most > b ? most : b;
+      }
+      atomicMax(&top[u / parts], most);
+    });
+    __syncthreads();
+  }
+  auto exponent = [&](int m) __attribute__((always_inline)) {
+    const int e = (int)(top[m] >> 7) - 127;
+    return !bf16 || top[m] == 0 || top[m] >= 0x7f80u ? 0 : e < -126 ? -126 : e;
+  };
+  each([&](int u, u16x8 v) __attribute__((always_inline)) {
+    const int m = u / parts, k = (u % parts) * 512 + 8 * lane;
+    if (k >= a.K) return;
+    half8 y = __builtin_bit_cast(half8, v);
+    if (bf16) {
+      const int e = exponent(m);
+      const bf16x8 x = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = (_Float16)ldexpf((float)x[i], -e);
+    }
+    // in the order that the codes are taken: lane l of four holds codes 8 (l % 4) .. of a chunk
+    _Float16* to = xs + m * pitch + (k & ~31);
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+      if ((lane & 3) != l) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[kPairs.pos[8 * l + i]] = y[i];
+    }
+  });
+  __syncthreads();
+
+  const int apart = a.lg_cpg == 0 ? 4 : a.lg_cpg == 1 ? 2 : 1;    // groups of a step's 128 columns
+  f32x4 tot[2][TT];
+  const _Float16* xrow[TT];       // rows that are not there read the first; nobody reads their sums
+#pragma unroll
+  for (int i = 0; i < TT; ++i) xrow[i] = xs + (16 * i + r < t.rows ? 16 * i + r : 0) * pitch;
+  auto multiply = [&](int i, const Step& b) __attribute__((always_inline)) {
+    const int s = member + i * p.team, j = 4 * s + g;
+    const bool in = j < chunks;
+    i32x4 x[TT][4];
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x[i][q] = *(const i32x4*)(xrow[i] + 32 * (in ? j : 0) + 8 * q);
+        if (4 * s + 4 > chunks) x[i][q] = in ? x[i][q] : i32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const half2v minus = minus_f16(b.m[w].y);
+      const i32x4 f[4] = {eight_paired<0>(b.w[w], minus), eight_paired<1>(b.w[w], minus), eight_paired<2>(b.w[w], minus),
+                          eight_paired<3>(b.w[w], minus)};
+      if (apart == 1) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc = mfma16x32<_Float16>(x[i][q], f[q], acc);
+          tot[w][i] += acc * b.m[w].x;
+        }
+      } else {
+        // several groups in the step: one at a time, the other chunks' activations taken as 0
+        for (int part = 0; part < apart; ++part) {
+          const int g0 = part * (4 / apart);
+          const bool on = g >= g0 && g < g0 + 4 / apart;
+          const float d = __shfl(b.m[w].x, 16 * g0 + r);
+#pragma unroll
+          for (int i = 0; i < TT; ++i) {
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc = mfma16x32<_Float16>(on ? x[i][q] : i32x4{0, 0, 0, 0}, f[q], acc);
+            tot[w][i] += acc * d;
+          }
+        }
+      }
+    }
+  };
+  int buf = 0;
+  for (int c0 = col0; c0 < p.col_tiles; c0 += stride, buf ^= 1) {
+    const int col = c0 + wave / p.team;
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < TT; ++i) tot[w][i] = f32x4{0, 0, 0, 0};
+    if (col < p.col_tiles) {
+      for (int i0 = 0; i0 < mine; i0 += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          if (i0 + d >= mine) break;
+          multiply(i0 + d, ring[d]);
+          if (i0 + d + kAhead < mine) load(i0 + d + kAhead, ring[d]);
+        }
+      }
+      if (col + stride < p.col_tiles) prime(col + stride);
+    }
+    f32x4* sums = red + (buf * kRowWaves + mate0) * 2 * TT * 64;  // the team's
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < TT; ++i) sums[((member * 2 + w) * TT + i) * 64 + lane] = tot[w][i];
+    if (p.team > 1) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // lane l of a tile holds weight row l % 16 and output rows 4 (l / 16) .. + 3
+    auto sum = [&](int w, int m, int n) __attribute__((always_inline)) {
+      const float* q = (const float*)sums + (((w * TT + (m >> 4)) * 64 + n + 16 * ((m & 15) >> 2)) * 4 + (m & 3));
+      float v = 0.0f;
+      for (int k = 0; k < p.team; ++k) v += q[k * 2 * TT * 256];
+      return v;
+    };
+    if (col < p.col_tiles) {
+      for (int e = member * 64 + lane; e < t.rows * wide; e += p.team * 64) {
+        const int n = e % wide, m = e / wide;
+        if (col * wide + n >= outputs) continue;
+        const float by = ldexpf(kHalfScale, exponent(m));
+        float v[1] = {by * sum(a.gated ? 0 : n >> 4, m, n & 15)}, up[1] = {a.gated ? by * sum(1, m, n) : 0.0f};
+        finish(a, t.expert, t.row0 + m, col * wide + n, v, up);
+      }
+    }
+  }
+}
+
 // ---- many rows -----------------------------------------------------------------------------------
-// A workgroup of four waves takes 32 MT output rows and 256 weight rows, a wave all the output
-// rows and 64 weight rows (gated: 32 gates and the same ups).  Activations go through LDS, 128
-// columns at a time, two buffers; a wave unpacks its own weights in registers, so each code
-// is unpacked once for 32 MT rows: lane half h takes codes 16 h .. 16 h + 15 of a chunk.
+// A workgroup takes 32 MT output rows and 256 weight rows, a wave all the output rows and 64 weight
+// rows (gated: 32 gates and the same ups).  Activations go through LDS, 128 columns at a time, two
+// buffers; a wave unpacks its own weights in registers, so each code is unpacked once for 32 MT
+// rows: lane half h takes codes 16 h .. 16 h + 15 of a chunk.  KS = 2: two sets of four waves take
+// every other 128 columns, and add up at the end.
 // The sums are in units of the group's step U: where the next group begins they are multiplied by
 // U / U', a step of 0 leaves the unit as it is and its codes count as 0.
-constexpr int kTileWaves = 4;
-
-template <class S, int MT>
-__global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a, int col_tiles) {
-  constexpr int NW = (BITS + 1) / 2;
+// WIDE: groups of 128 columns and more, so a step lies in one.
+template <class S, int MT, int KS, bool WIDE>
+__global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(LinearArgs a, int col_tiles) {
+  constexpr bool kF16 = sizeof(S) == 2 && std::is_same<S, _Float16>::value;
+  constexpr int NW = (BITS + 1) / 2, M = WIDE ? 1 : 4;
   constexpr int kRows = 32 * MT, kPer = 2 * MT;                  // transfers of a wave and step
-  __shared__ __attribute__((aligned(1024))) char xs[2][kRows * 256];
+  constexpr int kPitch = 68;     // floats of a row in the epilogue
+  __shared__ __attribute__((aligned(1024))) char xs[KS][2][kRows * 256];
+  static_assert(sizeof(xs) >= KS * 4 * 16 * kPitch * 4);
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, set = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
   const int r = lane & 31, h = lane >> 5;
   const int outputs = a.gated ? a.N / 2 : a.N;
   const int wide = a.gated ? 32 : 64;                            // outputs of a wave
-  const int first = (int)(blockIdx.x % (uint32_t)col_tiles) * kTileWaves * wide, n0 = first + wave * wide;
-  const Tile t = find_tile(a, kRows, blockIdx.x / (uint32_t)col_tiles);
-  if (t.rows == 0) return;
+  // Two workgroups share a compute unit.  Where more follow, the second of each pair starts 4 us
+  // later, so that one multiplies while the other waits for its first rows or stores its last
+  // (24570 rows for 64 experts, 2816 x 2048, 4 bits: 362 us without, 337 with 4, 341 with 8)
+  if (KS == 1 && gridDim.x > 512 && blockIdx.x >= 256 && blockIdx.x < 512)
+    for (int i = 0; i < 4; ++i) __builtin_amdgcn_s_sleep(32);
+  Tiles tiles(a, kRows);
+  if (blockIdx.x >= (uint32_t)tiles.all * (uint32_t)col_tiles) return;
+  const Place at = place_of(blockIdx.x, col_tiles, tiles.all);
+  const int first = at.col * 4 * wide, n0 = first + wave * wide;
+  const Tile t = tiles.at(at.row);
   if (t.expert == a.experts) {
-    const int span = kTileWaves * wide;
-    for (int e = tid; e < t.rows * span; e += 256)
+    const int span = 4 * wide;
+    for (int e = tid; e < t.rows * span; e += 256 * KS)
       if (first + e % span < outputs) store_as(a.out, (t.row0 + e / span) * outputs + first + e % span, a.out_type, 0.0f);
     return;
   }
   const int chunks = (int)(a.K / 32), steps = (chunks + 3) / 4, cmask = (1 << a.lg_cpg) - 1;
-  int64_t wrow[2];
+  const uint32_t R = (uint32_t)a.R;
+  uint32_t woff[2], moff[2];
+  const int qw = (16 * h * BITS) >> 5, qoff = (16 * h * BITS) & 31;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     int n = n0 + (a.gated ? 0 : 32 * w) + r;
     n = n < outputs ? n : outputs - 1;
-    wrow[w] = (int64_t)t.expert * a.N + n + (a.gated && w ? outputs : 0);
+    const uint32_t row = (uint32_t)t.expert * a.N + n + (a.gated && w ? outputs : 0);
+    woff[w] = (row * BITS + qw) * 4;
+    moff[w] = row * 8;
   }
+  const Buffer rc = buffer_of(a.codes, (uint32_t)chunks * R * BITS * 4);
+  const Buffer rm = buffer_of(a.meta, (uint32_t)(chunks >> a.lg_cpg) * R * 8);
   // activations: transfer q of a step brings rows 4 q .. 4 q + 3, 16-byte part p of row m from
   // part p ^ (m % 16); rows past the last are the first again
   const i32x4 rx = byte_range(a.x, (uint32_t)(((a.x_rows - 1) * a.stride + a.K) * 2));
-  const uint32_t base = (uint32_t)(uintptr_t)&xs[0][0];
+  const uint32_t base = (uint32_t)(uintptr_t)&xs[set][0][0];
   uint32_t xoff[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int m = 4 * (wave * kPer + i) + (lane >> 4);
     const int64_t row = source(a, t.row0 + (m < t.rows ? m : 0));
-    xoff[i] = (uint32_t)((row * a.stride + 8 * ((lane & 15) ^ (m & 15))) * 2);
+    xoff[i] = (uint32_t)((row * a.stride + 8 * ((lane & 15) ^ (m & 15))) * 2) + 256 * set;
   }
   auto fetch_x = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       to_lds16(rx, base + buf * (kRows * 256) + (wave * kPer + i) * 1024, xoff[i]);
-      xoff[i] += 256;
+      xoff[i] += 256 * KS;
     }
   };
-  const int qw = (16 * h * BITS) >> 5, qoff = (16 * h * BITS) & 31;
   struct Codes {
     uint32_t w[2][4][NW];
-    float2 m[2][4];
+    float2 m[2][M];
   };
   auto fetch_codes = [&](int s, Codes& c) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int64_t j = 4 * s + q < chunks ? 4 * s + q : chunks - 1;
+      int j = 4 * s + q;
+      if (!WIDE) j = j < chunks ? j : chunks - 1;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t* p = a.codes + (j * a.R + wrow[w]) * BITS + qw;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) c.w[w][q][i] = p[i];
-        c.m[w][q] = a.meta[(j >> a.lg_cpg) * a.R + wrow[w]];
+        load_words<NW>(rc, woff[w], (uint32_t)j * R * (BITS * 4), c.w[w][q]);
+        if (q < M) {
+          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rm, moff[w], (uint32_t)(j >> a.lg_cpg) * R * 8, 0);
+          c.m[w][q < M ? q : 0] = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+        }
       }
     }
   };
   const QuarterOps<BITS> ops = magic_ops<BITS, QuarterWindows<BITS>::kPer>();
   f32x16 acc[MT][2];
-  float unit[2] = {1.0f, 1.0f};
+  float unit[2] = {0.0f, 0.0f};      // 0: none yet
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int w = 0; w < 2; ++w) acc[i][w] = f32x16{};
-  auto multiply = [&](int s, const Codes& c, const char* xb) __attribute__((always_inline)) {
+  // where a group begins
+  auto rescale = [&](auto blocks, const float2 (&m)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const float u = m[w].x != 0.0f ? m[w].x : unit[w], by = unit[w] == 0.0f ? 1.0f : unit[w] / u;   // 1 within a group
+#pragma unroll
+      for (int i = 0; i < decltype(blocks)::value; ++i) acc[i][w] *= by;
+      unit[w] = u;
+    }
+  };
+  typedef i32x4 Weights[2][2];
+  auto unpack = [&](const Codes& c, int q, Weights& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const float2 m = c.m[w][q < M ? q : 0];
+      const bool live = m.x != 0.0f;
+      uint32_t run[NW];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        uint32_t v = c.w[w][q][i];
+        if constexpr (BITS % 2 == 1) v = i + 1 < NW ? __builtin_amdgcn_alignbit(c.w[w][q][i + 1 < NW ? i + 1 : i], v, qoff) : v >> qoff;
+        run[i] = kF16 || live ? v : 0u;
+      }
+      const float z = live ? m.y : 0.0f;
+      if constexpr (kF16) {
+        const half2v minus = minus_f16(z);
+        f[w][0] = eight_f16<0>(run, live, minus);
+        f[w][1] = eight_f16<1>(run, live, minus);
+      } else {
+        const Zero zero(z);
+        f[w][0] = eight<S, NW, 0>(run, zero.neg, zero.sub, ops);
+        f[w][1] = eight<S, NW, 1>(run, zero.neg, zero.sub, ops);
+      }
+    }
+  };
+  auto multiply = [&](auto blocks, int s, const Codes& c, const char* xb) __attribute__((always_inline)) {
+    constexpr int B = decltype(blocks)::value;      // row blocks that there are
+    if (WIDE) rescale(blocks, {c.m[0][0], c.m[1][0]});
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = 4 * s + q;
-      if (j >= chunks) break;
-      if ((j & cmask) == 0) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const float u = c.m[w][q].x != 0.0f ? c.m[w][q].x : unit[w];
-          if (j > 0) {
-            const float by = unit[w] / u;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) acc[i][w] *= by;
-          }
-          unit[w] = u;
-        }
+      if (!WIDE) {
+        if (j >= chunks) break;
+        if ((j & cmask) == 0 || q == 0) rescale(blocks, {c.m[0][q < M ? q : 0], c.m[1][q < M ? q : 0]});
       }
-      i32x4 f[2][2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const bool live = c.m[w][q].x != 0.0f;
-        uint32_t run[NW];
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          uint32_t v = c.w[w][q][i];
-          if constexpr (BITS % 2 == 1) v = i + 1 < NW ? __builtin_amdgcn_alignbit(c.w[w][q][i + 1 < NW ? i + 1 : i], v, qoff) : v >> qoff;
-          run[i] = live ? v : 0u;
-        }
-        const Zero z(live ? c.m[w][q].y : 0.0f);
-        f[w][0] = eight<S, NW, 0>(run, z.neg, z.sub, ops);
-        f[w][1] = eight<S, NW, 1>(run, z.neg, z.sub, ops);
-      }
+      Weights f;
+      unpack(c, q, f);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int i = 0; i < B; ++i) {
           const int m = 32 * i + r, p = 4 * q + 2 * h + k;
           const i32x4 fa = *(const i32x4*)(xb + m * 256 + 16 * (p ^ (m & 15)));
 #pragma unroll
@@ -376,54 +834,108 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a, int c
         }
     }
   };
-  Codes cur, next;
-  fetch_x(0);
-  fetch_codes(0, cur);
-  vm_wait<0>();
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) {
-      fetch_x((s + 1) & 1);
-      fetch_codes(s + 1, next);
+  auto run = [&](auto blocks) __attribute__((always_inline)) {
+    Codes one, two;
+    auto step = [&](int s, Codes& cur, Codes& next, int buf) __attribute__((always_inline)) {
+      if (s + KS < steps) {
+        fetch_x(buf ^ 1);
+        fetch_codes(s + KS, next);
+      }
+      if (s < steps) multiply(blocks, s, cur, xs[set][buf]);
+      vm_wait<0>();
+      __syncthreads();
+    };
+    if (set < steps) {
+      fetch_x(0);
+      fetch_codes(set, one);
     }
-    multiply(s, cur, xs[s & 1]);
     vm_wait<0>();
     __syncthreads();
-    cur = next;
+    for (int s = 0; s < steps; s += 2 * KS) {
+      step(s + set, one, two, 0);
+      if (s + KS < steps) step(s + KS + set, two, one, 1);
+    }
+  };
+  // an expert's last tile of half the rows or fewer takes half the products
+  if (MT > 1 && t.rows <= 16 * MT) {
+    asm volatile("");
+    run(std::integral_constant<int, (MT + 1) / 2>());
+  } else {
+    run(std::integral_constant<int, MT>());
   }
   // Lane l holds weight row l % 32 and output rows 8 (e / 4) + 4 (l / 32) + e % 4.  Sixteen rows at
-  // a time go through LDS, so that a wave stores whole rows of its outputs.
-  float* turn = (float*)&xs[0][0] + wave * 16 * 64;
-  const int span = a.gated ? 32 : 64, col = lane % span;
+  // a time go through LDS, from where a lane takes four columns of a row: 16 lanes a row (gated: 8).
+  float* turn = (float*)&xs[0][0][0] + wave * 16 * kPitch;
+  const int span = a.gated ? 8 : 16, col = 4 * (lane % span);
+  // a wave's LDS operations are in order; two sets wait for each other
+  auto meet = [&]() __attribute__((always_inline)) {
+    if (KS == 2) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int m = 8 * (e >> 2) + 4 * h + (e & 3);
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        turn[m * 64 + ((32 * w + r) ^ (32 * h))] = acc[i >> 1][w][8 * (i & 1) + e] * unit[w];
-    }
-    __syncthreads();
+  for (int w = 0; w < 2; ++w) unit[w] *= kF16 ? kHalfScale : 1.0f;
 #pragma unroll 1
-    for (int m = lane / span; m < 16; m += 64 / span) {
-      if (16 * i + m >= t.rows || n0 + col >= outputs) continue;
-      const int swap = 32 * ((m >> 2) & 1);
-      const float v = turn[m * 64 + (col ^ swap)];
-      const float up = a.gated ? turn[m * 64 + ((32 + col) ^ swap)] : 0.0f;
-      finish(a, t.expert, t.row0 + 16 * i + m, n0 + col, v, up);
+  for (int i = 0; i < 2 * MT && 16 * i < t.rows; ++i) {
+#pragma unroll
+    for (int k = 0; k < 2 * MT; ++k) {
+      if (k != i) continue;              // registers have no index: a copy of the stores for each, one of the rest
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int m = 8 * (e >> 2) + 4 * h + (e & 3);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          turn[set * (4 * 16 * kPitch) + m * kPitch + 32 * w + r] = acc[k >> 1][w][8 * (k & 1) + e] * unit[w];
+      }
     }
-    __syncthreads();
+    meet();
+#pragma unroll 1
+    for (int m = lane / span + set * (64 / span); m < 16; m += 64 / span * KS) {
+      if (16 * i + m >= t.rows) continue;
+      f32x4 v = *(const f32x4*)&turn[m * kPitch + col], up = *(const f32x4*)&turn[m * kPitch + 32 + col % 32];
+      if (KS == 2) {
+        v += *(const f32x4*)&turn[4 * 16 * kPitch + m * kPitch + col];
+        up += *(const f32x4*)&turn[4 * 16 * kPitch + m * kPitch + 32 + col % 32];
+      }
+      const int64_t row = t.row0 + 16 * i + m;
+      if (a.x_scale) {
+        const float by = a.x_scale[source(a, row)];
+        v *= by;
+        up *= by;
+      }
+      if (n0 + col + 4 <= outputs) {
+        float x[4] = {v[0], v[1], v[2], v[3]}, y[4] = {up[0], up[1], up[2], up[3]};
+        finish(a, t.expert, row, n0 + col, x, y);
+      } else {
+        for (int c = 0; c < outputs - n0 - col; ++c) {
+          float x[1] = {c == 0 ? v[0] : c == 1 ? v[1] : v[2]}, y[1] = {c == 0 ? up[0] : c == 1 ? up[1] : up[2]};
+          finish(a, t.expert, row, n0 + col + c, x, y);
+        }
+      }
+    }
+    meet();
   }
+}
+
+template <class S, bool WIDE>
+void go_tiles(const LinearArgs& a, const LinearPlan& p, unsigned grid, hipStream_t st) {
+  if (p.blocks == 2) linear_tile_kernel<S, 2, 1, WIDE><<<grid, 256, 0, st>>>(a, p.col_tiles);
+  else if (p.waves == 4) linear_tile_kernel<S, 4, 1, WIDE><<<grid, 256, 0, st>>>(a, p.col_tiles);
+  else linear_tile_kernel<S, 4, 2, WIDE><<<grid, 512, 0, st>>>(a, p.col_tiles);
 }
 
 template <class S>
 void go(const LinearArgs& a, const LinearPlan& p, hipStream_t st) {
   const unsigned grid = (unsigned)(p.col_tiles * p.row_tiles);
   if (p.tiles) {
-    if (p.blocks == 1) linear_tile_kernel<S, 1><<<grid, 256, 0, st>>>(a, p.col_tiles);
-    else if (p.blocks == 2) linear_tile_kernel<S, 2><<<grid, 256, 0, st>>>(a, p.col_tiles);
-    else linear_tile_kernel<S, 4><<<grid, 256, 0, st>>>(a, p.col_tiles);
+    if (a.lg_cpg >= 2) go_tiles<S, true>(a, p, grid, st);
+    else go_tiles<S, false>(a, p, grid, st);
+    return;
+  }
+  if (p.team > 0) {
+    const int bf16 = !std::is_same<S, _Float16>::value;
+    const unsigned blocks = (unsigned)(p.col_groups * p.row_tiles);
+    if (p.blocks == 1) linear_rows_kernel<1><<<blocks, 64 * kRowWaves, p.lds, st>>>(a, p, bf16);
+    else linear_rows_kernel<2><<<blocks, 64 * kRowWaves, p.lds, st>>>(a, p, bf16);
     return;
   }
   const size_t lds = (size_t)p.waves * 2 * p.blocks * 1024;

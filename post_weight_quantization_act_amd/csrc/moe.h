@@ -72,6 +72,7 @@ struct LinearArgs {
   const void* residual;          // [rows][outputs] of the output's type, or null
   void* out;                     // [rows][outputs]
   const int32_t *offsets, *order;   // null: all rows are expert 0's; rows as they are
+  const float* x_scale;          // [x_rows]: what a row of x is to be multiplied by; null: 1
   int64_t K, stride, residual_stride, x_rows;
   int64_t R;                     // rows of all experts' weights
   int64_t rows;
@@ -79,6 +80,6 @@ struct LinearArgs {
 };
 size_t linear_ws_bytes(const LinearArgs& a, awq_dtype_t dt);   // from rows, x_rows, N, K, experts, gated
 int64_t linear_threads(const LinearArgs& a);   // of the call's grid
-hipError_t launch_linear(const LinearArgs& a, awq_dtype_t dt, int bits, void* ws, hipStream_t st);
+hipError_t launch_linear(LinearArgs a, awq_dtype_t dt, int bits, void* ws, hipStream_t st);
 
 }  // namespace awq

@@ -160,6 +160,7 @@ def linear_args(**over):
     (dict(offsets=None, experts=1, x_rows=12), INVALID), (dict(per_token=0), INVALID), (dict(order=None), INVALID),
     (dict(experts=1025), UNSUPPORTED), (dict(N=1 << 30), UNSUPPORTED), (dict(rows=1 << 30), UNSUPPORTED),
     (dict(x_rows=1 << 31), UNSUPPORTED), (dict(K=1 << 30), UNSUPPORTED), (dict(rows=0), 0), (dict(x_rows=0), INVALID),
+    (dict(N=1 << 20, K=8192), UNSUPPORTED), (dict(N=1 << 23, bits=8), UNSUPPORTED),
     (dict(x_rows=1 << 24, stride=256), UNSUPPORTED), (dict(stride=1 << 31), UNSUPPORTED), (dict(stride=1 << 60), UNSUPPORTED),
     (dict(x=None), INVALID), (dict(codes=None), INVALID), (dict(meta=None), INVALID), (dict(out=None), INVALID),
     (dict(x=P + 8), UNSUPPORTED), (dict(codes=P + 2), UNSUPPORTED), (dict(meta=P + 4), UNSUPPORTED),
