@@ -616,7 +616,7 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
  * awq_moe_route_grad: dlogits [T, E] dense of dtype from dweights [T, k] and the
  *   experts that the call chose; no gradient goes to the choice, or to the bias.
  * awq_moe_sort: sorts n pairs by their experts [n].
- *   workspace: awq_moe_sort_workspace_size(n, count) bytes, 4-byte aligned, may be
+ *   workspace: awq_moe_sort_workspace_size(n, count) bytes, 16-byte aligned, may be
  *   NULL when that is 0; for awq_moe_route too, n = T k.
  * awq_moe_gather: out [T k, C] dense: row place[t, j] = weights[t, j] x[t], x [T, C] of
  *   dtype (row stride in elements), weights fp32 [T, k] or NULL: 1.  Products are

@@ -834,9 +834,9 @@ def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages:
 
 
 class Routing:
-    """Which tokens go to which experts: experts int32 [T, k] (their numbers), weights fp32 [T, k] or
-    None, and the pairs sorted by expert: offsets int32 [count + 1], order int32 [T k], place int32
-    [T, k].  Made by awq_moe_route or awq_moe_sort."""
+    """Which tokens go to which experts: experts int32 [T, k] (their numbers) or None, weights fp32
+    [T, k] or None, and the pairs sorted by expert: offsets int32 [count + 1], order int32 [T k], place
+    int32 [T, k].  Made by awq_moe_route or awq_moe_sort."""
 
     __slots__ = ("experts", "weights", "offsets", "order", "place", "gpu", "tokens", "k", "count")
 
@@ -844,19 +844,22 @@ class Routing:
         if not isinstance(place, _Tensor) or not place.is_cuda or place.dim() != 2:
             _refuse(place, "place", -1, "int32 [T, k]")
         gpu = place.get_device()
-        self.tokens, self.k = shape = place.shape
+        shape = place.shape
         _ints(place, "place", gpu, shape)
-        _ints(order, "order", gpu, (self.tokens * self.k,))
-        if not isinstance(offsets, _Tensor) or offsets.dim() != 1 or not offsets.shape[0]:
+        _ints(order, "order", gpu, (shape[0] * shape[1],))
+        if not isinstance(offsets, _Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
             _refuse(offsets, "offsets", gpu, "int32 [count + 1]")
         _ints(offsets, "offsets", gpu, offsets.shape)
         if experts is not None:
             _ints(experts, "experts", gpu, shape)
         if weights is not None:
             _dense(weights, "weights", gpu, shape, torch.float32)
-        self.count = offsets.shape[0] - 1
-        self.experts, self.weights, self.offsets, self.order, self.place, self.gpu = \
-            experts, weights, offsets, order, place, gpu
+        self._hold(experts, weights, offsets, order, place, gpu, shape[0], shape[1], offsets.shape[0] - 1)
+
+    def _hold(self, experts, weights, offsets, order, place, gpu, tokens, k, count):
+        self.experts, self.weights, self.offsets, self.order, self.place = experts, weights, offsets, order, place
+        self.gpu, self.tokens, self.k, self.count = gpu, tokens, k, count
+        return self
 
 
 def awq_moe_sort_workspace_size(n: int, count: int) -> int:
@@ -864,15 +867,17 @@ def awq_moe_sort_workspace_size(n: int, count: int) -> int:
 
 
 def _lists(T: int, k: int, count: int, device):
-    """offsets, order, place and a workspace, with their pointers."""
+    """Three int32 [T, k] of one allocation (the second is place, the third order) and offsets, with
+    the first's pointer and those of offsets, order, place and a workspace."""
     n = T * k
-    offsets = torch.empty(max(count, 0) + 1, dtype=torch.int32, device=device)
-    order = torch.empty(n, dtype=torch.int32, device=device)
-    place = torch.empty((T, k), dtype=torch.int32, device=device)
-    size = (_LIB or library()).awq_moe_sort_workspace_size(n, count)
-    ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
-    return (offsets, order, place), (offsets.data_ptr(), order.data_ptr(), place.data_ptr(),
-                                     None if ws is None else ws.data_ptr(), size), ws
+    ints = torch.empty((3, T, k), dtype=torch.int32, device=device)
+    offsets = torch.empty(count + 1 if count > 0 else 1, dtype=torch.int32, device=device)
+    at, ws, size = ints.data_ptr(), None, 0
+    if n > 1024:            # fewer are sorted without one
+        size = (_LIB or library()).awq_moe_sort_workspace_size(n, count)
+        ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    return ints.unbind(0), offsets, ws, at, (offsets.data_ptr(), at + 8 * n, at + 4 * n,
+                                             None if ws is None else ws.data_ptr(), size)
 
 
 def awq_moe_sort(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
@@ -886,9 +891,9 @@ def awq_moe_sort(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
     ep = _ints(experts, "experts", gpu, shape)
     if weights is not None:
         _dense(weights, "weights", gpu, shape, torch.float32)
-    lists, pointers, ws = _lists(T, k, num_experts, experts.device)
+    (_, place, order), offsets, ws, _, pointers = _lists(T, k, num_experts, experts.device)
     _run("awq_moe_sort", gpu, ep, T * k, first_expert, num_experts, *pointers)
-    return Routing(experts, weights, *lists)
+    return Routing.__new__(Routing)._hold(experts, weights, offsets, order.view(-1), place, gpu, T, k, num_experts)
 
 
 def _rows_of(x: torch.Tensor, name: str, gpu: int = -1) -> int:
@@ -910,26 +915,20 @@ def awq_moe_route(logits: torch.Tensor, k: int, score: str = "softmax",
     _rows_of(logits, "logits")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    rest = k, score, normalise, scale
-    local = logits.shape[1] if num_experts is None else num_experts, first_expert
-    if logits.requires_grad and torch.is_grad_enabled():
-        return Routing(*_RouteGrad.apply(logits, bias, rest, local))
-    return Routing(*_route(logits, bias, rest, local))
-
-
-def _route(logits, bias, rest, local):
+    if k < 1:
+        raise ValueError("k must be >= 1")
     gpu, device = logits.get_device(), logits.device
     T, E = logits.shape
-    k, score, normalise, scale = rest
-    if k < 0:
-        raise ValueError("k must be >= 1")
+    count = E if num_experts is None else num_experts
     bp = None if bias is None else _dense(bias, "bias", gpu, (E,), torch.float32)
-    experts = torch.empty((T, k), dtype=torch.int32, device=device)
     weights = torch.empty((T, k), dtype=torch.float32, device=device)
-    lists, pointers, ws = _lists(T, k, local[0], device)
+    (experts, place, order), offsets, ws, ep, pointers = _lists(T, k, count, device)
     _run("awq_moe_route", gpu, logits.data_ptr(), _dtype(logits), T, E, logits.stride(0), k, bp,
-         _SCORES[score], AWQ_ROUTE_NORMALISE if normalise else 0, scale, experts.data_ptr(), weights.data_ptr(), local[1], local[0], *pointers)
-    return experts, weights, *lists
+         _SCORES[score], AWQ_ROUTE_NORMALISE if normalise else 0, scale, ep, weights.data_ptr(),
+         first_expert, count, *pointers)
+    if logits.requires_grad and torch.is_grad_enabled():
+        weights = _RouteGrad.apply(logits, (weights, experts, score, normalise, scale))
+    return Routing.__new__(Routing)._hold(experts, weights, offsets, order.view(-1), place, gpu, T, k, count)
 
 
 def awq_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor,
@@ -951,23 +950,19 @@ def awq_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, dweights: to
 
 
 class _RouteGrad(torch.autograd.Function):
+    """Joins weights that awq_moe_route has made to the logits."""
+
     @staticmethod
-    def forward(ctx, logits, bias, rest, local):
-        out = _route(logits, bias, rest, local)
-        ctx.mark_non_differentiable(out[0], *out[2:])
-        ctx.set_materialize_grads(False)
-        ctx.save_for_backward(logits, out[0])
-        ctx.rest = rest
-        return out
+    def forward(ctx, logits, made):
+        weights, experts, *ctx.rest = made
+        ctx.save_for_backward(logits, experts)
+        return weights
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, _, g, *unused):
-        if g is None:
-            return None, None, None, None
+    def backward(ctx, g):
         logits, experts = ctx.saved_tensors
-        _, score, normalise, scale = ctx.rest
-        return awq_moe_route_grad(logits, experts, g.contiguous(), score, normalise, scale), None, None, None
+        return awq_moe_route_grad(logits, experts, g.contiguous(), *ctx.rest), None
 
 
 def _pair_weights(routing, weights, gpu):

@@ -245,8 +245,8 @@ awq_status_t moe_lists(int64_t n, int64_t first, int64_t count, int32_t* offsets
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(AWQ_ERR_WORKSPACE, "sorting needs %zu workspace bytes, got %zu", need,
                 workspace ? workspace_bytes : (size_t)0);
-  if (need > 0 && !aligned(workspace, 4))
-    return fail(AWQ_ERR_WORKSPACE, "workspace must be 4-byte aligned");
+  if (need > 0 && !aligned(workspace, 16))
+    return fail(AWQ_ERR_WORKSPACE, "workspace must be 16-byte aligned");
   s->offsets = offsets;
   s->order = order;
   s->place = place;

@@ -36,30 +36,42 @@ __device__ __forceinline__ int wave_sums(int x) {
   return x;
 }
 
-// The rows' tiles of `most` rows, expert by expert, and last those of rows that no expert has: a lane
-// counts a run of experts.
+// The rows' tiles of `most` rows, expert by expert, and last those of rows that no expert has.  A lane
+// counts a run of experts; of up to 255 it holds their offsets, so that finding a tile waits for
+// memory once.
 struct Tiles {
+  static constexpr int kHeld = 4;
   const LinearArgs& a;
   int most, each, mine, upto, all;     // all: tiles
+  int bound[kHeld + 1];
 
-  __device__ __forceinline__ void rows_of(int e, int& lo, int& hi) const {
-    const int total = (int)a.rows;
-    lo = e <= a.experts ? a.offsets[e] : total;
-    hi = e < a.experts ? a.offsets[e + 1] : total;
-    lo = lo < 0 ? 0 : lo > total ? total : lo;
-    hi = hi < lo ? lo : hi > total ? total : hi;
+  // Where expert e's rows begin; e = experts: where the others' do.
+  __device__ __forceinline__ int begin(int e) const {
+    const int total = (int)a.rows, o = e <= a.experts ? a.offsets[e] : total;
+    return o < 0 ? 0 : o > total ? total : o;
   }
+  __device__ __forceinline__ int tiles_in(int lo, int hi) const { return hi > lo ? (hi - lo + most - 1) / most : 0; }
+
   __device__ __forceinline__ Tiles(const LinearArgs& args, int most_rows) : a(args), most(most_rows) {
     if (!a.offsets) {
       all = (int)((a.rows + most - 1) / most);
       return;
     }
     each = a.experts / 64 + 1;         // experts + 1 of them in all
+    const int e0 = (int)(threadIdx.x & 63) * each;
     mine = 0;
-    for (int i = 0; i < each; ++i) {
-      int lo, hi;
-      rows_of((int)(threadIdx.x & 63) * each + i, lo, hi);
-      mine += (hi - lo + most - 1) / most;
+    if (each <= kHeld) {
+#pragma unroll
+      for (int i = 0; i <= kHeld; ++i) bound[i] = begin(e0 + (i < each ? i : each));
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) mine += tiles_in(bound[i], bound[i + 1]);
+    } else {
+      int lo = begin(e0);
+      for (int i = 0; i < each; ++i) {
+        const int hi = begin(e0 + i + 1);
+        mine += tiles_in(lo, hi);
+        lo = hi;
+      }
     }
     upto = wave_sums(mine);
     all = __builtin_amdgcn_readlane(upto, 63);
@@ -75,19 +87,38 @@ struct Tiles {
       return t;
     }
     const int l = __builtin_ctzll(__ballot(want < upto));
-    want -= __builtin_amdgcn_readlane(upto - mine, l);
-    for (int e = l * each;; ++e) {
-      int lo, hi;
-      rows_of(e, lo, hi);
-      const int tiles = (hi - lo + most - 1) / most;
-      if (want < tiles || e >= a.experts) {
-        t.row0 = lo + (int64_t)want * most;
-        t.rows = hi - (int)t.row0 < most ? hi - (int)t.row0 : most;
-        t.expert = e;
-        return t;
+    int lo = 0, hi = 0, e = 0, w = want - (upto - mine);
+    if (each <= kHeld) {
+      int at = 0;                        // tiles before the run's expert i
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int n = tiles_in(bound[i], bound[i + 1]);
+        if (w >= at && w < at + n) {
+          e = i;
+          lo = bound[i] + (w - at) * most;
+          hi = bound[i + 1];
+        }
+        at += n;
       }
-      want -= tiles;
+      t.row0 = __builtin_amdgcn_readlane(lo, l);
+      hi = __builtin_amdgcn_readlane(hi, l);
+      t.expert = l * each + __builtin_amdgcn_readlane(e, l);
+    } else {
+      w = __builtin_amdgcn_readlane(w, l);
+      e = l * each;
+      lo = begin(e);
+      hi = begin(e + 1);
+      for (int n = tiles_in(lo, hi); w >= n && e < a.experts; n = tiles_in(lo, hi)) {
+        w -= n;
+        ++e;
+        lo = hi;
+        hi = begin(e + 1);
+      }
+      t.row0 = lo + w * most;
+      t.expert = e;
     }
+    t.rows = hi - (int)t.row0 < most ? hi - (int)t.row0 : most;
+    return t;
   }
 };
 
