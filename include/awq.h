@@ -678,8 +678,13 @@ awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t 
  *   bias fp32 [experts, N] or NULL; residual [rows, outputs] of out_dtype with a row
  *   stride, or NULL; out [rows, outputs] dense of out_dtype (any), outputs = N, or
  *   N / 2 where gated.
- *   Products x (c - z) are exact and summed in fp32; steps must be finite, those of
- *   a row within a factor of 2^100 of each other.  The result is rounded once.
+ *   Products x (c - z) are exact and summed in fp32, where K is long and rows are few in
+ *   parts that are added in their order; steps must be finite, those of
+ *   a row within a factor of 2^100 of each other, and sums of x (c - z) within fp32's
+ *   range.  bf16 rows of large calls (more than 256 rows an expert, or some 256 tiles of 128 rows by
+ *   256 columns) are taken to fp16 first, scaled by a power of two for each row: an
+ *   element keeps all its bits down to 2^-16 of its row's largest, and is within 2^-25 of that largest
+ *   below.  The result is rounded once.
  *   workspace: awq_lowbit_linear_workspace_size(...) bytes, 256-byte aligned, may be NULL
  *   when that is 0.
  * ------------------------------------------------------------------------ */
@@ -717,7 +722,7 @@ awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows,
  * epilogue), awq_gemm_w8a8_store (the INT8 GEMM writing y).  awq_rope_table, awq_rope,
  * awq_kv_append, awq_kv_read, awq_kv_attention, awq_kv_attention_join.  awq_moe_sort,
  * awq_moe_route, awq_moe_route_grad, awq_moe_gather, awq_moe_combine, awq_moe_combine_grad,
- * awq_lowbit_linear.
+ * awq_lowbit_linear, awq_lowbit_linear_scale, awq_lowbit_linear_join.
  * awq_profile_reset() drops the records.  Thread-safe.
  * ------------------------------------------------------------------------ */
 awq_status_t awq_profile_enable(int enable);

@@ -1321,7 +1321,13 @@ size_t awq_lowbit_linear_workspace_size(awq_dtype_t dtype, int64_t rows, int64_t
   a.K = K;
   a.experts = (int)experts;
   a.gated = (flags & AWQ_LINEAR_GATED) != 0;
-  return align_up(awq::linear_ws_bytes(a, dtype));
+  a.grouped = true;
+  size_t need = awq::linear_ws_bytes(a, dtype);
+  if (experts == 1) {            // with offsets or without
+    a.grouped = false;
+    need = std::max(need, awq::linear_ws_bytes(a, dtype));
+  }
+  return align_up(need);
 }
 
 awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows, int64_t K,
@@ -1398,9 +1404,10 @@ awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows,
   a.act = act;
   a.gated = gated;
   a.out_type = (int)out_dtype;
+  a.grouped = offsets != nullptr;
   if (awq::linear_threads(a) > (int64_t)UINT32_MAX)
     return fail(AWQ_ERR_UNSUPPORTED, "too many rows and columns for one call");
-  const size_t need = awq_lowbit_linear_workspace_size(dtype, rows, x_rows, N, K, experts, flags);
+  const size_t need = align_up(awq::linear_ws_bytes(a, dtype));
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(AWQ_ERR_WORKSPACE, "lowbit_linear needs %zu workspace bytes, got %zu", need,
                 workspace ? workspace_bytes : (size_t)0);

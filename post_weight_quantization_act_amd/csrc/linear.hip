@@ -5,12 +5,13 @@
 // (j R + n) bits, R the rows of all experts; (step, z) of group g at g R + n.  Codes become the
 // exact integers c - z in the activations' type, in the registers that the matrix
 // instructions read them from; products are exact and sums are held in fp32, by group, scaled by
-// the group's step.
+// the group's step.  Two kernels: linear_few_kernel for few rows, which waits for the weights alone, and
+// linear_tile_kernel, bound by the weights up to some 32 rows an expert and by the matrix
+// instructions from some 128 on.
 #ifndef AWQ_LINEAR_BITS
 #error "compiled once for each width of codes"
 #endif
 
-#include "kv.h"
 #include "linear.h"
 
 namespace awq {
@@ -145,77 +146,6 @@ __device__ __forceinline__ int64_t source(const LinearArgs& a, int64_t r) {
   return s < a.x_rows ? s : 0;
 }
 
-// ---- epilogue ------------------------------------------------------------------------------
-// exp, quotients and tanh from the hardware's exp2 and reciprocal (an ulp each): relative error
-// a few 2^-24 and that of the exponent's own rounding, |v| 2^-24.  tanh's form is v / (1 + exp(-2 u)).
-__device__ __forceinline__ float over_one_plus_exp(float v, float minus) {
-  return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(minus * -1.44269504088896341f));
-}
-template <int ACT>
-__device__ __forceinline__ float activate(float v) {
-  if constexpr (ACT == AWQ_ACT_RELU) return v < 0.0f ? 0.0f : v;
-  else if constexpr (ACT == AWQ_ACT_SILU) return over_one_plus_exp(v, v);
-  else if constexpr (ACT == AWQ_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  else if constexpr (ACT == AWQ_ACT_GELU_TANH)
-    return over_one_plus_exp(v, 1.5957691216057307f * fmaf(0.044715f * v, v * v, v));
-  else return v;
-}
-
-__device__ __forceinline__ float load_as(const void* p, int64_t i, int type) {
-  if (type == AWQ_F32) return ((const float*)p)[i];
-  return type == AWQ_F16 ? (float)((const _Float16*)p)[i] : (float)((const __bf16*)p)[i];
-}
-__device__ __forceinline__ void store_as(void* p, int64_t i, int type, float v) {
-  if (type == AWQ_F32) ((float*)p)[i] = v;
-  else if (type == AWQ_F16) ((_Float16*)p)[i] = (_Float16)v;
-  else ((__bf16*)p)[i] = (__bf16)v;
-}
-
-// N outputs of a row from column n on, from their sums, gates and ups where gated.
-template <int ACT, int N>
-__device__ __forceinline__ void finish_act(const LinearArgs& a, int expert, int64_t row, int n, float (&v)[N],
-                                           float (&up)[N]) {
-  const int outputs = a.gated ? a.N / 2 : a.N;
-  if (a.bias) {
-    const float* b = a.bias + (int64_t)expert * a.N + n;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] += b[i];
-      if (a.gated) up[i] += b[outputs + i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = activate<ACT>(v[i]);
-    if (a.gated) v[i] *= up[i];
-  }
-  if (a.residual) {
-    const int64_t at = row * a.residual_stride + n;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += load_as(a.residual, at + i, a.out_type);
-  }
-  const int64_t at = row * outputs + n;
-  if constexpr (N == 1) {
-    store_as(a.out, at, a.out_type, v[0]);
-  } else if (a.out_type == AWQ_F32) {
-    store_run<N>((float*)a.out + at, v);
-  } else if (a.out_type == AWQ_F16) {
-    store_run<N>((_Float16*)a.out + at, v);
-  } else {
-    store_run<N>((__bf16*)a.out + at, v);
-  }
-}
-template <int N>
-__device__ __forceinline__ void finish(const LinearArgs& a, int expert, int64_t row, int n, float (&v)[N], float (&up)[N]) {
-  switch (a.act) {
-    case AWQ_ACT_RELU: return finish_act<AWQ_ACT_RELU>(a, expert, row, n, v, up);
-    case AWQ_ACT_SILU: return finish_act<AWQ_ACT_SILU>(a, expert, row, n, v, up);
-    case AWQ_ACT_GELU: return finish_act<AWQ_ACT_GELU>(a, expert, row, n, v, up);
-    case AWQ_ACT_GELU_TANH: return finish_act<AWQ_ACT_GELU_TANH>(a, expert, row, n, v, up);
-    default: return finish_act<AWQ_ACT_NONE>(a, expert, row, n, v, up);
-  }
-}
-
 // ---- codes to values ------------------------------------------------------------------------
 // Eight consecutive ones, the Q-th of a run's words, as a fragment.
 template <class S, int NW, int Q>
@@ -265,70 +195,6 @@ __device__ __forceinline__ i32x4 eight_f16(const uint32_t (&w)[NW], bool live, h
   return i32x4{one(two_codes<4 * Q>(w)), one(two_codes<4 * Q + 1>(w)), one(two_codes<4 * Q + 2>(w)),
                one(two_codes<4 * Q + 3>(w))};
 }
-// Where the activations' order is the kernel's own, a chunk's 32 codes are taken in pairs that one
-// AND finds: in a window of the chunk's bits from o on, code a lies within bits 0 .. 9, code b within
-// bits 16 .. 25, both subnormals of their halves, and each half has its own factor in the
-// multiply-add.  Two instructions a pair, and one for each window.  32 codes of 4 bits: 36, of 3 bits:
-// 39 (64 in their order), of 2 bits: 34, of 5 to 7 bits: 47.
-struct Pairs {
-  int a[16], b[16], o[16];
-  int pos[32];                  // where code i's activation goes
-};
-constexpr Pairs pairs_of(int bits) {
-  Pairs p = {};
-  int n = 0;
-  for (int a0 = 0; a0 < 32;) {
-    // a run of `apart` codes with the next as many
-    const int apart = bits == 2 ? 8 : bits == 3 ? (a0 < 24 ? 6 : 4) : bits == 4 ? 4 : bits == 5 ? (a0 < 24 ? 3 : 4) : 2;
-    const int run = 32 - a0 < 2 * apart ? (32 - a0) / 2 : apart;
-    for (int i = 0; i < run; ++i) {
-      p.a[n] = a0 + i;
-      p.b[n] = a0 + run + i;
-      ++n;
-    }
-    a0 += 2 * run;
-  }
-  for (int i = 0; i < 16; ++i) {
-    const int at = bits * p.a[i], d = bits * (p.b[i] - p.a[i]);
-    const int least = d < 16 ? 16 - d : 0, most = 10 - bits < 26 - bits - d ? 10 - bits : 26 - bits - d;
-    // the window before, if it holds both; else one that begins as late as it may
-    const int before = i > 0 ? at - p.o[i - 1] : -1;
-    p.o[i] = before >= least && before <= most ? p.o[i - 1] : at - least;
-    p.pos[p.a[i]] = 2 * i;
-    p.pos[p.b[i]] = 2 * i + 1;
-  }
-  return p;
-}
-constexpr Pairs kPairs = pairs_of(BITS);
-constexpr bool pairs_fit() {
-  for (int i = 0; i < 16; ++i) {
-    const int s = BITS * kPairs.a[i] - kPairs.o[i], t = BITS * kPairs.b[i] - kPairs.o[i];
-    if (s < 0 || s + BITS > 10 || t < 16 || t + BITS > 26) return false;
-  }
-  return true;
-}
-static_assert(pairs_fit());
-
-template <int P>
-__device__ __forceinline__ int pair_of_window(const uint32_t (&w)[BITS], half2v minus) {
-  constexpr int o = kPairs.o[P], s = BITS * kPairs.a[P] - o, t = BITS * kPairs.b[P] - o - 16;
-  constexpr int wi = o < 0 ? 0 : o >> 5, sh = o < 0 ? 0 : o & 31;
-  constexpr uint32_t mask = (1u << BITS) - 1u;
-  uint32_t v;
-  if constexpr (o < 0) v = w[0] << -o;
-  else if constexpr (sh == 0) v = w[wi];
-  else if constexpr (sh + 26 > 32 && wi + 1 < BITS) v = __builtin_amdgcn_alignbit(w[wi + 1], w[wi], sh);
-  else v = w[wi] >> sh;
-  const half2v by = {(_Float16)(float)(1 << (14 - s)), (_Float16)(float)(1 << (14 - t))};
-  return (int)__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(
-                                               __builtin_bit_cast(half2v, v & (mask << s | mask << (16 + t))), by, minus));
-}
-template <int Q>
-__device__ __forceinline__ i32x4 eight_paired(const uint32_t (&w)[BITS], half2v minus) {
-  return i32x4{pair_of_window<4 * Q>(w, minus), pair_of_window<4 * Q + 1>(w, minus), pair_of_window<4 * Q + 2>(w, minus),
-               pair_of_window<4 * Q + 3>(w, minus)};
-}
-
 __device__ __forceinline__ half2v minus_f16(float z) {
   const _Float16 n = (_Float16)(z * (-1.0f / kHalfScale));
   return half2v{n, n};
@@ -368,7 +234,10 @@ __device__ __forceinline__ void load_words(Buffer b, uint32_t voff, uint32_t sof
 // A workgroup takes WT tiles of 16 weight rows (gated: a tile of gates and the same of ups) and
 // 16 TT output rows; its waves share the columns of K, 128 at a time, and add up in LDS.  Lane
 // 16 g + r holds weight row r and the 32 codes of chunk g of the four: one load of `bits` words;
-// instruction i of four multiplies the chunks' codes 8 i .. 8 i + 7.
+// instruction i of four multiplies the chunks' codes 8 i .. 8 i + 7.  One row of 8192 to 28672
+// columns, 3 bits: 36 us, 2.8 TB/s; bound by unpacking.  8 rows for 8 of 128 experts, 1536 x 2048, 4
+// bits: 11 us, of which the weights are 2.7; bound by its chain of loads (offsets, codes, the
+// rows' places, the rows).
 template <class S, int TT, int WT>
 __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int col_tiles) {
   extern __shared__ __attribute__((aligned(16))) f32x4 red[];      // [waves][WT][TT][64]
@@ -396,20 +265,14 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
     wrow[w] = (int64_t)t.expert * a.N + n + (a.gated && w ? outputs : 0);
   }
   const S* x[TT];
-#pragma unroll
-  for (int i = 0; i < TT; ++i) {
-    const int m = 16 * i + r;
-    x[i] = m < t.rows ? (const S*)a.x + source(a, t.row0 + m) * a.stride : nullptr;
-  }
   struct Step {
     uint32_t w[WT][BITS];
     float2 m[WT];
     i32x4 x[TT][4];
   };
-  auto load = [&](int s, Step& b) __attribute__((always_inline)) {
+  auto load_codes = [&](int s, Step& b) __attribute__((always_inline)) {
     const int j = 4 * s + g;
-    const bool in = j < chunks;
-    const int64_t jj = in ? j : chunks - 1;
+    const int64_t jj = j < chunks ? j : chunks - 1;
 #pragma unroll
     for (int w = 0; w < WT; ++w) {
       const uint32_t* p = a.codes + (jj * a.R + wrow[w]) * BITS;
@@ -417,12 +280,15 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
       for (int i = 0; i < BITS; ++i) b.w[w][i] = p[i];
       b.m[w] = a.meta[(jj >> a.lg_cpg) * a.R + wrow[w]];
     }
+  };
+  auto load_x = [&](int s, Step& b) __attribute__((always_inline)) {
+    const int64_t j = 4 * s + g;
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         b.x[i][q] = i32x4{0, 0, 0, 0};
-        if (x[i] && in) b.x[i][q] = *(const i32x4*)(x[i] + 32 * jj + 8 * q);
+        if (x[i] && j < chunks) b.x[i][q] = *(const i32x4*)(x[i] + 32 * j + 8 * q);
       }
   };
   const int apart = a.lg_cpg == 0 ? 4 : a.lg_cpg == 1 ? 2 : 1;   // groups of a step's 128 columns
@@ -465,9 +331,17 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
   };
   Step cur, next;
   int s = wave;
-  if (s < steps) load(s, cur);
+  // codes before the rows: those wait for their places
+  if (s < steps) load_codes(s, cur);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    const int m = 16 * i + r;
+    x[i] = m < t.rows ? (const S*)a.x + source(a, t.row0 + m) * a.stride : nullptr;
+  }
+  if (s < steps) load_x(s, cur);
   for (; s < steps; s += waves) {
-    if (s + waves < steps) load(s + waves, next);
+    if (s + waves < steps) load_codes(s + waves, next), load_x(s + waves, next);
     multiply(cur);
     cur = next;
   }
@@ -492,225 +366,6 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
   }
 }
 
-// Few rows and K columns that fit LDS: the rows come there once, as fp16 (bf16 ones scaled by a power
-// of two for each row, as scale_rows_kernel does).  The workgroup's eight waves are teams of `team`:
-// a team takes a column tile of 32 weight rows (gated: 16 gates and 16 ups), its waves 128 columns of
-// K each in turn, and adds up in LDS; then the next tile, whose first steps are on their way by then.
-constexpr int kRowPad = 8;         // elements between rows in LDS: 16 rows' parts lie in different banks
-constexpr int kRowWaves = 8;
-
-template <int TT>
-__global__ __launch_bounds__(64 * kRowWaves, TT == 1 ? 4 : 2) void linear_rows_kernel(LinearArgs a, LinearPlan p, int bf16) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  constexpr int kAhead = BITS <= 4 ? 3 : 2;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), member = wave & (p.team - 1), mate0 = wave - member;
-  const int r = lane & 15, g = lane >> 4;
-  const int outputs = a.gated ? a.N / 2 : a.N, wide = a.gated ? 16 : 32;   // outputs of a column tile
-  Tiles tiles(a, p.most);
-  const int want = (int)(blockIdx.x / (uint32_t)p.col_groups);
-  if (want >= tiles.all) return;
-  const Tile t = tiles.at(want);
-  const int teams = kRowWaves / p.team, stride = p.col_groups * teams;
-  const int col0 = (int)(blockIdx.x % (uint32_t)p.col_groups) * teams;
-  if (t.expert == a.experts) {
-    for (int c0 = col0; c0 < p.col_tiles; c0 += stride)
-      for (int e = tid; e < t.rows * wide * teams; e += 64 * kRowWaves) {
-        const int n = c0 * wide + e % (wide * teams);
-        if (n < outputs) store_as(a.out, (t.row0 + e / (wide * teams)) * outputs + n, a.out_type, 0.0f);
-      }
-    return;
-  }
-  const int chunks = (int)(a.K / 32), steps = (chunks + 3) / 4;
-  const int mine = member < steps ? (steps - 1 - member) / p.team + 1 : 0;    // of a tile's steps
-  struct Step {
-    uint32_t w[2][BITS];
-    float2 m[2];
-  };
-  const uint32_t R = (uint32_t)a.R;
-  const Buffer rc = buffer_of(a.codes, (uint32_t)chunks * R * BITS * 4);
-  const Buffer rm = buffer_of(a.meta, (uint32_t)(chunks >> a.lg_cpg) * R * 8);
-  // offsets of this lane's row and chunk; a chunk past the last reads as 0, and its activations are 0
-  const uint32_t gm = (uint32_t)g >> a.lg_cpg;
-  uint32_t woff[2], moff[2];
-  auto aim = [&](int col) __attribute__((always_inline)) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      int n = col * wide + (a.gated ? 0 : 16 * w) + r;
-      n = n < outputs ? n : outputs - 1;
-      const uint32_t row = (uint32_t)t.expert * a.N + n + (a.gated && w ? outputs : 0);
-      woff[w] = (g * R + row) * (BITS * 4);
-      moff[w] = (gm * R + row) * 8;
-    }
-  };
-  auto load = [&](int i, Step& b) __attribute__((always_inline)) {
-    const uint32_t s = member + i * p.team;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      load_words<BITS>(rc, woff[w], 4 * s * R * (BITS * 4), b.w[w]);
-      const auto v = __builtin_amdgcn_raw_buffer_load_b64(rm, moff[w], (4 * s >> a.lg_cpg) * R * 8, 0);
-      b.m[w] = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-    }
-  };
-  Step ring[kAhead];
-  auto prime = [&](int col) __attribute__((always_inline)) {
-    aim(col);
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-      if (d < mine) load(d, ring[d]);
-  };
-  if (col0 + wave / p.team < p.col_tiles) prime(col0 + wave / p.team);
-
-  // the rows
-  const int pitch = (int)a.K + kRowPad;
-  _Float16* xs = (_Float16*)lds;
-  f32x4* red = (f32x4*)(lds + (size_t)p.most * pitch * 2);        // [2][waves][2][TT][64]
-  __shared__ uint32_t top[16 * TT];
-  const int parts = ((int)a.K + 511) / 512, units = t.rows * parts;   // 512 elements: a wave's
-  constexpr int kHeld = 2;                                        // units that stay in registers
-  u16x8 held[kHeld];
-  auto fetch = [&](int u) __attribute__((always_inline)) {
-    const int m = u / parts, k = (u % parts) * 512 + 8 * lane;
-    return k < a.K ? *(const u16x8*)((const uint16_t*)a.x + source(a, t.row0 + m) * a.stride + k) : u16x8{};
-  };
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (wave + i * kRowWaves < units) held[i] = fetch(wave + i * kRowWaves);
-  auto each = [&](auto f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (wave + i * kRowWaves < units) f(wave + i * kRowWaves, held[i]);
-    for (int u = wave + kHeld * kRowWaves; u < units; u += kRowWaves) f(u, fetch(u));
-  };
-  if (bf16) {
-    if (tid < 16 * TT) top[tid] = 0;
-    __syncthreads();
-    each([&](int u, u16x8 v) __attribute__((always_inline)) {
-      uint32_t most = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t b = v[i] & 0x7fffu;
-        most = most > b ? most : b;
-      }
-      atomicMax(&top[u / parts], most);
-    });
-    __syncthreads();
-  }
-  auto exponent = [&](int m) __attribute__((always_inline)) {
-    const int e = (int)(top[m] >> 7) - 127;
-    return !bf16 || top[m] == 0 || top[m] >= 0x7f80u ? 0 : e < -126 ? -126 : e;
-  };
-  each([&](int u, u16x8 v) __attribute__((always_inline)) {
-    const int m = u / parts, k = (u % parts) * 512 + 8 * lane;
-    if (k >= a.K) return;
-    half8 y = __builtin_bit_cast(half8, v);
-    if (bf16) {
-      const int e = exponent(m);
-      const bf16x8 x = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = (_Float16)ldexpf((float)x[i], -e);
-    }
-    // in the order that the codes are taken: lane l of four holds codes 8 (l % 4) .. of a chunk
-    _Float16* to = xs + m * pitch + (k & ~31);
-#pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      if ((lane & 3) != l) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) to[kPairs.pos[8 * l + i]] = y[i];
-    }
-  });
-  __syncthreads();
-
-  const int apart = a.lg_cpg == 0 ? 4 : a.lg_cpg == 1 ? 2 : 1;    // groups of a step's 128 columns
-  f32x4 tot[2][TT];
-  const _Float16* xrow[TT];       // rows that are not there read the first; nobody reads their sums
-#pragma unroll
-  for (int i = 0; i < TT; ++i) xrow[i] = xs + (16 * i + r < t.rows ? 16 * i + r : 0) * pitch;
-  auto multiply = [&](int i, const Step& b) __attribute__((always_inline)) {
-    const int s = member + i * p.team, j = 4 * s + g;
-    const bool in = j < chunks;
-    i32x4 x[TT][4];
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        x[i][q] = *(const i32x4*)(xrow[i] + 32 * (in ? j : 0) + 8 * q);
-        if (4 * s + 4 > chunks) x[i][q] = in ? x[i][q] : i32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const half2v minus = minus_f16(b.m[w].y);
-      const i32x4 f[4] = {eight_paired<0>(b.w[w], minus), eight_paired<1>(b.w[w], minus), eight_paired<2>(b.w[w], minus),
-                          eight_paired<3>(b.w[w], minus)};
-      if (apart == 1) {
-#pragma unroll
-        for (int i = 0; i < TT; ++i) {
-          f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc = mfma16x32<_Float16>(x[i][q], f[q], acc);
-          tot[w][i] += acc * b.m[w].x;
-        }
-      } else {
-        // several groups in the step: one at a time, the other chunks' activations taken as 0
-        for (int part = 0; part < apart; ++part) {
-          const int g0 = part * (4 / apart);
-          const bool on = g >= g0 && g < g0 + 4 / apart;
-          const float d = __shfl(b.m[w].x, 16 * g0 + r);
-#pragma unroll
-          for (int i = 0; i < TT; ++i) {
-            f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc = mfma16x32<_Float16>(on ? x[i][q] : i32x4{0, 0, 0, 0}, f[q], acc);
-            tot[w][i] += acc * d;
-          }
-        }
-      }
-    }
-  };
-  int buf = 0;
-  for (int c0 = col0; c0 < p.col_tiles; c0 += stride, buf ^= 1) {
-    const int col = c0 + wave / p.team;
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int i = 0; i < TT; ++i) tot[w][i] = f32x4{0, 0, 0, 0};
-    if (col < p.col_tiles) {
-      for (int i0 = 0; i0 < mine; i0 += kAhead) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-          if (i0 + d >= mine) break;
-          multiply(i0 + d, ring[d]);
-          if (i0 + d + kAhead < mine) load(i0 + d + kAhead, ring[d]);
-        }
-      }
-      if (col + stride < p.col_tiles) prime(col + stride);
-    }
-    f32x4* sums = red + (buf * kRowWaves + mate0) * 2 * TT * 64;  // the team's
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int i = 0; i < TT; ++i) sums[((member * 2 + w) * TT + i) * 64 + lane] = tot[w][i];
-    if (p.team > 1) __syncthreads();
-    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    // lane l of a tile holds weight row l % 16 and output rows 4 (l / 16) .. + 3
-    auto sum = [&](int w, int m, int n) __attribute__((always_inline)) {
-      const float* q = (const float*)sums + (((w * TT + (m >> 4)) * 64 + n + 16 * ((m & 15) >> 2)) * 4 + (m & 3));
-      float v = 0.0f;
-      for (int k = 0; k < p.team; ++k) v += q[k * 2 * TT * 256];
-      return v;
-    };
-    if (col < p.col_tiles) {
-      for (int e = member * 64 + lane; e < t.rows * wide; e += p.team * 64) {
-        const int n = e % wide, m = e / wide;
-        if (col * wide + n >= outputs) continue;
-        const float by = ldexpf(kHalfScale, exponent(m));
-        float v[1] = {by * sum(a.gated ? 0 : n >> 4, m, n & 15)}, up[1] = {a.gated ? by * sum(1, m, n) : 0.0f};
-        finish(a, t.expert, t.row0 + m, col * wide + n, v, up);
-      }
-    }
-  }
-}
-
 // ---- many rows -----------------------------------------------------------------------------------
 // A workgroup takes 32 MT output rows and 256 weight rows, a wave all the output rows and 64 weight
 // rows (gated: 32 gates and the same ups).  Activations go through LDS, 128 columns at a time, two
@@ -720,14 +375,24 @@ __global__ __launch_bounds__(64 * kRowWaves, TT == 1 ? 4 : 2) void linear_rows_k
 // The sums are in units of the group's step U: where the next group begins they are multiplied by
 // U / U', a step of 0 leaves the unit as it is and its codes count as 0.
 // WIDE: groups of 128 columns and more, so a step lies in one.
+// splits > 1: a workgroup takes the steps of one part of K and leaves fp32 sums to a kernel that joins them.
+// 4 bits: 2047 x 4096 x 11008 in fp16 190 us, 0.97 PFLOP/s; 24570 rows for 64 experts, 2816 x 2048, 345
+// us, 0.82 PFLOP/s; a library's product of such a size reaches 1.17 to 1.23 here, and this loop by
+// itself 1.13.  The rest are rows that the last tile of an expert lacks, and the first loads and last
+// stores of a round of workgroups.  488 rows for 128 experts, 1536 x 2048: 56 us, 3.8 TB/s; each step
+// waits for its codes, and a ring of three steps in flight gained nothing.
+// Workgroups of a compute unit: as many as their registers allow without spills.
+constexpr int tile_groups(int mt, bool wide) {
+  return mt == 1 ? (BITS <= 4 && wide ? 4 : 3) : mt == 2 && BITS <= 4 && wide ? 3 : 2;
+}
 template <class S, int MT, int KS, bool WIDE>
-__global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(LinearArgs a, int col_tiles) {
+__global__ __launch_bounds__(256 * KS, KS == 2 ? 1 : tile_groups(MT, WIDE)) void linear_tile_kernel(LinearArgs a, LinearPlan p) {
   constexpr bool kF16 = sizeof(S) == 2 && std::is_same<S, _Float16>::value;
   constexpr int NW = (BITS + 1) / 2, M = WIDE ? 1 : 4;
   constexpr int kRows = 32 * MT, kPer = 2 * MT;                  // transfers of a wave and step
   constexpr int kPitch = 68;     // floats of a row in the epilogue
-  __shared__ __attribute__((aligned(1024))) char xs[KS][2][kRows * 256];
-  static_assert(sizeof(xs) >= KS * 4 * 16 * kPitch * 4);
+  constexpr int kBuffer = kRows * 256, kTurns = KS * 4 * 16 * kPitch * 4;
+  __shared__ __attribute__((aligned(1024))) char xs[KS * 2 * kBuffer > kTurns ? KS * 2 * kBuffer : kTurns];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, set = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
   const int r = lane & 31, h = lane >> 5;
@@ -736,11 +401,13 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(
   // Two workgroups share a compute unit.  Where more follow, the second of each pair starts 4 us
   // later, so that one multiplies while the other waits for its first rows or stores its last
   // (24570 rows for 64 experts, 2816 x 2048, 4 bits: 362 us without, 337 with 4, 341 with 8)
-  if (KS == 1 && gridDim.x > 512 && blockIdx.x >= 256 && blockIdx.x < 512)
+  if (MT == 4 && KS == 1 && gridDim.x > 512 && blockIdx.x >= 256 && blockIdx.x < 512)
     for (int i = 0; i < 4; ++i) __builtin_amdgcn_s_sleep(32);
   Tiles tiles(a, kRows);
-  if (blockIdx.x >= (uint32_t)tiles.all * (uint32_t)col_tiles) return;
-  const Place at = place_of(blockIdx.x, col_tiles, tiles.all);
+  const uint32_t part = blockIdx.x % (uint32_t)p.splits, id = blockIdx.x / (uint32_t)p.splits;
+  if (id >= (uint32_t)tiles.all * (uint32_t)p.col_tiles) return;
+  const Place at = p.splits > 1 ? Place{(int)(id % (uint32_t)tiles.all), (int)(id / (uint32_t)tiles.all)}
+                                : place_of(id, p.col_tiles, tiles.all);
   const int first = at.col * 4 * wide, n0 = first + wave * wide;
   const Tile t = tiles.at(at.row);
   if (t.expert == a.experts) {
@@ -749,7 +416,8 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(
       if (first + e % span < outputs) store_as(a.out, (t.row0 + e / span) * outputs + first + e % span, a.out_type, 0.0f);
     return;
   }
-  const int chunks = (int)(a.K / 32), steps = (chunks + 3) / 4, cmask = (1 << a.lg_cpg) - 1;
+  const int chunks = (int)(a.K / 32), cmask = (1 << a.lg_cpg) - 1, step0 = (int)part * p.per;
+  const int steps = step0 + p.per < (chunks + 3) / 4 ? step0 + p.per : (chunks + 3) / 4;    // where this part ends
   const uint32_t R = (uint32_t)a.R;
   uint32_t woff[2], moff[2];
   const int qw = (16 * h * BITS) >> 5, qoff = (16 * h * BITS) & 31;
@@ -766,18 +434,18 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(
   // activations: transfer q of a step brings rows 4 q .. 4 q + 3, 16-byte part p of row m from
   // part p ^ (m % 16); rows past the last are the first again
   const i32x4 rx = byte_range(a.x, (uint32_t)(((a.x_rows - 1) * a.stride + a.K) * 2));
-  const uint32_t base = (uint32_t)(uintptr_t)&xs[set][0][0];
+  const uint32_t base = (uint32_t)(uintptr_t)xs + set * 2 * kBuffer;
   uint32_t xoff[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int m = 4 * (wave * kPer + i) + (lane >> 4);
     const int64_t row = source(a, t.row0 + (m < t.rows ? m : 0));
-    xoff[i] = (uint32_t)((row * a.stride + 8 * ((lane & 15) ^ (m & 15))) * 2) + 256 * set;
+    xoff[i] = (uint32_t)((row * a.stride + 8 * ((lane & 15) ^ (m & 15))) * 2) + 256 * (step0 + set);
   }
   auto fetch_x = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      to_lds16(rx, base + buf * (kRows * 256) + (wave * kPer + i) * 1024, xoff[i]);
+      to_lds16(rx, base + buf * kBuffer + (wave * kPer + i) * 1024, xoff[i]);
       xoff[i] += 256 * KS;
     }
   };
@@ -872,17 +540,17 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(
         fetch_x(buf ^ 1);
         fetch_codes(s + KS, next);
       }
-      if (s < steps) multiply(blocks, s, cur, xs[set][buf]);
+      if (s < steps) multiply(blocks, s, cur, xs + (set * 2 + buf) * kBuffer);
       vm_wait<0>();
       __syncthreads();
     };
-    if (set < steps) {
+    if (step0 + set < steps) {
       fetch_x(0);
-      fetch_codes(set, one);
+      fetch_codes(step0 + set, one);
     }
     vm_wait<0>();
     __syncthreads();
-    for (int s = 0; s < steps; s += 2 * KS) {
+    for (int s = step0; s < steps; s += 2 * KS) {
       step(s + set, one, two, 0);
       if (s + KS < steps) step(s + KS + set, two, one, 1);
     }
@@ -896,7 +564,7 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(
   }
   // Lane l holds weight row l % 32 and output rows 8 (e / 4) + 4 (l / 32) + e % 4.  Sixteen rows at
   // a time go through LDS, from where a lane takes four columns of a row: 16 lanes a row (gated: 8).
-  float* turn = (float*)&xs[0][0][0] + wave * 16 * kPitch;
+  float* turn = (float*)xs + wave * 16 * kPitch;
   const int span = a.gated ? 8 : 16, col = 4 * (lane % span);
   // a wave's LDS operations are in order; two sets wait for each other
   auto meet = [&]() __attribute__((always_inline)) {
@@ -933,7 +601,19 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(
         v *= by;
         up *= by;
       }
-      if (n0 + col + 4 <= outputs) {
+      if (p.splits > 1) {
+        float* to = p.partial + ((int64_t)part * a.rows + row) * a.N + n0 + col;
+        if (n0 + col + 4 <= outputs) {
+          const float x[4] = {v[0], v[1], v[2], v[3]}, y[4] = {up[0], up[1], up[2], up[3]};
+          store_run<4>(to, x);
+          if (a.gated) store_run<4>(to + outputs, y);
+        } else {
+          for (int c = 0; c < outputs - n0 - col; ++c) {
+            to[c] = c == 0 ? v[0] : c == 1 ? v[1] : v[2];
+            if (a.gated) to[outputs + c] = c == 0 ? up[0] : c == 1 ? up[1] : up[2];
+          }
+        }
+      } else if (n0 + col + 4 <= outputs) {
         float x[4] = {v[0], v[1], v[2], v[3]}, y[4] = {up[0], up[1], up[2], up[3]};
         finish(a, t.expert, row, n0 + col, x, y);
       } else {
@@ -949,9 +629,11 @@ __global__ __launch_bounds__(256 * KS, KS == 1 ? 2 : 1) void linear_tile_kernel(
 
 template <class S, bool WIDE>
 void go_tiles(const LinearArgs& a, const LinearPlan& p, unsigned grid, hipStream_t st) {
-  if (p.blocks == 2) linear_tile_kernel<S, 2, 1, WIDE><<<grid, 256, 0, st>>>(a, p.col_tiles);
-  else if (p.waves == 4) linear_tile_kernel<S, 4, 1, WIDE><<<grid, 256, 0, st>>>(a, p.col_tiles);
-  else linear_tile_kernel<S, 4, 2, WIDE><<<grid, 512, 0, st>>>(a, p.col_tiles);
+  grid *= p.splits;
+  if (p.blocks == 1) linear_tile_kernel<S, 1, 1, WIDE><<<grid, 256, 0, st>>>(a, p);
+  else if (p.blocks == 2) linear_tile_kernel<S, 2, 1, WIDE><<<grid, 256, 0, st>>>(a, p);
+  else if (p.waves == 4) linear_tile_kernel<S, 4, 1, WIDE><<<grid, 256, 0, st>>>(a, p);
+  else linear_tile_kernel<S, 4, 2, WIDE><<<grid, 512, 0, st>>>(a, p);
 }
 
 template <class S>
@@ -962,23 +644,15 @@ void go(const LinearArgs& a, const LinearPlan& p, hipStream_t st) {
     else go_tiles<S, false>(a, p, grid, st);
     return;
   }
-  if (p.team > 0) {
-    const int bf16 = !std::is_same<S, _Float16>::value;
-    const unsigned blocks = (unsigned)(p.col_groups * p.row_tiles);
-    if (p.blocks == 1) linear_rows_kernel<1><<<blocks, 64 * kRowWaves, p.lds, st>>>(a, p, bf16);
-    else linear_rows_kernel<2><<<blocks, 64 * kRowWaves, p.lds, st>>>(a, p, bf16);
-    return;
-  }
   const size_t lds = (size_t)p.waves * 2 * p.blocks * 1024;
   if (p.blocks == 1) linear_few_kernel<S, 1, 2><<<grid, 64 * p.waves, lds, st>>>(a, p.col_tiles);
-  else if (p.blocks == 2) linear_few_kernel<S, 2, 2><<<grid, 64 * p.waves, lds, st>>>(a, p.col_tiles);
-  else linear_few_kernel<S, 4, 2><<<grid, 64 * p.waves, lds, st>>>(a, p.col_tiles);
+  else linear_few_kernel<S, 2, 2><<<grid, 64 * p.waves, lds, st>>>(a, p.col_tiles);
 }
 
 }  // namespace
 
 template <>
-hipError_t launch_linear_bits<BITS>(const LinearArgs& a, awq_dtype_t dt, const LinearPlan& p, void*, hipStream_t st) {
+hipError_t launch_linear_bits<BITS>(const LinearArgs& a, awq_dtype_t dt, const LinearPlan& p, hipStream_t st) {
   ProfScope prof("awq_lowbit_linear", st);
   if (dt == AWQ_F16) go<_Float16>(a, p, st);
   else go<__bf16>(a, p, st);

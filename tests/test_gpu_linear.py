@@ -136,7 +136,28 @@ DENSE = [   # rows, n, K, bits, group, kind, out, act, gated, bias, residual, pa
 ]
 
 
-@pytest.mark.parametrize("case", DENSE, ids=lambda c: "-".join(map(str, c)))
+LONG = [   # K in parts, joined: gated, odd widths, groups that end inside a part's last step
+    (33, 300, 4096, 4, 128, "bf16", "bf16", "none", False, True, True, 0),
+    (40, 258, 2080, 3, 32, "f16", "f32", "silu", True, True, True, 8),
+    (64, 101, 11008, 4, 256, "f16", "f16", "gelu", False, False, False, 0),
+    (65, 130, 3200, 5, 64, "bf16", "f32", "relu", True, False, False, 0),
+    (190, 514, 1056, 2, 32, "bf16", "f16", "none", False, False, True, 0),
+    (500, 37, 2176, 8, 128, "f16", "bf16", "gelu_tanh", False, True, False, 16),
+]
+
+LARGE = [   # tiles of 128 rows: 256 of them and fewer, more, more than two to a compute unit; few rows of many columns
+    (1000, 8100, 160, 4, 32, "bf16", "bf16", "none", False, False, False, 0),
+    (1000, 8100, 288, 4, 32, "f16", "f16", "silu", True, True, False, 0),
+    (900, 8192, 640, 2, 128, "f16", "f32", "none", False, False, True, 0),
+    (1030, 7300, 256, 4, 128, "bf16", "f32", "gelu", False, True, True, 8),
+    (2500, 6700, 128, 3, 128, "bf16", "f32", "silu", True, False, False, 0),
+    (2400, 7001, 64, 5, 64, "f16", "f16", "none", False, False, True, 0),
+    (3, 16500, 96, 3, 32, "bf16", "bf16", "gelu_tanh", False, True, False, 0),
+    (30, 12500, 64, 4, 64, "bf16", "f32", "none", False, False, False, 0),
+]
+
+
+@pytest.mark.parametrize("case", DENSE + LONG + LARGE, ids=lambda c: "-".join(map(str, c)))
 def test_one_projection(case):
     run(np.random.default_rng(case[0] * 31 + case[1]), *case)
 
@@ -173,6 +194,13 @@ EXPERTS = [   # T, k, of, count, lean, then as above without rows and pad
     (257, 4, 70, 65, 0, 40, 128, 2, 128, "bf16", "bf16", "none", False, False, False),
     (64, 1, 2, 2, 1.0, 258, 320, 8, 64, "f16", "f32", "silu", True, False, False),
     (900, 1, 130, 129, 0.3, 36, 64, 6, 32, "f16", "f32", "none", False, False, False),
+    (600, 4, 8, 8, 0.2, 1030, 96, 4, 32, "bf16", "bf16", "silu", True, False, False),
+    (600, 4, 8, 7, 0.2, 1100, 128, 3, 128, "bf16", "f32", "none", False, True, True),
+    (700, 2, 300, 260, 0, 24, 64, 4, 32, "bf16", "f32", "none", False, True, False),
+    (1500, 2, 1024, 1000, 0.1, 18, 32, 4, 32, "f16", "f16", "none", False, False, False),
+    (90, 1, 3, 1, 0, 300, 1056, 4, 32, "bf16", "bf16", "none", False, True, True),
+    (900, 1, 3, 1, 0.9, 4200, 64, 4, 64, "bf16", "f32", "relu", False, False, False),
+    (20, 2, 300, 280, 0, 40, 96, 7, 32, "f16", "bf16", "gelu", True, False, True),
 ]
 
 
@@ -225,6 +253,79 @@ def test_large_and_small_activations(rows):
     want = ref.experts_product(wide(x), p.W, [0, rows])
     off = bound(wide(x), p.W, [0, rows], None, 128, None, "none", False, want, None, "f32")
     assert (np.abs(wide(y) - want) <= off).all()
+
+
+def test_large_calls_take_rows_to_fp16():
+    """bf16 elements down to 2^-40 of their row's largest, rows far apart in size, one that is not finite: an
+    element is off by 2^-25 of its row's largest at most, beside the sums' errors."""
+    rng = np.random.default_rng(5)
+    p = Packed(rng, 1, 8100, 128, 4, 128)
+    x = rng.normal(size=(1000, 128)) * 2.0 ** rng.integers(-60, 60, size=(1000, 1)) * 2.0 ** rng.integers(-40, 1, size=(1000, 128))
+    x[3] = 0
+    x[4] = 2.0 ** -133           # the smallest there is
+    x[5, 0] = 2.0 ** 127
+    x = torch.from_numpy(x.astype(np.float32)).bfloat16().cuda()
+    y = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 128, out_dtype=torch.float32)
+    xn = wide(x)
+    want = ref.experts_product(xn, p.W, [0, 1000])
+    off = bound(xn, p.W, [0, 1000], None, 128, None, "none", False, want, None, "f32")
+    off = off + 1.02 * 2.0 ** -25 * np.abs(xn).max(1)[:, None] * np.abs(p.W[0]).sum(1)[None]
+    assert (np.abs(wide(y) - want) <= off).all()
+    assert (wide(y)[3] == 0).all()
+    bad = x.clone()
+    bad[7, 5], bad[8, 6] = float("inf"), float("nan")
+    z = awq.awq_lowbit_linear(bad, p.codes, p.meta, 4, 128, out_dtype=torch.float32)
+    assert not torch.isfinite(z[7:9]).any()
+    keep = torch.ones(1000, dtype=torch.bool, device="cuda")
+    keep[7:9] = False
+    assert torch.equal(z[keep], y[keep])
+
+
+def test_offsets_that_do_not_fit_their_rows():
+    """Lists that no sort makes: nothing outside the tensors is read or written."""
+    rng = np.random.default_rng(8)
+    p = Packed(rng, 4, 40, 64, 4, 32)
+    for T in (3, 300):
+        r = routed(rng, T, 2, 4, 4)
+        x = normal(rng, (T, 64), "f16")
+        for offsets in ([0, 0, 0, 0, 0], [0, -5, 10 ** 9, 7, 2], [5, 4, 3, 2, 1], [2 ** 31 - 1] * 5, [-(2 ** 31)] * 5):
+            r.offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+            r.order.copy_(torch.randint(-(2 ** 31), 2 ** 31 - 1, r.order.shape, dtype=torch.int32))
+            guard = torch.full((2 * T + 2, 40), 7.0, dtype=torch.float16, device="cuda")
+            awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32, routing=r, gather=True, out=guard[1:-1])
+            torch.cuda.synchronize()
+            assert (guard[0] == 7).all() and (guard[-1] == 7).all()
+
+
+@pytest.mark.parametrize("rows,n,K", [(48, 300, 4096), (1000, 8100, 64)])
+def test_own_workspace(rows, n, K):
+    rng = np.random.default_rng(rows)
+    p = Packed(rng, 1, n, K, 4, 64)
+    x = normal(rng, (rows, K), "bf16")
+    want = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64)
+    size = awq.awq_lowbit_linear_workspace_size(torch.bfloat16, rows, rows, n, K)
+    assert size > 0
+    space = torch.full((size + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert torch.equal(awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64, workspace=space[:size]), want)
+    assert (space[size:] == 0xA5).all()
+    for bad in (space[:size - 256], space[8:size + 8]):
+        with pytest.raises(awq.AwqError):
+            awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64, workspace=bad)
+
+
+def test_on_another_stream():
+    rng = np.random.default_rng(6)
+    p = Packed(rng, 1, 300, 4096, 4, 64)
+    x = normal(rng, (48, 4096), "f16")
+    want = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
 
 
 def test_as_the_other_packed_products():
