@@ -44,9 +44,10 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const __bf16* x, int64_
 // Whether bf16 activations of a large call are taken to fp16 first: unpacking takes half the
 // instructions then, 2 to 4% of a call, and the pass as many bytes again as x has.  From 4096
 // products for each element on (4095 tokens, 6 of 64 experts, 2816 x 2048, 4 bits: 353 us without,
-// 344 with; the same rows, sorted, 2048 x 1408: no gain).
+// 344 with; the same rows, sorted, 2048 x 1408: no gain).  They are dense then, and stay within a
+// buffer's 4 GiB where overlapping ones would not.
 bool scaled(const LinearArgs& a, awq_dtype_t dt, const LinearPlan& p) {
-  return dt == AWQ_BF16 && p.tiles && p.blocks == 4 && a.rows * a.N >= 4096 * a.x_rows;
+  return dt == AWQ_BF16 && p.tiles && p.blocks == 4 && a.rows * a.N >= 4096 * a.x_rows && a.x_rows * a.K < 1ll << 31;
 }
 
 // The parts' sums [splits][rows][N], added in their order, and the rest of the product.
