@@ -313,6 +313,49 @@ def test_own_workspace(rows, n, K):
             awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64, workspace=bad)
 
 
+@pytest.mark.parametrize("rows,n,K", [(9, 40, 256), (48, 300, 2048), (200, 70, 256), (1000, 8100, 64)])
+def test_one_row_for_all_and_onto_the_residual(rows, n, K):
+    """Rows of stride 0, and the residual's own memory for the result."""
+    rng = np.random.default_rng(rows + n)
+    p = Packed(rng, 1, n, K, 4, 64)
+    x, res = normal(rng, (1, K), "bf16"), normal(rng, (1, n), "bf16")
+    want = awq.awq_lowbit_linear(x.repeat(rows, 1), p.codes, p.meta, 4, 64, residual=res.repeat(rows, 1))
+    assert torch.equal(awq.awq_lowbit_linear(x.expand(rows, K), p.codes, p.meta, 4, 64, residual=res.expand(rows, n)), want)
+    stream = res.repeat(rows, 1)
+    awq.awq_lowbit_linear(x.expand(rows, K), p.codes, p.meta, 4, 64, residual=stream, out=stream)
+    assert torch.equal(stream, want)
+
+
+@pytest.mark.parametrize("rows,n,K", [(5, 200, 2048), (48, 300, 4096), (1000, 8100, 64)])
+def test_one_projection_captured_and_replayed(rows, n, K):
+    rng = np.random.default_rng(n)
+    p = Packed(rng, 1, n, K, 4, 64)
+    x = normal(rng, (rows, K), "bf16")
+    awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64, activation="gelu")
+    for i in range(4):
+        x.copy_(normal(rng, (rows, K), "bf16"))
+        graph.replay()
+        want = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64, activation="gelu")
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+
+
+def test_more_than_two_to_the_31_outputs():
+    rng = np.random.default_rng(9)
+    rows, n, K = 66001, 32768, 32
+    p = Packed(rng, 1, n, K, 4, 32)
+    x = normal(rng, (rows, K), "f16")
+    y = awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 32)
+    at = [0, 1, 65535, 65536, 65791, 65999, 66000]
+    want = wide(x[at]) @ p.W[0].T
+    off = bound(wide(x[at]), p.W, [0, len(at)], None, 32, None, "none", False, want, None, "f16")
+    assert (np.abs(wide(y[at]) - want) <= off).all()
+
+
 def test_on_another_stream():
     rng = np.random.default_rng(6)
     p = Packed(rng, 1, 300, 4096, 4, 64)

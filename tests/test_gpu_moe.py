@@ -284,6 +284,24 @@ def test_gradient_of_a_wider_output_and_of_a_sum():
     assert (wide(rows.grad) == 1).all()
 
 
+def test_more_than_two_to_the_31_elements():
+    """There and back: eight times each row, exactly, and the same for the gradients."""
+    T, k, C = 131081, 8, 2056
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    e = torch.rand((T, 16), generator=gen, device="cuda").topk(k).indices.int()
+    x = torch.randn((T, C), generator=gen, device="cuda").bfloat16()
+    r = awq.awq_moe_sort(e, 16)
+    rows = awq.awq_moe_gather(x, r)
+    y = awq.awq_moe_combine(rows, r)
+    assert torch.equal(y, x * 8)
+    drows, dweights = awq.awq_moe_combine_grad(y, r, rows=rows)
+    at = torch.tensor([0, 70000, T - 1], device="cuda")
+    assert torch.equal(drows[r.place[at].long()], y[at][:, None].expand(3, k, C))
+    want = (y[at].double() * x[at].double()).sum(-1)
+    # C products, exact in 48 bits, rounded to fp32 and added: C additions at most
+    assert ((dweights[at].double() - want[:, None]).abs() <= 1.01 * (C + 1) * 2.0 ** -24 * want[:, None]).all()
+
+
 def test_shared_residual_row_and_out():
     rng = np.random.default_rng(1)
     r, (offsets, _, place) = routed(rng, 5, 2, 6, 6)
