@@ -669,15 +669,15 @@ awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t 
  *   awq_lowbit_repack's layout: one projection [N, K], or, with offsets, the rows
  *   of `experts` projections one after another, repacked as one weight of
  *   experts * N rows.
- *   x [x_rows, K] of dtype (AWQ_F16 or AWQ_BF16; row stride in elements, a
- *   multiple of 8; 16-byte aligned).  Without offsets row r of the outputs is row r of
+ *   x [x_rows, K] of dtype (AWQ_F16 or AWQ_BF16; row stride in elements, for
+ *   more than one row a multiple of 8; 16-byte aligned).  Without offsets row r of the outputs is row r of
  *   x (x_rows = rows) and `experts` is 1.  With offsets [experts + 1] rows
  *   [offsets[e], offsets[e + 1]) are expert e's, rows past the last are zero; they
  *   take row r of x or, with order [rows] (awq_moe_sort's), row order[r] /
  *   per_token of x: the tokens' rows, without sorted copies of them.
  *   bias fp32 [experts, N] or NULL; residual [rows, outputs] of out_dtype with a row
  *   stride, or NULL; out [rows, outputs] dense of out_dtype (any), outputs = N, or
- *   N / 2 where gated.
+ *   N / 2 where gated; it may be the residual itself.
  *   Products x (c - z) are exact and summed in fp32, where K is long and rows are few in
  *   parts that are added in their order; steps must be finite, those of
  *   a row within a factor of 2^100 of each other, and sums of x (c - z) within fp32's

@@ -1356,7 +1356,7 @@ awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows,
   const bool gated = (flags & AWQ_LINEAR_GATED) != 0;
   if (gated && N % 2 != 0)
     return fail(AWQ_ERR_INVALID_ARG, "N=%lld gates and ups are not as many of each", (long long)N);
-  if (stride < 0 || stride % 8 != 0)
+  if (stride < 0 || (x_rows > 1 && stride % 8 != 0))
     return fail(AWQ_ERR_UNSUPPORTED, "x's row stride %lld must be a multiple of 8", (long long)stride);
   if (residual && residual_stride < 0) return fail(AWQ_ERR_INVALID_ARG, "negative row stride");
   if (!offsets && (experts != 1 || order || x_rows != rows))

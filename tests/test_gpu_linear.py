@@ -324,6 +324,8 @@ def test_one_row_for_all_and_onto_the_residual(rows, n, K):
     stream = res.repeat(rows, 1)
     awq.awq_lowbit_linear(x.expand(rows, K), p.codes, p.meta, 4, 64, residual=stream, out=stream)
     assert torch.equal(stream, want)
+    alone = x.view(K, 1).T          # one row, of stride 1
+    assert torch.equal(awq.awq_lowbit_linear(alone, p.codes, p.meta, 4, 64), awq.awq_lowbit_linear(x, p.codes, p.meta, 4, 64))
 
 
 @pytest.mark.parametrize("rows,n,K", [(5, 200, 2048), (48, 300, 4096), (1000, 8100, 64)])
