@@ -627,21 +627,25 @@ __global__ __launch_bounds__(256 * KS, KS == 2 ? 1 : tile_groups(MT, WIDE)) void
   }
 }
 
-template <class S, bool WIDE>
+template <class S, int KS, bool WIDE>
 void go_tiles(const LinearArgs& a, const LinearPlan& p, unsigned grid, hipStream_t st) {
   grid *= p.splits;
-  if (p.blocks == 1) linear_tile_kernel<S, 1, 1, WIDE><<<grid, 256, 0, st>>>(a, p);
-  else if (p.blocks == 2) linear_tile_kernel<S, 2, 1, WIDE><<<grid, 256, 0, st>>>(a, p);
-  else if (p.waves == 4) linear_tile_kernel<S, 4, 1, WIDE><<<grid, 256, 0, st>>>(a, p);
-  else linear_tile_kernel<S, 4, 2, WIDE><<<grid, 512, 0, st>>>(a, p);
+  if (p.blocks == 1) linear_tile_kernel<S, 1, KS, WIDE><<<grid, 256 * KS, 0, st>>>(a, p);
+  else if (p.blocks == 2) linear_tile_kernel<S, 2, KS, WIDE><<<grid, 256 * KS, 0, st>>>(a, p);
+  else linear_tile_kernel<S, 4, KS, WIDE><<<grid, 256 * KS, 0, st>>>(a, p);
+}
+template <class S, bool WIDE>
+void go_sets(const LinearArgs& a, const LinearPlan& p, unsigned grid, hipStream_t st) {
+  if (p.waves == 8) go_tiles<S, 2, WIDE>(a, p, grid, st);
+  else go_tiles<S, 1, WIDE>(a, p, grid, st);
 }
 
 template <class S>
 void go(const LinearArgs& a, const LinearPlan& p, hipStream_t st) {
   const unsigned grid = (unsigned)(p.col_tiles * p.row_tiles);
   if (p.tiles) {
-    if (a.lg_cpg >= 2) go_tiles<S, true>(a, p, grid, st);
-    else go_tiles<S, false>(a, p, grid, st);
+    if (a.lg_cpg >= 2) go_sets<S, true>(a, p, grid, st);
+    else go_sets<S, false>(a, p, grid, st);
     return;
   }
   const size_t lds = (size_t)p.waves * 2 * p.blocks * 1024;

@@ -92,8 +92,9 @@ LinearPlan plan(const LinearArgs& a) {
   // rows that an expert has if all have alike, and experts that have any
   const int64_t each = a.grouped ? parts(a.experts) : a.rows, busy = a.grouped ? std::min<int64_t>(a.rows, a.experts) : 1;
   // Few rows: 16 rows of 4096 x 11008 20 us, 32 in tiles; 32 rows of 11008 x 4096 27 and 28, of 28672 x
-  // 4096 51 and 32.  64 experts, 2816 x 2048: 32 rows 31 and 34, 64 rows 50 and 37.
-  const bool few = a.grouped ? a.rows < a.experts || (each <= 16 && busy * cols < 128)
+  // 4096 51 and 32.  64 experts, 2816 x 2048: 32 rows 31 and 34, 64 rows 50 and 37.  8 experts, 32 rows
+  // each, of 512 x 2048: 15 and 29.
+  const bool few = a.grouped ? a.rows < a.experts || (each <= 32 && busy * cols < 128)
                              : a.rows <= 16 || (a.rows <= 32 && cols <= 48);
   p.splits = 1;
   if (few) {
@@ -109,17 +110,25 @@ LinearPlan plan(const LinearArgs& a) {
     // 58, 64 and 96, 80 rows 138, 127 and 141, 256 rows 315, 268 and 276; 384 rows of 2048 x 1408 223
     // with 2 and 214 with 4.  One projection: 256 rows of 28672 x 4096 106, 89 and 84 us, 2048 rows of
     // 4096 x 11008 283, 229 and 206.
-    if (a.grouped) p.blocks = each <= 32 ? 1 : each <= 256 ? 2 : 4;
-    else p.blocks = parts(128) * cols >= 256 ? 4 : a.rows <= 64 ? 1 : 2;
-    const int64_t groups = parts(32 * p.blocks) * cols;
-    // one workgroup to a compute unit: two sets of waves
-    p.waves = p.blocks == 4 && groups <= 256 ? 8 : 4;
+    auto groups = [&]() { return a.grouped ? busy * ((each + 32 * p.blocks - 1) / (32 * p.blocks)) * cols : parts(32 * p.blocks) * cols; };
+    if (a.grouped) {
+      p.blocks = each <= 32 ? 1 : each <= 256 ? 2 : 4;
+      // smaller tiles where there is not one for each compute unit: 8 experts, 128 rows each, of 512 x
+      // 2048: 39 us with 2 blocks, 30 with 1
+      while (p.blocks > 1 && groups() < 256) p.blocks /= 2;
+    } else {
+      p.blocks = parts(128) * cols >= 256 ? 4 : a.rows <= 64 ? 1 : 2;
+    }
     // where tiles leave compute units idle, K in parts of at least four steps: 64 rows of 4096 x 11008
     // 92 us without, 33 with 8 parts of K; 512 rows 129 and 78
     if (!a.grouped && p.blocks < 4)
-      while (2 * p.splits * groups <= 512 && steps >= 8 * p.splits) p.splits *= 2;
+      while (2 * p.splits * groups() <= 512 && steps >= 8 * p.splits) p.splits *= 2;
     p.per = (steps + p.splits - 1) / p.splits;
     p.splits = (steps + p.per - 1) / p.per;
+    // two sets of waves where a workgroup has a compute unit to itself, for smaller tiles half of them: 8
+    // experts, 64 rows each, of 512 x 2048 (32 tiles) 29 us with one set and 24 with two, 16 rows of
+    // 8192 x 2048 (256) 32 and 32, 24 rows 40 and 47
+    p.waves = groups() * p.splits <= (p.blocks == 4 ? 256 : 128) ? 8 : 4;
   }
   // each expert may leave a part of a tile, and so may the rows that none has
   const int most = (p.tiles ? 32 : 16) * p.blocks;

@@ -201,6 +201,12 @@ EXPERTS = [   # T, k, of, count, lean, then as above without rows and pad
     (90, 1, 3, 1, 0, 300, 1056, 4, 32, "bf16", "bf16", "none", False, True, True),
     (900, 1, 3, 1, 0.9, 4200, 64, 4, 64, "bf16", "f32", "relu", False, False, False),
     (20, 2, 300, 280, 0, 40, 96, 7, 32, "f16", "bf16", "gelu", True, False, True),
+    (600, 4, 8, 8, 0.2, 2750, 96, 4, 32, "bf16", "bf16", "none", False, True, False),
+    (620, 4, 8, 8, 0.1, 3700, 128, 3, 128, "bf16", "f32", "silu", True, False, False),
+    (600, 4, 8, 8, 0.2, 3900, 64, 4, 64, "f16", "f16", "none", False, False, True),
+    (1000, 4, 40, 40, 0.1, 900, 64, 3, 64, "bf16", "f32", "gelu", False, False, True),
+    (1000, 4, 40, 38, 0.1, 1100, 160, 5, 32, "f16", "f16", "silu", True, True, False),
+    (800, 4, 40, 40, 0.1, 1500, 128, 4, 128, "f16", "f32", "none", False, False, False),
 ]
 
 
