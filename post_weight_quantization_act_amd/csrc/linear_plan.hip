@@ -50,7 +50,8 @@ bool scaled(const LinearArgs& a, awq_dtype_t dt, const LinearPlan& p) {
   return dt == AWQ_BF16 && p.tiles && p.blocks == 4 && a.rows * a.N >= 4096 * a.x_rows && a.x_rows * a.K < 1ll << 31;
 }
 
-// The parts' sums [splits][rows][N], added in their order, and the rest of the product.
+// The parts' sums [splits][rows][N], added in their order, and the rest of the product.  Bound by memory,
+// the caches' for the most part: 64 rows of 4096 columns in 8 parts are 8 MB.
 __global__ __launch_bounds__(256) void join_kernel(LinearArgs a, LinearPlan p, uint32_t runs) {
   const uint32_t at = blockIdx.x * 256 + threadIdx.x;
   const int64_t row = at / runs;
