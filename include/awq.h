@@ -611,7 +611,8 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
  *   [E] fp32 (NULL: none) is added, in 64 bits, for the choice alone.  NaN ranks
  *   last.  weights_out[t, j] fp32 = scale p_j, p the softmax over all E logits, or
  *   the sigmoid; with AWQ_ROUTE_NORMALISE over their sum over the k chosen.  Where
- *   that sum is 0 (a row of -inf) the weights are 0.  experts_out [T, k] int32.
+ *   that sum is 0 (a row of -inf; sigmoids are summed in 64 bits where a logit is below -80, and are 0 below
+ *   -745) the weights are 0.  experts_out [T, k] int32.
  *   Where offsets is not NULL the pairs are sorted as awq_moe_sort does.
  * awq_moe_route_grad: dlogits [T, E] dense of dtype from dweights [T, k] and the
  *   experts that the call chose; no gradient goes to the choice, or to the bias.

@@ -16,6 +16,11 @@ template <int N>
 __device__ __forceinline__ uint32_t turned(uint32_t x) {
   return __builtin_amdgcn_update_dpp(0, x, 0x120 + N, 0xf, 0xf, false);
 }
+template <int N>
+__device__ __forceinline__ double turned(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  return __longlong_as_double((long long)((uint64_t)turned<N>((uint32_t)(u >> 32)) << 32 | turned<N>((uint32_t)u)));
+}
 template <class F>
 __device__ __forceinline__ uint32_t row_all(uint32_t x, F f) {
   x = f(x, turned<8>(x));
@@ -41,6 +46,12 @@ __device__ __forceinline__ float row_sum(float x) {
   return __uint_as_float(row_all(__float_as_uint(x), [](uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
+}
+__device__ __forceinline__ double row_sum(double x) {
+  x += turned<8>(x);
+  x += turned<4>(x);
+  x += turned<2>(x);
+  return x + turned<1>(x);
 }
 __device__ __forceinline__ uint64_t row_umax(uint64_t x) {
   const uint32_t hi = row_umax((uint32_t)(x >> 32));
@@ -79,6 +90,31 @@ __device__ __forceinline__ void take_largest(Key (&key)[VPL], int l, int count, 
     f(j, top, (int)won);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] = won == (uint32_t)(l + 16 * i) ? (Key)0 : key[i];
+  }
+}
+
+// The sigmoids p of the chosen logits v (choice j in lane j % 16 of a row) and, normalise, over their sum.
+// In 32 bits one below 2^-126 loses bits and one below e^-88 is 0, and so is the sum where all are: a row
+// with a logit below -80 is taken in 64, which are whole down to -708 and 0 below -745.  16381 x 256 with a
+// bias as before, 22 us.
+__device__ __forceinline__ void sigmoids(const float (&v)[2], const bool (&there)[2], bool normalise, float by, float (&p)[2]) {
+  constexpr float kLow = -80.0f;
+  float f[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) f[s] = there[s] ? 1.0f / (1.0f + expf(-v[s])) : 0.0f;
+  const float sum = normalise ? row_sum(f[0] + f[1]) : 1.0f;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) p[s] = sum == 0.0f ? 0.0f : f[s] / sum * by;
+  const bool low = row_or((there[0] && v[0] < kLow) || (there[1] && v[1] < kLow)) != 0;
+  if (!__any(low)) return;
+  double d[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) d[s] = there[s] ? 1.0 / (1.0 + exp(-(double)v[s])) : 0.0;
+  const double total = normalise ? row_sum(d[0] + d[1]) : 1.0;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const float exact = total == 0.0 ? 0.0f : (float)(d[s] / total * by);
+    p[s] = low ? exact : p[s];
   }
 }
 
@@ -145,14 +181,13 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const S* row, in
     }
   }
   const bool there[2] = {l < a.k, 16 + l < a.k};
-  float v[2], p[2], sum;
+  float v[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) v[s] = there[s] ? to_f32(row[index[s]]) : -INFINITY;
   if (a.sigmoid) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) p[s] = there[s] ? 1.0f / (1.0f + expf(-v[s])) : 0.0f;
-    sum = a.normalise ? row_sum(p[0] + p[1]) : 1.0f;
+    sigmoids(v, there, a.normalise, a.scale, weight);
   } else {
+    float p[2], sum;
     // the weights of the chosen alone need their own largest; a row of -inf has no weight
     float top = fmaxf(v[0], v[1]);
     if (!a.normalise) {
@@ -170,9 +205,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const S* row, in
       for (int i = 0; i < VPL; ++i) sum += expf(x[i] - least);   // exp(-inf) past the last
     }
     sum = row_sum(sum);
-  }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) weight[s] = sum == 0.0f ? 0.0f : p[s] / sum * a.scale;
+    for (int s = 0; s < 2; ++s) weight[s] = sum == 0.0f ? 0.0f : p[s] / sum * a.scale;
+  }
 }
 
 __device__ __forceinline__ int bucket_of(const SortArgs& a, int expert) {
@@ -452,26 +487,29 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
     }
   }
   // choice j in lane j % 16: probability, gradient, and how it goes on to the logit
-  float p[2], g[2], sum = 0.0f, dot = 0.0f;
+  float p[2], g[2], v[2], dot = 0.0f;
   int index[2];
+  bool ok[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int j = 16 * s + l;
     index[s] = j < a.k ? a.experts[p0 + j] : -1;
-    const bool ok = (uint32_t)index[s] < (uint32_t)a.E;
-    index[s] = ok ? index[s] : -1;
-    const float v = ok ? to_f32(row[index[s]]) : -INFINITY;
-    p[s] = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top);
-    p[s] = ok ? p[s] : 0.0f;
-    g[s] = ok ? a.dweights[p0 + j] * a.scale : 0.0f;
-    sum += p[s];
+    ok[s] = (uint32_t)index[s] < (uint32_t)a.E;
+    index[s] = ok[s] ? index[s] : -1;
+    v[s] = ok[s] ? to_f32(row[index[s]]) : -INFINITY;
+    g[s] = ok[s] ? a.dweights[p0 + j] * a.scale : 0.0f;
   }
-  sum = a.normalise ? row_sum(sum) : a.sigmoid ? 1.0f : all;
+  if (a.sigmoid) {
+    sigmoids(v, ok, a.normalise, 1.0f, p);
+  } else {
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    p[s] = sum == 0.0f ? 0.0f : p[s] / sum;
-    dot += index[s] >= 0 ? g[s] * p[s] : 0.0f;
+    for (int s = 0; s < 2; ++s) p[s] = ok[s] ? expf(v[s] - top) : 0.0f;
+    const float sum = a.normalise ? row_sum(p[0] + p[1]) : all;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) p[s] = sum == 0.0f ? 0.0f : p[s] / sum;
   }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) dot += ok[s] ? g[s] * p[s] : 0.0f;
   dot = row_sum(dot);
   float d[2];
 #pragma unroll

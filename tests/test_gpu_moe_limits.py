@@ -1,0 +1,99 @@
+"""The router and its gradient at the ends of their ranges on the GPU, against the 64-bit oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_act_amd as awq
+from oracle import moe_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF_ULP = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+TINY = {"f32": 2.0 ** -149, "f16": 2.0 ** -24, "bf16": 2.0 ** -133}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    awq.library()
+    yield
+    torch.cuda.synchronize()
+
+
+def wide(t):
+    """Exact fp64 NumPy copy."""
+    return t.detach().double().cpu().numpy()
+
+
+def ints(t):
+    return t.cpu().numpy().astype(np.int64)
+
+
+# ---------------------------------------------------------------------------------------------
+# sigmoids of logits far below 0
+# ---------------------------------------------------------------------------------------------
+LEVELS = [0, -70, -79, -81, -87, -88.5, -90, -97, -103, -110, -200, -400, -690]
+
+
+def low_logits(rng, E, kind):
+    """Rows about each level, rows of which some are ordinary and the rest low, rows all but two masked."""
+    rows = [level + rng.normal(size=E) * 2 for level in LEVELS for _ in range(3)]
+    for level in LEVELS:
+        row = level + rng.normal(size=E)
+        row[rng.permutation(E)[:2]] += 45
+        rows.append(row)
+        row = np.full(E, -np.inf)
+        row[rng.permutation(E)[:2]] = level + rng.normal(size=2)
+        rows.append(row)
+    x = np.stack(rows)[rng.permutation(len(rows))].astype(np.float32)
+    return torch.from_numpy(x).to(TYPES[kind]).cuda()
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (40, 6), (70, 17)])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("normalise", [True, False])
+def test_low_sigmoids(E, k, kind, normalise):
+    rng = np.random.default_rng(E + k)
+    logits = low_logits(rng, E, kind)
+    x = wide(logits)
+    r = awq.awq_moe_route(logits, k, score="sigmoid", normalise=normalise, scale=1.5)
+    e = ref.choose(x, k, "sigmoid")
+    assert (ints(r.experts) == e).all()
+    w = ref.route_weights(x, e, "sigmoid", normalise, 1.5)
+    # an exponential (2 ulp), a sum, a quotient, their sum, a quotient and a product; below 2^-126 half a step
+    # of the subnormals
+    assert (np.abs(wide(r.weights) - w) <= (8 + E / 16) * 2.0 ** -24 * w + TINY["f32"]).all()
+    if normalise:
+        assert (np.abs(wide(r.weights).sum(1) - 1.5) < 1e-5).all()       # every row has some that are not -inf
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (40, 6), (70, 17)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("normalise", [True, False])
+def test_gradient_of_low_sigmoids(E, k, kind, normalise):
+    rng = np.random.default_rng(E * 3 + k)
+    logits = low_logits(rng, E, kind).requires_grad_()
+    g = torch.from_numpy(rng.normal(size=(logits.shape[0], k)).astype(np.float32)).cuda()
+    r = awq.awq_moe_route(logits, k, score="sigmoid", normalise=normalise, scale=0.7)
+    d, = torch.autograd.grad(r.weights, logits, g)
+    x, e, gn = wide(logits), ints(r.experts), wide(g)
+    want = ref.route_grad(x, e, gn, "sigmoid", normalise, 0.7)
+    # share (g - sum g share) (1 - p): each factor as the weights above, the sum k additions more
+    q = ref.route_weights(x, e, "sigmoid", normalise)
+    size = np.zeros_like(x)
+    np.put_along_axis(size, e, 0.7 * q * (np.abs(gn) + (q * np.abs(gn)).sum(1, keepdims=True)), 1)
+    bound = (3 * (8 + E / 16) + k + 8) * 2.0 ** -24 * size + 4 * TINY["f32"]
+    assert (np.abs(wide(d) - want) <= bound + HALF_ULP[kind] * np.abs(want) + TINY[kind]).all()
+
+
+def test_low_rows_do_not_change_their_neighbours():
+    rng = np.random.default_rng(2)
+    logits = torch.from_numpy(rng.normal(size=(64, 16)).astype(np.float32)).cuda()
+    alone = awq.awq_moe_route(logits, 4, score="sigmoid").weights
+    mixed = logits.clone()
+    mixed[1::2] -= 95
+    got = awq.awq_moe_route(mixed, 4, score="sigmoid").weights
+    assert torch.equal(got[::2], alone[::2]) and not torch.equal(got[1::2], alone[1::2])
