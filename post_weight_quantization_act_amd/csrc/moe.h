@@ -39,6 +39,7 @@ struct RouteGradArgs {
   int64_t T, stride;
   float scale;
   int E, k, sigmoid, normalise;
+  uint32_t first_block;
 };
 
 // Tokens [T][C] against sorted rows [T k][C].
@@ -56,7 +57,7 @@ struct RowsArgs {
 size_t moe_sort_ws_bytes(int64_t n, int count);
 hipError_t launch_moe_sort(SortArgs a, hipStream_t st);
 hipError_t launch_moe_route(RouteArgs a, awq_dtype_t dt, hipStream_t st);
-hipError_t launch_moe_route_grad(const RouteGradArgs& a, awq_dtype_t dt, hipStream_t st);
+hipError_t launch_moe_route_grad(RouteGradArgs a, awq_dtype_t dt, hipStream_t st);
 hipError_t launch_moe_gather(RowsArgs a, awq_dtype_t dt, hipStream_t st);
 // out [T][C] of out_dt = tokens (or 0) + sum of weighted rows
 hipError_t launch_moe_combine(RowsArgs a, awq_dtype_t dt, awq_dtype_t out_dt, hipStream_t st);

@@ -465,7 +465,7 @@ template <class T>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
   typedef typename T::storage S;
   const int l = threadIdx.x & 15;
-  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const int64_t t = (((int64_t)a.first_block + blockIdx.x) * 256 + threadIdx.x) >> 4;
   const bool in = t < a.T;
   const S* row = (const S*)a.logits + (in ? t : 0) * a.stride;
   const int64_t p0 = (in ? t : 0) * a.k;
@@ -796,10 +796,13 @@ hipError_t launch_moe_route(RouteArgs a, awq_dtype_t dt, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_moe_route_grad(const RouteGradArgs& a, awq_dtype_t dt, hipStream_t st) {
+hipError_t launch_moe_route_grad(RouteGradArgs a, awq_dtype_t dt, hipStream_t st) {
   ProfScope prof("awq_moe_route_grad", st);
   return by_type(dt, [&](auto t) {
-    route_grad_kernel<decltype(t)><<<(unsigned)((a.T + 15) / 16), 256, 0, st>>>(a);
+    in_parts((a.T + 15) / 16, 256, [&](uint32_t first, unsigned grid) {
+      a.first_block = first;
+      route_grad_kernel<decltype(t)><<<grid, 256, 0, st>>>(a);
+    });
   });
 }
 

@@ -97,3 +97,25 @@ def test_low_rows_do_not_change_their_neighbours():
     mixed[1::2] -= 95
     got = awq.awq_moe_route(mixed, 4, score="sigmoid").weights
     assert torch.equal(got[::2], alone[::2]) and not torch.equal(got[1::2], alone[1::2])
+
+
+# ---------------------------------------------------------------------------------------------
+# more tokens than one launch has threads for
+# ---------------------------------------------------------------------------------------------
+def test_gradient_of_more_than_two_to_the_28_tokens():
+    """Sixteen threads a token: 2^32 and more. The last token, those around the first launch's end, and all."""
+    T = 2 ** 28 + 2 ** 20 + 7
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.empty((T, 2), dtype=torch.float16, device="cuda").normal_(generator=gen).requires_grad_()
+    g = torch.empty((T, 1), device="cuda").normal_(generator=gen)
+    r = awq.awq_moe_route(logits, 1, score="sigmoid", normalise=False)
+    d, = torch.autograd.grad(r.weights, logits, g)
+    for lo in range(0, T, 2 ** 24):
+        part = slice(lo, lo + 2 ** 24)
+        x, e = logits.detach()[part].double(), r.experts[part].long()
+        assert torch.equal(e, (x[:, 1:] > x[:, :1]).long())
+        p = torch.sigmoid(x)
+        want = torch.zeros_like(x).scatter_(1, e, g[part].double()) * p * (1 - p)
+        # five roundings in fp32 and the exponentials' two ulp, one to fp16
+        bound = (16 * 2.0 ** -24 + HALF_ULP["f16"]) * want.abs() + TINY["f16"]
+        assert bool(((d[part].double() - want).abs() <= bound).all()), lo
