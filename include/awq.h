@@ -684,7 +684,7 @@ awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t 
  *   a row within a factor of 2^100 of each other, and sums of x (c - z) within fp32's
  *   range.  bf16 rows of large calls (more than 256 rows an expert, or some 256 tiles of 128 rows by
  *   256 columns) are taken to fp16 first, scaled by a power of two for each row: an
- *   element keeps all its bits down to 2^-16 of its row's largest, and is within 2^-25 of that largest
+ *   element keeps all its bits down to 2^-32 of its row's largest, and is within 2^-40 of that largest
  *   below.  The result is rounded once.
  *   workspace: awq_lowbit_linear_workspace_size(...) bytes, 256-byte aligned, may be NULL
  *   when that is 0.

@@ -7,6 +7,9 @@
 
 namespace awq {
 
+// Rows that are taken from bf16 to fp16 have their largest element at 2^kRowScale and up to twice that.
+constexpr int kRowScale = 15;
+
 // ---- epilogue ------------------------------------------------------------------------------
 // exp, quotients and tanh from the hardware's exp2 and reciprocal (an ulp each): relative error
 // a few 2^-24 and that of the exponent's own rounding, |v| 2^-24.  tanh's form is v / (1 + exp(-2 u)).

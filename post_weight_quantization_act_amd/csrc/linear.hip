@@ -572,7 +572,7 @@ __global__ __launch_bounds__(256 * KS, KS == 2 ? 1 : tile_groups(MT, WIDE)) void
     else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
 #pragma unroll
-  for (int w = 0; w < 2; ++w) unit[w] *= kF16 ? kHalfScale : 1.0f;
+  for (int w = 0; w < 2; ++w) unit[w] *= !kF16 ? 1.0f : a.x_scale ? kHalfScale / (1 << kRowScale) : kHalfScale;
 #pragma unroll 1
   for (int i = 0; i < 2 * MT && 16 * i < t.rows; ++i) {
 #pragma unroll

@@ -6,9 +6,10 @@
 namespace awq {
 namespace {
 
-// bf16 rows as fp16 ones: scaled by the power of two that takes their largest finite element below 2,
-// they keep all bits down to 2^-16 of it, and further down an error of at most 2^-25 of it.  A
-// wave a row.
+// bf16 rows as fp16 ones: scaled by the power of two that takes their largest finite element to
+// [2^15, 2^16), the last one that fp16 has, they keep all bits down to 2^-32 of it, and further down an error
+// of at most 2^-40 of it: 2^-16 of the rounding of a sum that has it.  A wave a row; scale is the
+// factor that is left beside kRowScale's.
 __global__ __launch_bounds__(256) void scale_rows_kernel(const __bf16* x, int64_t rows, int64_t K, int64_t stride,
                                                          _Float16* out, float* scale) {
   const int lane = threadIdx.x & 63;
@@ -35,7 +36,7 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const __bf16* x, int64_
     const bf16x8 v = *(const bf16x8*)(p + k);
     half8 y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = (_Float16)ldexpf((float)v[i], -e);
+    for (int i = 0; i < 8; ++i) y[i] = (_Float16)ldexpf((float)v[i], kRowScale - e);
     *(half8*)(out + row * K + k) = y;
   }
   if (lane == 0) scale[row] = ldexpf(1.0f, e);
