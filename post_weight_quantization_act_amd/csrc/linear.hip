@@ -366,42 +366,6 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
   }
 }
 
-// ---- sums that left fp32 ------------------------------------------------------------------------
-// linear_tile_kernel's sums are in units of a group's step, so one that meets a step 2^32 below an earlier
-// one may leave fp32 where the result does not.  Such a sum is taken again from memory, one group after another
-// as linear_few_kernel does, by the lane that found it.  Nothing of this is on the way of sums that are finite.
-
-// Whether a weight row's steps of groups lo .. hi - 1 lie more than 2^32 apart.
-__device__ __forceinline__ bool steps_far(const LinearArgs& a, int64_t row, int64_t lo, int64_t hi) {
-  float least = INFINITY, most = 0.0f;
-#pragma unroll 4
-  for (int64_t g = lo; g < hi; ++g) {
-    const float u = fabsf(a.meta[g * a.R + row].x);
-    least = u != 0.0f && u < least ? u : least;
-    most = u > most ? u : most;
-  }
-  return most > 0x1p32f * least;
-}
-// sum of x (c - z) step over chunks lo .. hi - 1 of a weight row.
-template <class S>
-__device__ __forceinline__ float sum_again(const LinearArgs& a, const S* x, int64_t row, int64_t lo, int64_t hi) {
-  float all = 0.0f;
-#pragma unroll 1
-  for (int64_t j = lo; j < hi; ++j) {
-    const uint32_t* p = a.codes + (j * a.R + row) * BITS;
-    const float2 m = a.meta[(j >> a.lg_cpg) * a.R + row];
-    float part = 0.0f;
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-      const int b = i * BITS, w = b >> 5, o = b & 31;
-      const uint64_t two = p[w] | (uint64_t)(o + BITS > 32 ? p[w + 1] : 0u) << 32;
-      part = fmaf((float)x[32 * j + i], (float)((uint32_t)(two >> o) & ((1u << BITS) - 1u)) - m.y, part);
-    }
-    all = fmaf(part, m.x, all);
-  }
-  return all;
-}
-
 // ---- many rows -----------------------------------------------------------------------------------
 // A workgroup takes 32 MT output rows and 256 weight rows, a wave all the output rows and 64 weight
 // rows (gated: 32 gates and the same ups).  Activations go through LDS, 128 columns at a time, two
@@ -602,33 +566,6 @@ __global__ __launch_bounds__(256 * KS, KS == 2 ? 1 : tile_groups(MT, WIDE)) void
   // a time go through LDS, from where a lane takes four columns of a row: 16 lanes a row (gated: 8).
   float* turn = (float*)xs + wave * 16 * kPitch;
   const int span = a.gated ? 8 : 16, col = 4 * (lane % span);
-  const float row_scale = a.x_scale ? 1.0f / (1 << kRowScale) : 1.0f;
-  int far = -1;                      // whether one of the lane's columns has steps far apart; -1: not known yet
-  auto mend = [&](f32x4& v, int half, int64_t row) __attribute__((always_inline)) {
-    bool good = true;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) good &= fabsf(v[c]) < INFINITY;
-    if (good || far == 0) return;
-    const int64_t lo = 4 * (int64_t)step0, hi = 4 * (int64_t)steps < chunks ? 4 * (int64_t)steps : chunks;
-    const int64_t w = (int64_t)t.expert * a.N + n0 + col;
-    const int left = outputs - n0 - col < 4 ? outputs - n0 - col : 4;
-    if (far < 0) {
-      far = 0;
-#pragma unroll 1
-      for (int c = 0; c < left; ++c)
-        far |= steps_far(a, w + c, lo >> a.lg_cpg, ((hi - 1) >> a.lg_cpg) + 1) ||
-               (a.gated && steps_far(a, w + outputs + c, lo >> a.lg_cpg, ((hi - 1) >> a.lg_cpg) + 1));
-      if (far == 0) return;
-    }
-#pragma unroll 1
-    for (int c = 0; c < left; ++c) {
-      const float was = c == 0 ? v[0] : c == 1 ? v[1] : c == 2 ? v[2] : v[3];
-      if (fabsf(was) < INFINITY) continue;
-      const float again = row_scale * sum_again(a, (const S*)a.x + source(a, row) * a.stride, w + half + c, lo, hi);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = k == c ? again : v[k];
-    }
-  };
   // a wave's LDS operations are in order; two sets wait for each other
   auto meet = [&]() __attribute__((always_inline)) {
     if (KS == 2) __syncthreads();
@@ -659,8 +596,6 @@ __global__ __launch_bounds__(256 * KS, KS == 2 ? 1 : tile_groups(MT, WIDE)) void
         up += *(const f32x4*)&turn[4 * 16 * kPitch + m * kPitch + 32 + col % 32];
       }
       const int64_t row = t.row0 + 16 * i + m;
-      mend(v, 0, row);
-      if (a.gated) mend(up, outputs, row);
       if (a.x_scale) {
         const float by = a.x_scale[source(a, row)];
         v *= by;
