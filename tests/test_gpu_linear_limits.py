@@ -84,3 +84,60 @@ def test_rows_at_the_ends_of_bfloat16():
     want = xn @ ref.weights_of(codes, steps, zeros, group).T
     # one product of 8 and 4 bits and a power of two: exact but for fp32's subnormals
     assert (np.abs(y - want) <= np.where(np.abs(want) < 2.0 ** -126, 2.0 ** -149, 0)).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# steps far apart
+# ---------------------------------------------------------------------------------------------
+FAR = [   # rows, n, K, bits, group, kind, gated, experts
+    (8, 60, 512, 4, 32, "bf16", False, 0), (20, 1300, 256, 4, 128, "bf16", False, 0), (40, 300, 4096, 4, 128, "bf16", False, 0),
+    (33, 258, 2080, 3, 32, "f16", True, 0), (150, 130, 640, 5, 64, "bf16", True, 0), (500, 70, 1152, 8, 128, "f16", False, 0),
+    (1000, 8100, 160, 4, 32, "bf16", False, 0), (1030, 7300, 256, 4, 128, "f16", False, 0), (2500, 800, 128, 2, 32, "bf16", False, 0),
+    (130, 130, 384, 4, 128, "bf16", False, 4), (700, 300, 160, 7, 32, "f16", True, 6), (61, 96, 288, 6, 32, "bf16", True, 8),
+]
+
+
+@pytest.mark.parametrize("case", FAR, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("spread,size", [(0, 70), (15, 60), (30, 20), (40, 0), (50, -10)])
+def test_steps_far_apart(case, spread, size):
+    """Steps up to 2^(2 spread) apart, rows of about 2^size (fp16: 1), up to the limit that the header states: the
+    largest step over the smallest, times the sums of |x (c - z)|, within fp32.  One row is not finite and
+    stays alone."""
+    rows, n, K, bits, group, kind, gated, experts = case
+    rng = np.random.default_rng(rows + spread)
+    if kind == "f16":
+        size = 0
+    codes = rng.integers(0, 2 ** bits, size=(max(1, experts) * n, K)).astype(np.uint8)
+    zeros = rng.integers(0, 2 ** bits, size=(len(codes), K // group))
+    # gated results are squares: about 1
+    steps = np.exp2(rng.uniform(-spread, spread, size=zeros.shape) - (size + spread if gated else size / 2)).astype(np.float32)
+    steps[rng.random(steps.shape) < 0.05] = 0
+    ct, mt = packed(codes, steps, zeros, bits)
+    W = ref.weights_of(codes, steps, zeros, group).reshape(max(1, experts), n, K)
+    x = torch.from_numpy((rng.normal(size=(rows, K)) * 2.0 ** size).astype(np.float32)).to(TYPES[kind]).cuda()
+    bad = min(3, rows - 1)
+    x[bad, K // 2] = float("nan")
+    more, own = {}, np.zeros(rows, dtype=np.int64)
+    if experts:
+        r = awq.awq_moe_sort(torch.from_numpy(rng.integers(0, experts, size=(rows, 1)).astype(np.int32)).cuda(), experts)
+        more, order = dict(routing=r, gather=True), r.order.cpu().numpy()
+        own = np.searchsorted(r.offsets.cpu().numpy(), np.arange(rows), side="right") - 1
+    else:
+        order = np.arange(rows)
+    y = wide(awq.awq_lowbit_linear(x, ct, mt, bits, group, gated=gated, out_dtype=torch.float32, **more))
+    xn = np.nan_to_num(wide(x))[order]
+    v, dv = np.empty((rows, n)), np.empty((rows, n))
+    for e in range(max(1, experts)):
+        v[own == e], dv[own == e] = xn[own == e] @ W[e].T, summed(xn[own == e], W[e], group)
+    if gated:
+        g, u, dg, du = v[:, :n // 2], v[:, n // 2:], dv[:, :n // 2], dv[:, n // 2:]
+        want, off = g * u, np.abs(g) * du + np.abs(u) * dg + dg * du
+    else:
+        want, off = v, dv
+    off = off + 2.0 ** -23 * (np.abs(want) + off) + 2.0 ** -149
+    assert np.abs(want).max() < 2.0 ** 126
+    ratio = max((row[row > 0].max() / row[row > 0].min() for row in steps.astype(np.float64) if row.any()), default=1)
+    assert ratio * K * 2 ** bits * np.abs(xn).max() < 2.0 ** 127
+    keep = order != bad
+    assert not np.isfinite(y[~keep]).any() and np.isfinite(y[keep]).all()
+    assert (np.abs(y - want)[keep] <= off[keep]).all()
