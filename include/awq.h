@@ -688,7 +688,8 @@ awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t 
  *   element keeps all its bits down to 2^-32 of its row's largest, and is within 2^-40 of that largest
  *   below.  The result is rounded once.
  *   workspace: awq_lowbit_linear_workspace_size(...) bytes, 256-byte aligned, may be NULL
- *   when that is 0.
+ *   when that is 0, cover this call and every one on the same weight with no more rows and x_rows;
+ *   awq_lowbit_linear_workspace_needed says what the call with these alone needs.
  * ------------------------------------------------------------------------ */
 #define AWQ_ACT_NONE 0
 #define AWQ_ACT_RELU 1
@@ -698,6 +699,8 @@ awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t 
 #define AWQ_LINEAR_GATED 1u
 size_t awq_lowbit_linear_workspace_size(awq_dtype_t dtype, int64_t rows, int64_t x_rows, int64_t N,
                                         int64_t K, int64_t experts, uint32_t flags);
+size_t awq_lowbit_linear_workspace_needed(awq_dtype_t dtype, int64_t rows, int64_t x_rows, int64_t N,
+                                          int64_t K, int64_t experts, uint32_t flags);
 awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows, int64_t K,
                                int64_t stride, const uint32_t* codes_t, const void* meta_t,
                                int64_t N, int64_t experts, int bits, int group, const float* bias,

@@ -33,6 +33,7 @@ __all__ = [
     "awq_kv_attention_workspace_size", "awq_kv_attention_workspace_needed", "awq_kv_attention",
     "Routing", "awq_moe_route", "awq_moe_sort", "awq_moe_sort_workspace_size", "awq_moe_gather",
     "awq_moe_combine", "awq_moe_combine_grad", "awq_moe_route_grad", "awq_lowbit_linear", "awq_lowbit_linear_workspace_size",
+    "awq_lowbit_linear_workspace_needed",
     "awq_profile_enable", "awq_profile_select", "awq_profile_read", "awq_profile_reset",
     "packed_words_per_row",
 ]
@@ -166,6 +167,7 @@ _SIGS = {
     "awq_moe_combine_grad": ([_P, _I32, _I64, _I64, _I64, _I32, _I64, _P, _P, _P, _P, _I32, _P, _P,
                               _P], _I32),
     "awq_lowbit_linear_workspace_size": ([_I32, _I64, _I64, _I64, _I64, _I64, _U32], _SZ),
+    "awq_lowbit_linear_workspace_needed": ([_I32, _I64, _I64, _I64, _I64, _I64, _U32], _SZ),
     "awq_lowbit_linear": ([_P, _I32, _I64, _I64, _I64, _P, _P, _I64, _I64, _I32, _I32, _P, _I32, _U32,
                            _P, _P, _I32, _I64, _P, _I64, _P, _I32, _P, _SZ, _P], _I32),
     "awq_profile_enable": ([_I32], _I32),
@@ -1100,8 +1102,16 @@ class _CombineGrad(torch.autograd.Function):
 
 def awq_lowbit_linear_workspace_size(dtype: torch.dtype, rows: int, x_rows: int, N: int, K: int,
                                      experts: int = 1, gated: bool = False) -> int:
+    """Bytes for a call with these sizes and every one on the same weight with no more rows and x_rows."""
     return int(library().awq_lowbit_linear_workspace_size(_DTYPES[dtype], rows, x_rows, N, K, experts,
                                                           AWQ_LINEAR_GATED if gated else 0))
+
+
+def awq_lowbit_linear_workspace_needed(dtype: torch.dtype, rows: int, x_rows: int, N: int, K: int,
+                                       experts: int = 1, gated: bool = False) -> int:
+    """Bytes for a call with these sizes alone."""
+    return int(library().awq_lowbit_linear_workspace_needed(_DTYPES[dtype], rows, x_rows, N, K, experts,
+                                                            AWQ_LINEAR_GATED if gated else 0))
 
 
 def awq_lowbit_linear(x: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tensor, bits: int, group: int,
@@ -1169,7 +1179,7 @@ def awq_lowbit_linear(x: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tens
         ws = _dense(workspace, "workspace", gpu, workspace.shape, workspace.dtype)
         size = workspace.nbytes
     else:
-        ws, size = None, (_LIB or library()).awq_lowbit_linear_workspace_size(_dtype(x), rows, M, N, K, experts, flags)
+        ws, size = None, (_LIB or library()).awq_lowbit_linear_workspace_needed(_dtype(x), rows, M, N, K, experts, flags)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
             ws = workspace.data_ptr()

@@ -296,6 +296,29 @@ awq_status_t moe_rows(awq_dtype_t dtype, int64_t T, int64_t C, int64_t stride, i
   return AWQ_OK;
 }
 
+// A size of the packed product's workspace; 0 for what the call refuses.
+template <class F>
+size_t linear_workspace(F bytes, awq_dtype_t dtype, int64_t rows, int64_t x_rows, int64_t N, int64_t K,
+                        int64_t experts, uint32_t flags) {
+  if (!valid_dtype(dtype) || rows < 1 || x_rows < 1 || N < 1 || K < 32 || experts < 1 ||
+      rows > INT32_MAX || x_rows > INT32_MAX || N > INT32_MAX || experts > awq::kMostExperts)
+    return 0;
+  awq::LinearArgs a = {};
+  a.rows = rows;
+  a.x_rows = x_rows;
+  a.N = (int)N;
+  a.K = K;
+  a.experts = (int)experts;
+  a.gated = (flags & AWQ_LINEAR_GATED) != 0;
+  a.grouped = true;
+  size_t need = bytes(a, dtype);
+  if (experts == 1) {            // with offsets or without
+    a.grouped = false;
+    need = std::max(need, bytes(a, dtype));
+  }
+  return align_up(need);
+}
+
 // A size of the cache attention's workspace; 0 for what the call refuses.
 template <class F>
 size_t kv_workspace(F bytes, int64_t T, int64_t B, int64_t Hq, int64_t kv_heads, int64_t D,
@@ -1311,23 +1334,12 @@ awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t 
 
 size_t awq_lowbit_linear_workspace_size(awq_dtype_t dtype, int64_t rows, int64_t x_rows, int64_t N,
                                         int64_t K, int64_t experts, uint32_t flags) {
-  if (!valid_dtype(dtype) || rows < 1 || x_rows < 1 || N < 1 || K < 32 || experts < 1 ||
-      rows > INT32_MAX || x_rows > INT32_MAX || N > INT32_MAX || experts > awq::kMostExperts)
-    return 0;
-  awq::LinearArgs a = {};
-  a.rows = rows;
-  a.x_rows = x_rows;
-  a.N = (int)N;
-  a.K = K;
-  a.experts = (int)experts;
-  a.gated = (flags & AWQ_LINEAR_GATED) != 0;
-  a.grouped = true;
-  size_t need = awq::linear_ws_bytes(a, dtype);
-  if (experts == 1) {            // with offsets or without
-    a.grouped = false;
-    need = std::max(need, awq::linear_ws_bytes(a, dtype));
-  }
-  return align_up(need);
+  return linear_workspace(awq::linear_ws_bound, dtype, rows, x_rows, N, K, experts, flags);
+}
+
+size_t awq_lowbit_linear_workspace_needed(awq_dtype_t dtype, int64_t rows, int64_t x_rows, int64_t N,
+                                          int64_t K, int64_t experts, uint32_t flags) {
+  return linear_workspace(awq::linear_ws_bytes, dtype, rows, x_rows, N, K, experts, flags);
 }
 
 awq_status_t awq_lowbit_linear(const void* x, awq_dtype_t dtype, int64_t x_rows, int64_t K,

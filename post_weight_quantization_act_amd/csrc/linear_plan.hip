@@ -145,6 +145,25 @@ size_t linear_ws_bytes(const LinearArgs& a, awq_dtype_t dt) {
   return scaled(a, dt, p) ? (size_t)a.x_rows * (a.K * 2 + 4) : p.splits > 1 ? (size_t)p.splits * a.rows * a.N * 4 : 0;
 }
 
+// Parts of K: their number changes where the row tiles do, at multiples of 32 rows, and between two of those
+// what they need grows with the rows; from 256 tiles on, so at 16384 rows at the latest, there are none. Scaled
+// rows: tiles of 128 rows once there stay with more rows, so the largest call that has them has all of a.rows.
+size_t linear_ws_bound(LinearArgs a, awq_dtype_t dt) {
+  const LinearPlan p = plan(a);
+  size_t most = linear_ws_bytes(a, dt);
+  if (dt == AWQ_BF16 && p.tiles && p.blocks == 4) {
+    const int64_t x_rows = std::min({a.x_rows, a.rows * a.N / 4096, (int64_t)INT32_MAX / a.K});
+    most = std::max(most, (size_t)x_rows * (a.K * 2 + 4));
+  }
+  if (a.grouped) return most;
+  const int64_t rows = a.rows;
+  for (a.rows = 32; a.rows < rows && a.rows <= 16384; a.rows += 32) {
+    const LinearPlan q = plan(a);
+    if (q.splits > 1) most = std::max(most, (size_t)q.splits * a.rows * a.N * 4);
+  }
+  return most;
+}
+
 int64_t linear_threads(const LinearArgs& a) {
   const LinearPlan p = plan(a);
   return p.row_tiles * p.col_tiles * 64 * p.waves * p.splits;

@@ -80,7 +80,9 @@ struct LinearArgs {
   int N, experts, per_token, lg_cpg, act, gated, out_type;
   bool grouped;                  // offsets are given
 };
-size_t linear_ws_bytes(const LinearArgs& a, awq_dtype_t dt);   // from rows, x_rows, N, K, experts, gated, grouped
+// from rows, x_rows, N, K, experts, gated, grouped: of this call, and of it and every one with fewer rows
+size_t linear_ws_bytes(const LinearArgs& a, awq_dtype_t dt);
+size_t linear_ws_bound(LinearArgs a, awq_dtype_t dt);
 int64_t linear_threads(const LinearArgs& a);   // of the call's grid
 hipError_t launch_linear(LinearArgs a, awq_dtype_t dt, int bits, void* ws, hipStream_t st);
 

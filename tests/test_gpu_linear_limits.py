@@ -141,3 +141,21 @@ def test_steps_far_apart(case, spread, size):
     keep = order != bad
     assert not np.isfinite(y[~keep]).any() and np.isfinite(y[keep]).all()
     assert (np.abs(y - want)[keep] <= off[keep]).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# one workspace for all batches
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_the_largest_batchs_workspace_serves_smaller_ones(kind):
+    rng = np.random.default_rng(12)
+    n, K, bits, group, most = 4200, 2048, 4, 128, 2300
+    codes, zeros = rng.integers(0, 16, size=(n, K)).astype(np.uint8), rng.integers(0, 16, size=(n, K // group))
+    ct, mt = packed(codes, (0.01 * np.exp(0.2 * rng.normal(size=zeros.shape))).astype(np.float32), zeros, bits)
+    bytes_ = awq.awq_lowbit_linear_workspace_size(TYPES[kind], most, most, n, K)
+    space = torch.full((bytes_ + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    x = torch.from_numpy(rng.normal(size=(most, K)).astype(np.float32)).to(TYPES[kind]).cuda()
+    for rows in (most, 900, 512, 300, 256, 130, 64, 33, 17, 1):
+        y = awq.awq_lowbit_linear(x[:rows], ct, mt, bits, group, workspace=space[:bytes_])
+        assert torch.equal(y, awq.awq_lowbit_linear(x[:rows], ct, mt, bits, group)), rows
+    assert (space[bytes_:] == 0xA5).all()
