@@ -46,9 +46,10 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const __bf16* x, int64_
 // instructions then, 2 to 4% of a call, and the pass as many bytes again as x has.  From 4096
 // products for each element on (4095 tokens, 6 of 64 experts, 2816 x 2048, 4 bits: 353 us without,
 // 344 with; the same rows, sorted, 2048 x 1408: no gain).  They are dense then, and stay within a
-// buffer's 4 GiB where overlapping ones would not.
+// buffer's 4 GiB where overlapping ones would not; the pass's grid stays below 2^32 threads at 32 columns.
+constexpr int64_t kMostScaled = (1ll << 31) - 129;
 bool scaled(const LinearArgs& a, awq_dtype_t dt, const LinearPlan& p) {
-  return dt == AWQ_BF16 && p.tiles && p.blocks == 4 && a.rows * a.N >= 4096 * a.x_rows && a.x_rows * a.K < 1ll << 31;
+  return dt == AWQ_BF16 && p.tiles && p.blocks == 4 && a.rows * a.N >= 4096 * a.x_rows && a.x_rows * a.K <= kMostScaled;
 }
 
 // The parts' sums [splits][rows][N], added in their order, and the rest of the product.  Bound by memory,
@@ -152,7 +153,7 @@ size_t linear_ws_bound(LinearArgs a, awq_dtype_t dt) {
   const LinearPlan p = plan(a);
   size_t most = linear_ws_bytes(a, dt);
   if (dt == AWQ_BF16 && p.tiles && p.blocks == 4) {
-    const int64_t x_rows = std::min({a.x_rows, a.rows * a.N / 4096, (int64_t)INT32_MAX / a.K});
+    const int64_t x_rows = std::min({a.x_rows, a.rows * a.N / 4096, kMostScaled / a.K});
     most = std::max(most, (size_t)x_rows * (a.K * 2 + 4));
   }
   if (a.grouped) return most;

@@ -44,3 +44,10 @@ def test_linear_workspace_needed_of_what_is_refused():
     for over in (dict(dtype=7), dict(rows=0), dict(rows=-1), dict(x_rows=0), dict(N=0), dict(K=0), dict(experts=0),
                  dict(rows=1 << 31), dict(x_rows=1 << 31), dict(N=1 << 31), dict(experts=1025)):
         assert f(*{**good, **over}.values()) == 0
+
+
+def test_the_scaling_pass_stays_in_one_launch():
+    """A wave a row: rows of 32 columns are scaled up to where their waves would be 2^32 threads."""
+    assert needed(torch.bfloat16, 2 ** 26 - 5, 2 ** 26 - 5, 4096, 32) >= (2 ** 26 - 5) * 68
+    for rows in range(2 ** 26 - 4, 2 ** 26 + 4):
+        assert needed(torch.bfloat16, rows, rows, 4096, 32) == 0
