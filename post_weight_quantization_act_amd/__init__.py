@@ -1126,11 +1126,10 @@ def awq_lowbit_linear(x: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tens
     all its experts one after another, bias is [experts, N], and each expert multiplies its
     sorted rows: rows of x, or, gather, the tokens' that they come from.  activation "none", "relu",
     "silu", "gelu" or "gelu_tanh".  -> [rows, N or N/2] of out_dtype (None: x's).  Packed weights
-    take no gradient and the call records none: it refuses inputs that require one."""
+    take no gradient and the call records none: it refuses inputs that require one, steps among them."""
     xs = _rows_of(x, "x")
     gpu = x.get_device()
-    if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)
-                                    or (residual is not None and residual.requires_grad)):
+    if torch.is_grad_enabled() and any(isinstance(t, _Tensor) and t.requires_grad for t in (x, meta_t, bias, residual)):
         raise RuntimeError("awq_lowbit_linear records no gradient: call it under torch.no_grad()")
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {[a for a in _ACTIVATIONS if a]}")

@@ -159,3 +159,23 @@ def test_the_largest_batchs_workspace_serves_smaller_ones(kind):
         y = awq.awq_lowbit_linear(x[:rows], ct, mt, bits, group, workspace=space[:bytes_])
         assert torch.equal(y, awq.awq_lowbit_linear(x[:rows], ct, mt, bits, group)), rows
     assert (space[bytes_:] == 0xA5).all()
+
+
+def small_call():
+    rng = np.random.default_rng(3)
+    codes, zeros = rng.integers(0, 16, size=(24, 64)).astype(np.uint8), rng.integers(0, 16, size=(24, 2))
+    ct, mt = packed(codes, np.full((24, 2), 0.1, np.float32), zeros, 4)
+    x = torch.from_numpy(rng.normal(size=(5, 64)).astype(np.float32)).half().cuda()
+    return x, ct, mt, dict(bias=torch.zeros(1, 24, device="cuda"), residual=torch.zeros(5, 24, device="cuda").half())
+
+
+def test_any_input_that_requires_a_gradient_is_refused():
+    x, ct, mt, more = small_call()
+    awq.awq_lowbit_linear(x, ct, mt, 4, 32, **more)
+    for t in (x, mt, more["bias"], more["residual"]):
+        t.requires_grad_()
+        with pytest.raises(RuntimeError, match="no gradient"):
+            awq.awq_lowbit_linear(x, ct, mt, 4, 32, **more)
+        with torch.no_grad():
+            awq.awq_lowbit_linear(x, ct, mt, 4, 32, **more)
+        t.requires_grad_(False)
