@@ -179,3 +179,19 @@ def test_any_input_that_requires_a_gradient_is_refused():
         with torch.no_grad():
             awq.awq_lowbit_linear(x, ct, mt, 4, 32, **more)
         t.requires_grad_(False)
+
+
+def test_tangents_are_refused():
+    from torch.autograd import forward_ad
+
+    x, ct, mt, more = small_call()
+    with forward_ad.dual_level():
+        awq.awq_lowbit_linear(x, ct, mt, 4, 32, **more)
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            awq.awq_lowbit_linear(dual, ct, mt, 4, 32, **more)
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            awq.awq_lowbit_linear(x, ct, forward_ad.make_dual(mt, torch.ones_like(mt)), 4, 32, **more)
+        for name in more:
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                awq.awq_lowbit_linear(x, ct, mt, 4, 32, **{**more, name: forward_ad.make_dual(more[name], more[name] + 1)})

@@ -119,3 +119,27 @@ def test_gradient_of_more_than_two_to_the_28_tokens():
         # five roundings in fp32 and the exponentials' two ulp, one to fp16
         bound = (16 * 2.0 ** -24 + HALF_ULP["f16"]) * want.abs() + TINY["f16"]
         assert bool(((d[part].double() - want).abs() <= bound).all()), lo
+
+
+# ---------------------------------------------------------------------------------------------
+# derivatives that are not recorded, and what a backward pass has kept
+# ---------------------------------------------------------------------------------------------
+def test_tangents_are_refused():
+    from torch.autograd import forward_ad
+
+    logits, x, rows = (torch.randn(s, device="cuda") for s in ((5, 8), (5, 16), (10, 16)))
+    w, bias = torch.randn(5, 2, device="cuda"), torch.zeros(8, device="cuda")
+    with forward_ad.dual_level():
+        def d(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+
+        r = awq.awq_moe_route(logits, 2, bias=bias)
+        awq.awq_moe_combine(awq.awq_moe_gather(x, r, w), r, w, residual=x)
+        for call in (lambda: awq.awq_moe_route(d(logits), 2), lambda: awq.awq_moe_route(logits, 2, bias=d(bias)),
+                     lambda: awq.awq_moe_route_grad(logits, r.experts, d(w)), lambda: awq.awq_moe_gather(d(x), r),
+                     lambda: awq.awq_moe_gather(x, r, d(w)), lambda: awq.awq_moe_gather(d(x), r, out=torch.empty_like(rows)),
+                     lambda: awq.awq_moe_combine(d(rows), r), lambda: awq.awq_moe_combine(rows, r, d(w)),
+                     lambda: awq.awq_moe_combine(rows, r, residual=d(x)), lambda: awq.awq_moe_combine_grad(d(x), r, rows=rows),
+                     lambda: awq.awq_moe_combine_grad(x, r, rows=d(rows))):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call()
