@@ -1074,23 +1074,33 @@ def awq_moe_combine_grad(dy: torch.Tensor, routing: Routing, weights: torch.Tens
     return drows, dw
 
 
+def _kept(routing, *tensors):
+    """tensors and the lists that a backward pass reads, to be saved: lists that are written in between are
+    found out as other tensors are."""
+    return *tensors, routing.offsets, routing.place
+
+
+def _saved_routing(offsets, place):
+    T, k = place.shape
+    return Routing.__new__(Routing)._hold(None, None, offsets, None, place, place.get_device(), T, k, offsets.shape[0] - 1)
+
+
 class _GatherGrad(torch.autograd.Function):
     """Back from the sorted rows as awq_moe_combine does it."""
 
     @staticmethod
     def forward(ctx, x, weights, routing):
-        ctx.save_for_backward(x if weights is not None else None, weights)
-        ctx.routing = routing
+        ctx.save_for_backward(*_kept(routing, x if weights is not None else None, weights))
         return awq_moe_gather(x, routing, weights)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        x, weights = ctx.saved_tensors
-        g, dw = g.contiguous(), None
-        dx = awq_moe_combine(g, ctx.routing, weights) if ctx.needs_input_grad[0] else None
+        x, weights, *lists = ctx.saved_tensors
+        g, dw, routing = g.contiguous(), None, _saved_routing(*lists)
+        dx = awq_moe_combine(g, routing, weights) if ctx.needs_input_grad[0] else None
         if ctx.needs_input_grad[1]:
-            dw = awq_moe_combine_grad(x, ctx.routing, None, g, need_rows=False)[1]
+            dw = awq_moe_combine_grad(x, routing, None, g, need_rows=False)[1]
         return dx, dw, None
 
 
@@ -1099,19 +1109,19 @@ class _CombineGrad(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, rows, weights, residual, routing, out_dtype):
-        ctx.save_for_backward(rows if weights is not None else None, weights)
-        ctx.routing, ctx.dtype = routing, rows.dtype
+        ctx.save_for_backward(*_kept(routing, rows if weights is not None else None, weights))
+        ctx.dtype = rows.dtype
         return awq_moe_combine(rows, routing, weights, residual, out_dtype)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        rows, weights = ctx.saved_tensors
+        rows, weights, *lists = ctx.saved_tensors
         need = ctx.needs_input_grad
         drows = dw = None
         if need[0] or need[1]:
             dy = g if g.stride(1) == 1 or g.shape[1] == 1 else g.contiguous()
-            drows, dw = awq_moe_combine_grad(dy, ctx.routing, weights, rows, ctx.dtype, need[0], need[1])
+            drows, dw = awq_moe_combine_grad(dy, _saved_routing(*lists), weights, rows, ctx.dtype, need[0], need[1])
         return drows, dw, g if need[2] else None, None, None
 
 

@@ -143,3 +143,23 @@ def test_tangents_are_refused():
                      lambda: awq.awq_moe_combine_grad(x, r, rows=d(rows))):
             with pytest.raises(RuntimeError, match="forward-mode"):
                 call()
+
+
+@pytest.mark.parametrize("which", ["place", "offsets"])
+def test_lists_that_are_written_before_the_backward_pass_are_found_out(which):
+    x, rows = torch.randn(5, 16, device="cuda", requires_grad=True), torch.randn(10, 16, device="cuda", requires_grad=True)
+    logits = torch.randn(5, 8, device="cuda")
+    for call in (lambda r: awq.awq_moe_gather(x, r), lambda r: awq.awq_moe_combine(rows, r),
+                 lambda r: awq.awq_moe_gather(x, r, r.weights), lambda r: awq.awq_moe_combine(rows, r, r.weights)):
+        r = awq.awq_moe_route(logits, 2)
+        y = call(r)
+        want = torch.autograd.grad(y, [x, rows], torch.ones_like(y), retain_graph=True, allow_unused=True)
+        getattr(r, which).zero_()
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.sum().backward()
+        # another list in the routing's place changes nothing
+        r = awq.awq_moe_route(logits, 2)
+        y = call(r)
+        setattr(r, which, torch.zeros_like(getattr(r, which)))
+        got = torch.autograd.grad(y, [x, rows], torch.ones_like(y), allow_unused=True)
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
