@@ -163,3 +163,86 @@ def test_lists_that_are_written_before_the_backward_pass_are_found_out(which):
         setattr(r, which, torch.zeros_like(getattr(r, which)))
         got = torch.autograd.grad(y, [x, rows], torch.ones_like(y), allow_unused=True)
         assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------------------------------------
+# scores that 32 bits cannot tell apart
+# ---------------------------------------------------------------------------------------------
+def near_scores(rng, T, E, k, score, every):
+    """fp32 logits and biases: on every `every`-th token experts of one cluster, whose scores lie within some
+    2^-26 of each other in random order, stand around the k-th place; the rest are well apart."""
+    bias = rng.uniform(2.0 ** -4, 2.0 ** -3, size=E).astype(np.float32)
+    b = bias.astype(np.float64)
+    middle = 1.5 if score == "softmax" else 0.625
+    x = np.empty((T, E), np.float32)
+    close = np.arange(T) % every == 1 % every
+    for t in range(T):
+        order = rng.permutation(E)
+        # well apart: their scores 2^-12 and more from each other and from the cluster's
+        want = middle + (np.arange(E) - rng.integers(0, E)) * (0.2 / E) + 0.05 / E
+        s = np.empty(E)
+        s[order] = want
+        if close[t]:
+            few = min(E, rng.integers(2, 9))
+            first = min(max(0, E - k - rng.integers(0, few)), E - few)      # in rising order, around the k-th largest
+            s[order[first:first + few]] = middle + 0.2 * (first - E / 2) / E + rng.integers(-8, 9, size=few) * 2.0 ** -28
+            low = order[:first]
+            s[low] = np.minimum(s[low], middle + 0.2 * (first - E / 2) / E - 2.0 ** -14 * (1 + np.arange(first)[::-1]))
+            high = order[first + few:]
+            s[high] = np.maximum(s[high], middle + 0.2 * (first - E / 2) / E + 2.0 ** -14 * (1 + np.arange(len(high))))
+        v = s - b
+        x[t] = v if score == "softmax" else np.log(v / (1 - v))
+    return x, bias, close
+
+
+def fp32_scores(x, bias, score):
+    x = x.astype(np.float32)
+    return (x if score == "softmax" else np.float32(1) / (np.float32(1) + np.exp(-x))) + bias
+
+
+@pytest.mark.parametrize("T,E,k,every", [(3, 8, 3, 1), (300, 12, 12, 1), (400, 60, 4, 4), (90, 100, 8, 1), (700, 256, 8, 4),
+                                         (130, 300, 32, 2), (100, 1000, 6, 1), (2500, 40, 17, 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_near_scores_are_told_apart_in_64_bits(T, E, k, every, score):
+    rng = np.random.default_rng(E * 7 + k)
+    x, bias, close = near_scores(rng, T, E, k, score, every)
+    want = ref.choose(x, k, score, bias)
+    # in 32 bits others are chosen, or in another order, on the tokens that are close, and on no more
+    off = (ref.choose(fp32_scores(x, bias, score), k) != want).any(1)
+    assert off[close].mean() > 0.3 and not off[~close].any()
+    r = awq.awq_moe_route(torch.from_numpy(x).cuda(), k, score=score, bias=torch.from_numpy(bias).cuda())
+    assert (ints(r.experts) == want).all()
+    offsets, order, place = ref.sort_pairs(want, 0, E)
+    assert (ints(r.offsets) == offsets).all() and (ints(r.order) == order).all() and (ints(r.place) == place).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalise", [True, False])
+def test_gradient_of_a_choice_by_bias(kind, score, normalise):
+    """The bias moves the choice; weights and their gradient are those of the logits of what is chosen."""
+    rng = np.random.default_rng(17)
+    T, E, k = 70, 40, 5
+    logits = torch.from_numpy(rng.normal(size=(T, E)).astype(np.float32)).to(TYPES[kind]).cuda().requires_grad_()
+    bias = torch.from_numpy((rng.normal(size=E) * 2).astype(np.float32)).cuda()
+    g = torch.from_numpy(rng.normal(size=(T, k)).astype(np.float32)).cuda()
+    r = awq.awq_moe_route(logits, k, score=score, bias=bias, normalise=normalise, scale=0.7)
+    d, = torch.autograd.grad(r.weights, logits, g)
+    x, e, gn = wide(logits), ints(r.experts), wide(g)
+    assert (e == ref.choose(x, k, score, wide(bias))).all() and (np.sort(e) != np.sort(ref.choose(x, k, score))).any()
+    w = ref.route_weights(x, e, score, normalise, 0.7)
+    # differences of logits below 12, an exponential, a sum, a quotient, a product
+    steps = 2 * (4 + 12) + E / 16 + 8
+    assert (np.abs(wide(r.weights) - w) <= steps * 2.0 ** -24 * w).all()
+    want = ref.route_grad(x, e, gn, score, normalise, 0.7)
+    if score == "softmax" and not normalise:       # p g - p sum p g, over all experts
+        p = np.exp(x) / np.exp(x).sum(1, keepdims=True)
+        size = 0.7 * p * (np.take_along_axis(p, e, 1) * np.abs(gn)).sum(1, keepdims=True)
+    else:
+        q = w / 0.7
+        p, size = np.ones_like(x), np.zeros_like(x)
+        np.put_along_axis(size, e, 0.7 * q * (q * np.abs(gn)).sum(1, keepdims=True), 1)
+    here = np.zeros_like(x)
+    np.put_along_axis(here, e, 0.7 * np.abs(gn) * w / 0.7, 1)
+    bound = (3 * steps + k + 8) * 2.0 ** -24 * (size + here)
+    assert (np.abs(wide(d) - want) <= bound + HALF_ULP[kind] * np.abs(want) + TINY[kind]).all()
