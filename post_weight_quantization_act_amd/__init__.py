@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 from pathlib import Path
+from types import SimpleNamespace
 
 import torch
 from torch.autograd import forward_ad as _forward_ad
@@ -836,10 +837,12 @@ def awq_kv_attention(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, pages:
     return (out, lse) if return_lse else out
 
 
+# the level of forward-mode derivatives, below 0 outside of every one: looked at before the tensors are
+_AD = _forward_ad if hasattr(_forward_ad, "_current_level") else SimpleNamespace(_current_level=0)
+
+
 def _no_tangents(*tensors) -> None:
     """Refuses tensors with a forward-mode tangent, which the calls below would drop."""
-    if getattr(_forward_ad, "_current_level", 0) < 0:      # outside of every dual level
-        return
     for t in tensors:
         if isinstance(t, _Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
             raise RuntimeError("no forward-mode derivative is recorded: the tensors must have no tangents")
@@ -924,7 +927,8 @@ def awq_moe_route(logits: torch.Tensor, k: int, score: str = "softmax",
     score "softmax" or "sigmoid"; bias fp32 [E] is added to the scores for the choice alone;
     normalise: weights over their sum.  Where logits require a gradient that of the
     weights is recorded."""
-    _no_tangents(logits, bias)
+    if _AD._current_level >= 0:
+        _no_tangents(logits, bias)
     _rows_of(logits, "logits")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
@@ -948,7 +952,8 @@ def awq_moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, dweights: to
                        score: str = "softmax", normalise: bool = True, scale: float = 1.0) -> torch.Tensor:
     """The gradient of awq_moe_route's weights with respect to the logits, [T, E] of their type,
     from dweights fp32 [T, k] and the experts that it chose."""
-    _no_tangents(logits, dweights)
+    if _AD._current_level >= 0:
+        _no_tangents(logits, dweights)
     stride = _rows_of(logits, "logits")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
@@ -994,7 +999,8 @@ def awq_moe_gather(x: torch.Tensor, routing: Routing, weights: torch.Tensor | No
     """Tokens x [T, C] (any row stride) into the sorted rows [T k, C], times weights fp32 [T, k] if
     given; rows of pairs that no expert here has are zero.  The gradients of x and weights are recorded
     where they require one; into a given out they are not."""
-    _no_tangents(x, weights)
+    if _AD._current_level >= 0:
+        _no_tangents(x, weights)
     gpu = _is_routing(routing)
     xs = _rows_of(x, "x", gpu)
     if out is None and torch.is_grad_enabled() and (
@@ -1021,7 +1027,8 @@ def awq_moe_combine(rows: torch.Tensor, routing: Routing, weights: torch.Tensor 
     """Sorted rows [T k, C] back into tokens [T, C]: residual + the sum of each token's rows, times
     weights fp32 [T, k] if given.  residual [T, C] of out_dtype (None: rows').  The gradients
     of rows, weights and residual are recorded where they require one; into a given out they are not."""
-    _no_tangents(rows, weights, residual)
+    if _AD._current_level >= 0:
+        _no_tangents(rows, weights, residual)
     gpu = _is_routing(routing)
     if out is None and torch.is_grad_enabled() and (
             rows.requires_grad or (weights is not None and weights.requires_grad)
@@ -1054,7 +1061,8 @@ def awq_moe_combine_grad(dy: torch.Tensor, routing: Routing, weights: torch.Tens
                          need_rows: bool = True, need_weights: bool = True):
     """(drows, dweights) of awq_moe_combine for dy [T, C] (any row stride): drows [T k, C] of dtype
     (None: rows' or dy's), dweights fp32 [T, k] from rows; None for what is not needed."""
-    _no_tangents(dy, weights, rows)
+    if _AD._current_level >= 0:
+        _no_tangents(dy, weights, rows)
     gpu = _is_routing(routing)
     stride = _rows_of(dy, "dy", gpu)
     T, C = dy.shape
@@ -1152,10 +1160,13 @@ def awq_lowbit_linear(x: torch.Tensor, codes_t: torch.Tensor, meta_t: torch.Tens
     sorted rows: rows of x, or, gather, the tokens' that they come from.  activation "none", "relu",
     "silu", "gelu" or "gelu_tanh".  -> [rows, N or N/2] of out_dtype (None: x's).  Packed weights
     take no gradient and the call records none: it refuses inputs that require one, steps among them."""
-    _no_tangents(x, meta_t, bias, residual)
+    if _AD._current_level >= 0:
+        _no_tangents(x, meta_t, bias, residual)
     xs = _rows_of(x, "x")
     gpu = x.get_device()
-    if torch.is_grad_enabled() and any(isinstance(t, _Tensor) and t.requires_grad for t in (x, meta_t, bias, residual)):
+    if torch.is_grad_enabled() and (x.requires_grad or (isinstance(meta_t, _Tensor) and meta_t.requires_grad)
+                                    or (bias is not None and bias.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
         raise RuntimeError("awq_lowbit_linear records no gradient: call it under torch.no_grad()")
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {[a for a in _ACTIVATIONS if a]}")
