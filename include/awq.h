@@ -608,7 +608,8 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
  * awq_moe_route: from logits [T, E] of dtype (row stride in elements) the k experts
  *   with the largest scores, in falling order, the lower number first of equals.
  *   AWQ_SCORE_SOFTMAX: the score is the logit, AWQ_SCORE_SIGMOID: its sigmoid; bias
- *   [E] fp32 (NULL: none) is added, in 64 bits, for the choice alone.  NaN ranks
+ *   [E] fp32 (NULL: none) is added, in 64 bits, for the choice alone (to the logit, not to the
+ *   softmax's probability).  NaN ranks
  *   last.  weights_out[t, j] fp32 = scale p_j, p the softmax over all E logits, or
  *   the sigmoid; with AWQ_ROUTE_NORMALISE over their sum over the k chosen.  Where
  *   that sum is 0 (a row of -inf; sigmoids are summed in 64 bits where a logit is below -80, and are 0 below
@@ -631,7 +632,7 @@ awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const void* q, awq_dt
  *   and dweights [T, k] fp32 = <dy[t], rows[place[t, j]]>, rows of dtype (may be NULL;
  *   then rows may be).  With x for dy and the rows'
  *   gradient for rows dweights is awq_moe_gather's.
- * place and order outside [0, T k) are passed over; C < 2^31.
+ * place outside [0, T k) is passed over (an order outside has awq_lowbit_linear take x's first row); C < 2^31.
  * ------------------------------------------------------------------------ */
 #define AWQ_SCORE_SOFTMAX 0
 #define AWQ_SCORE_SIGMOID 1

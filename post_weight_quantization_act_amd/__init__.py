@@ -924,8 +924,8 @@ def awq_moe_route(logits: torch.Tensor, k: int, score: str = "softmax",
                   num_experts: int | None = None, first_expert: int = 0) -> Routing:
     """The k experts of every row of logits [T, E] with the largest scores, their weights, and the
     pairs sorted by expert, for experts [first_expert, first_expert + num_experts) (None: all).
-    score "softmax" or "sigmoid"; bias fp32 [E] is added to the scores for the choice alone;
-    normalise: weights over their sum.  Where logits require a gradient that of the
+    score "softmax" or "sigmoid"; bias fp32 [E] is added to the scores (softmax: to the logits) for the
+    choice alone; normalise: weights over their sum.  Where logits require a gradient that of the
     weights is recorded."""
     if _AD._current_level >= 0:
         _no_tangents(logits, bias)

@@ -12,7 +12,8 @@ constexpr int kRowScale = 15;
 
 // ---- epilogue ------------------------------------------------------------------------------
 // exp, quotients and tanh from the hardware's exp2 and reciprocal (an ulp each): relative error
-// a few 2^-24 and that of the exponent's own rounding, |v| 2^-24.  tanh's form is v / (1 + exp(-2 u)).
+// a few 2^-24 and that of the exponent's own rounding, |v| 2^-24, which v's rounding to fp32, |v| 2^-24 of it too,
+// makes of the result in any form.  tanh's form is v / (1 + exp(-2 u)).
 __device__ __forceinline__ float over_one_plus_exp(float v, float minus) {
   return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(minus * -1.44269504088896341f));
 }

@@ -235,7 +235,8 @@ __device__ __forceinline__ void load_words(Buffer b, uint32_t voff, uint32_t sof
 // 16 TT output rows; its waves share the columns of K, 128 at a time, and add up in LDS.  Lane
 // 16 g + r holds weight row r and the 32 codes of chunk g of the four: one load of `bits` words;
 // instruction i of four multiplies the chunks' codes 8 i .. 8 i + 7.  One row of 8192 to 28672
-// columns, 3 bits: 36 us, 2.8 TB/s; bound by unpacking.  8 rows for 8 of 128 experts, 1536 x 2048, 4
+// columns, 3 bits: 36 us, 2.8 TB/s; bound by unpacking (awq_lowbit_gemv, on the vector units alone, 33; four
+// rows 36 and 44; one row of 4096 x 4096, 4 bits, 11 and 13.5, of 11008 to 4096 15 and 14).  8 rows for 8 of 128 experts, 1536 x 2048, 4
 // bits: 11 us, of which the weights are 2.7; bound by its chain of loads (offsets, codes, the
 // rows' places, the rows).
 template <class S, int TT, int WT>
@@ -378,10 +379,10 @@ __global__ __launch_bounds__(512, 2) void linear_few_kernel(LinearArgs a, int co
 // group, cost every call 7 to 10%: 2047 x 4096 x 11008 185 -> 199 us.)
 // WIDE: groups of 128 columns and more, so a step lies in one.
 // splits > 1: a workgroup takes the steps of one part of K and leaves fp32 sums to a kernel that joins them.
-// 4 bits: 2047 x 4096 x 11008 in fp16 190 us, 0.97 PFLOP/s; 24570 rows for 64 experts, 2816 x 2048, 345
-// us, 0.82 PFLOP/s; a library's product of such a size reaches 1.17 to 1.23 here, and this loop by
+// 4 bits: 2047 x 4096 x 11008 in fp16 183 us, 1.01 PFLOP/s; 24570 rows for 64 experts, 2816 x 2048, 340
+// us, 0.83 PFLOP/s; a library's product of such a size reaches 1.17 to 1.23 here, and this loop by
 // itself 1.13.  The rest are rows that the last tile of an expert lacks, and the first loads and last
-// stores of a round of workgroups.  488 rows for 128 experts, 1536 x 2048: 56 us, 3.8 TB/s; each step
+// stores of a round of workgroups.  488 rows for 128 experts, 1536 x 2048: 55 us, 3.8 TB/s; each step
 // waits for its codes, and a ring of three steps in flight gained nothing.
 // Workgroups of a compute unit: as many as their registers allow without spills.
 constexpr int tile_groups(int mt, bool wide) {
@@ -402,7 +403,8 @@ __global__ __launch_bounds__(256 * KS, KS == 2 ? 1 : tile_groups(MT, WIDE)) void
   const int wide = a.gated ? 32 : 64;                            // outputs of a wave
   // Two workgroups share a compute unit.  Where more follow, the second of each pair starts 4 us
   // later, so that one multiplies while the other waits for its first rows or stores its last
-  // (24570 rows for 64 experts, 2816 x 2048, 4 bits: 362 us without, 337 with 4, 341 with 8)
+  // (24570 rows for 64 experts, 2816 x 2048, 4 bits: 362 us without, 337 with 4, 341 with 8; few steps of
+  // K: 4096 x 16384 x 128 in fp16 73 us without and 74 with, 256 columns 82 and 83, 512 103 and 103)
   if (MT == 4 && KS == 1 && gridDim.x > 512 && blockIdx.x >= 256 && blockIdx.x < 512)
     for (int i = 0; i < 4; ++i) __builtin_amdgcn_s_sleep(32);
   Tiles tiles(a, kRows);

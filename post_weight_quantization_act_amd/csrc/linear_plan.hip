@@ -109,7 +109,8 @@ LinearPlan plan(const LinearArgs& a) {
   } else {
     p.tiles = true;
     p.col_tiles = cols;
-    // 64 experts, 2816 x 2048, with 1, 2 and 4 blocks of 32 rows: 32 rows each 73, 70 and 103 us, 16 rows
+    // 64 experts, 2816 x 2048, as many rows for each, with 1, 2 and 4 blocks of 32 rows: 32 rows each 73, 70
+    // and 103 us (drawn alike, with 1 block 69, and 55 for 32 each), 16 rows
     // 58, 64 and 96, 80 rows 138, 127 and 141, 256 rows 315, 268 and 276; 384 rows of 2048 x 1408 223
     // with 2 and 214 with 4.  One projection: 256 rows of 28672 x 4096 106, 89 and 84 us, 2048 rows of
     // 4096 x 11008 283, 229 and 206.

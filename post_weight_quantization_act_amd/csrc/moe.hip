@@ -589,7 +589,7 @@ int64_t part_blocks(int64_t T, int64_t C) {
 
 // rows[place] = weight tokens[t], 0 where the expert is elsewhere. A token is read once for all of
 // its choices. Bound by memory, its writes above all: 8191 tokens of 2048 columns in bf16 to 8
-// places, 302 MB, 50 us, 6.0 TB/s.
+// places, 302 MB, 49 us, 6.1 TB/s (a call 51 where the same tensors come again, 58 with others).
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(256) void gather_kernel(RowsArgs a) {
   typedef typename T::storage S;
