@@ -683,8 +683,8 @@ awq_status_t awq_moe_combine_grad(const void* dy, awq_dtype_t dy_dtype, int64_t 
  *   Products x (c - z) are exact and summed in fp32, where K is long and rows are few in
  *   parts that are added in their order; steps must be finite.  Sums are
  *   held in units of a step: the largest step of a row over its smallest but 0, times the sum of
- *   |x (c - z)|, must be within fp32's range, whatever the number of rows (steps of a 2^30th, rows of up to
- *   2^60; fp16 rows: steps of a 2^80th).  bf16 rows of large calls (more than 256 rows an expert, or some 256 tiles of 128 rows by
+ *   |x (c - z)|, must be within fp32's range (as it is for rows of up to 2^60 with steps within 2^30 of each
+ *   other, and for fp16 rows with steps within 2^80).  bf16 rows of large calls (more than 256 rows an expert, or some 256 tiles of 128 rows by
  *   256 columns) are taken to fp16 first, scaled by a power of two for each row: an
  *   element keeps all its bits down to 2^-32 of its row's largest, and is within 2^-40 of that largest
  *   below.  The result is rounded once.
